@@ -21,7 +21,8 @@ SO = os.path.join(PKG, "libqt.so")
 ARCH = "gfx950"
 
 SOURCES = ["api.cpp", "quantize.hip", "gemv.hip", "grouped.hip", "gemm.hip", "hessian.hip",
-           "syrk.hip", "factor.hip", "gptq.hip", "moe.hip"]
+           "syrk.hip", "factor.hip", "gptq.hip", "moe.hip",
+           "api_tune.cpp", "ffn.hip", "qgrad.hip", "distill.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

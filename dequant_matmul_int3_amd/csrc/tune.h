@@ -1,0 +1,199 @@
+// Internal launch interface of the gated feed-forward block, the backward
+// passes and the distillation loss, with the host rules that size their
+// workspaces.  Arguments here are already validated.  Host-only code apart
+// from the launchers' declarations, so that the validation layer builds and
+// runs without a GPU compiler.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "qt_internal.h"
+
+namespace qt {
+
+constexpr int kCUs = 256;                  // compute units of an MI355X
+constexpr int64_t kTuneMaxDim = 1 << 20;   // D, F, O, I of these calls
+constexpr int64_t kTuneMaxTokens = 1 << 22;
+constexpr int kDistillMaxK = 1024;
+constexpr int64_t kDistillMaxV = 1LL << 31;  // row strides, too
+
+inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int64_t pad_to(int64_t a, int64_t b) { return cdiv(a, b) * b; }
+// Workspace sections start at multiples of 256 bytes.
+inline int64_t sect(int64_t bytes) { return pad_to(bytes, 256); }
+
+// A packed matrix and its bits (3 or 4).
+struct QMat {
+    const uint8_t* packed;
+    const float* scales;
+    int32_t bits;
+};
+
+// ------------------------------------------------------------ forward pass
+// Up to this many input rows (bf16 tokens, or three pieces per f32 token)
+// take the small kernel; more take the tile.
+constexpr int kSmallRows = 64;
+// Pieces per input value: an f32 input is split exactly into three bf16.
+inline int ffn_pieces(bool bf16) { return bf16 ? 1 : 3; }
+inline bool ffn_small(int64_t T, bool bf16) { return T * ffn_pieces(bf16) <= kSmallRows; }
+
+// Inputs are copied into padded bf16 planes when they are f32 or their rows
+// are not whole groups (the plane's padding is zero).
+inline bool x_planes_needed(int64_t D, bool bf16) { return !bf16 || D % kGroup != 0; }
+inline int64_t x_planes_bytes(int64_t T, int64_t D, bool bf16) {
+    return sect(T * ffn_pieces(bf16) * pad_to(D, kGroup) * 2);
+}
+
+constexpr int kTileN = 128;  // B columns of a block tile
+constexpr int kTileK = 64;   // inner elements of a step
+// 16-token tiles per wave of the 8-wave block tile: 1, 2 or 4
+inline int tile_mt(int64_t T, int most) {
+    int mt = 1;
+    while (mt < most && 128 * mt < T) mt *= 2;
+    return mt;
+}
+
+// Splits of the inner axis, so that the blocks fill the CUs: the count (at
+// most `most`) with the least work on the busiest CU, a split costing 1/16 of
+// the whole (its partial sums are written, read and joined).
+inline int inner_splits(int64_t blocks, int64_t steps, int most) {
+    int best = 1;
+    double cost = 1e30;
+    for (int s = 1; s <= most && (s == 1 || steps / s >= 4); ++s) {
+        const double c = (double)cdiv(blocks * s, kCUs) / s + (s > 1 ? 0.0625 * s : 0.0);
+        if (c < cost - 1e-9) {
+            cost = c;
+            best = s;
+        }
+    }
+    return best;
+}
+
+struct FfnPlan {
+    bool small;
+    bool planes;       // X is copied into padded planes first
+    int mt;            // tile form: 16-token tiles per wave
+    int splits;        // tile form: splits of the groups
+    int64_t planes_off, part_off, bytes;
+};
+inline FfnPlan ffn_plan(int64_t T, int64_t D, int64_t F, bool bf16) {
+    FfnPlan p{};
+    p.small = ffn_small(T, bf16);
+    p.planes = x_planes_needed(D, bf16);
+    p.splits = 1;
+    if (!p.small) {
+        p.mt = tile_mt(T, bf16 ? 4 : 2);
+        p.splits = inner_splits(cdiv(T, 128 * p.mt) * cdiv(F, kTileN / 2), cdiv(D, kGroup), 8);
+    }
+    p.planes_off = 0;
+    p.part_off = p.planes ? x_planes_bytes(T, D, bf16) : 0;
+    p.bytes = p.part_off + (p.splits > 1 ? sect(p.splits * 2 * T * F * 4) : 0);
+    return p;
+}
+
+struct FfnArgs {
+    QMat gate, up;
+    int64_t F, D;
+    int act;
+    const void* X;
+    bool bf16;
+    int64_t T;
+    void* H;
+    float* pre;  // [2][T][F] or null
+};
+hipError_t launch_ffn_gated(const FfnArgs& a, void* workspace, hipStream_t s);
+// X [T x D] -> padded bf16 planes (ffn.hip); also the scales' gradient's input.
+hipError_t launch_x_planes(const void* X, bool bf16, int64_t T, int64_t D, uint16_t* planes,
+                           hipStream_t s);
+
+// ----------------------------------------------------------- backward pass
+// dX = sum over the matrices of dY_m W_m; dscales of each matrix.  The
+// gradients dY come from pre and dH (the feed-forward block, two matrices) or
+// are given (one matrix).
+struct BwdArgs {
+    int nmat;          // 2: the feed-forward block, 1: a linear layer
+    QMat mat[2];
+    int64_t O, I, T;
+    int act;
+    const float* pre;  // nmat == 2: [2][T][O]
+    const void* dY;    // dH or dY
+    bool dy_bf16;
+    const void* X;     // null without dscales
+    bool bf16;         // type of X and dX
+    void* dX;          // or null
+    float* dscales[2]; // or null
+    int accumulate;
+};
+struct BwdPlan {
+    bool planes;
+    int dx_mt, dx_splits;
+    int ds_mt, ds_tb, ds_splits;  // token tiles per wave, token blocks, splits of the groups
+    int64_t grad_off, dxpart_off, planes_off, dspart_off, bytes;
+};
+inline BwdPlan bwd_plan(int64_t T, int64_t I, int64_t O, int nmat, bool bf16, bool want_dx,
+                        bool want_ds) {
+    BwdPlan p{};
+    const int64_t G = cdiv(I, kGroup);
+    int64_t off = 0;
+    p.dx_splits = 1;
+    if (want_dx) {
+        const int64_t K = nmat * pad_to(O, kTileK);
+        p.dx_mt = tile_mt(T, bf16 ? 4 : 2);
+        p.dx_splits = inner_splits(cdiv(T, 128 * p.dx_mt) * cdiv(I, kTileN), K / kTileK, 16);
+        p.grad_off = off;
+        off += sect(T * K * (bf16 ? 2 : 4));
+        p.dxpart_off = off;
+        off += p.dx_splits > 1 ? sect(p.dx_splits * T * I * 4) : 0;
+    }
+    if (want_ds) {
+        p.planes = x_planes_needed(I, bf16);
+        p.planes_off = off;
+        off += p.planes ? x_planes_bytes(T, I, bf16) : 0;
+        p.ds_mt = tile_mt(T, bf16 ? 4 : 2);
+        p.ds_tb = (int)cdiv(T, 128 * p.ds_mt);
+        // the groups split freely: every block writes its own groups' sums
+        const int64_t blocks = nmat * cdiv(O, kTileN) * p.ds_tb;
+        p.ds_splits = 1;
+        while (p.ds_splits < 16 && blocks * p.ds_splits < kCUs && G / (2 * p.ds_splits) >= 4)
+            p.ds_splits *= 2;
+        p.dspart_off = off;
+        off += p.ds_tb > 1 ? sect(p.ds_tb * nmat * O * G * 4) : 0;
+    }
+    p.bytes = off;
+    return p;
+}
+hipError_t launch_bwd(const BwdArgs& a, void* workspace, hipStream_t s);
+
+// ------------------------------------------------------------ distillation
+struct DistillArgs {
+    const void* logits;
+    bool bf16;
+    int64_t T, V, ld;
+    const int32_t* idx;
+    const float* tl;
+    int k;
+    float tau;
+    const float* gloss;
+};
+// Blocks per row of the split form; 0: the row form (see distill.hip).
+inline int distill_splits(int64_t T, int64_t V, bool bf16) {
+    const int64_t vecs = cdiv(V, bf16 ? 8 : 4);
+    if (vecs <= 512 || (T >= 128 && vecs <= 16 * 1024)) return 0;
+    const int64_t s = vecs / 1024 < cdiv(1024, T) ? vecs / 1024 : cdiv(1024, T);
+    return (int)(s < 1 ? 1 : s > 256 ? 256 : s);
+}
+inline int distill_bwd_splits(int64_t T, int64_t V, bool bf16) {
+    const int64_t vecs = cdiv(V, bf16 ? 8 : 4);
+    const int64_t s = vecs / 1024 < cdiv(2048, T) ? vecs / 1024 : cdiv(2048, T);
+    return (int)(s < 1 ? 1 : s > 256 ? 256 : s);
+}
+inline int64_t distill_workspace(int64_t T, int64_t V, bool bf16) {
+    const int S = distill_splits(T, V, bf16);
+    return S == 0 ? 0 : T * (2 * S + 2) * 4;
+}
+hipError_t launch_distill(const DistillArgs& a, float* loss, float* lse, void* dlogits,
+                          int64_t ldd, void* workspace, hipStream_t s);
+hipError_t launch_distill_bwd(const DistillArgs& a, const float* lse, void* dlogits, int64_t ldd,
+                              hipStream_t s);
+
+}  // namespace qt

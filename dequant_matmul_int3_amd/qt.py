@@ -8,6 +8,7 @@ no fallback: if libqt.so is missing, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 
@@ -65,6 +66,31 @@ _SIGS = {
     "qt_gptq_proxy_workspace_bytes": (C.c_size_t, [C.c_int64, C.c_int64]),
     "qt_gptq_proxy": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64, C.c_int64,
                                 C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "qt_ffn_gated_workspace_bytes": (C.c_size_t, [C.c_int64, C.c_int64, C.c_int64, C.c_int]),
+    "qt_ffn_gated": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p,
+                               C.c_int32, C.c_int64, C.c_int64, C.c_int, C.c_void_p, C.c_int,
+                               C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t,
+                               C.c_void_p]),
+    "qt_ffn_gated_bwd_workspace_bytes": (C.c_size_t, [C.c_int64, C.c_int64, C.c_int64, C.c_int,
+                                                      C.c_int32, C.c_int32]),
+    "qt_ffn_gated_bwd": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p,
+                                   C.c_int32, C.c_int64, C.c_int64, C.c_int, C.c_void_p,
+                                   C.c_void_p, C.c_void_p, C.c_int, C.c_int64, C.c_void_p,
+                                   C.c_void_p, C.c_void_p, C.c_int32, C.c_void_p, C.c_size_t,
+                                   C.c_void_p]),
+    "qt_matmul_bwd_workspace_bytes": (C.c_size_t, [C.c_int64, C.c_int64, C.c_int64, C.c_int,
+                                                   C.c_int32, C.c_int32]),
+    "qt_matmul_bwd": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int32, C.c_int64, C.c_int64,
+                                C.c_void_p, C.c_int, C.c_void_p, C.c_int, C.c_int64, C.c_void_p,
+                                C.c_void_p, C.c_int32, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "qt_distill_topk_workspace_bytes": (C.c_size_t, [C.c_int64, C.c_int64, C.c_int]),
+    "qt_distill_topk": (C.c_int, [C.c_void_p, C.c_int, C.c_int64, C.c_int64, C.c_int64,
+                                  C.c_void_p, C.c_void_p, C.c_int32, C.c_float, C.c_void_p,
+                                  C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p,
+                                  C.c_size_t, C.c_void_p]),
+    "qt_distill_topk_bwd": (C.c_int, [C.c_void_p, C.c_int, C.c_int64, C.c_int64, C.c_int64,
+                                      C.c_void_p, C.c_void_p, C.c_int32, C.c_float, C.c_void_p,
+                                      C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p]),
     "qt_quantize_g64_i4": (C.c_int, [C.c_void_p, C.c_int64, C.c_int64, C.c_void_p, C.c_int32,
                                      C.c_float, C.c_float, C.c_void_p, C.c_void_p, C.c_void_p,
                                      C.c_void_p]),
@@ -412,3 +438,249 @@ def qt_moe_layer(X, logits, k: int, gate, up, down, out=None, workspace=None, st
                               _ptr(down[0]), _ptr(down[1]), int(down[2]), _ptr(out),
                               _ptr(workspace), wsb, _stream(stream, dev)), "qt_moe_layer")
     return out
+
+
+# ------------------------------------- gated feed-forward block and its tuning
+QT_ACT = {"silu": 0, "gelu": 1}
+
+
+def _on(dev, stream=None):
+    """Context of a call on dev: its device is current (a launch goes to the
+    current device), and what it allocates belongs to the stream given."""
+    stack = contextlib.ExitStack()
+    if dev.index != torch.cuda.current_device():
+        stack.enter_context(torch.cuda.device(dev))
+    if stream is not None:
+        s = torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream
+        stack.enter_context(torch.cuda.stream(s))
+    return stack
+
+
+def _xtype(t, what):
+    if t.dtype == torch.float32:
+        return QT_F32
+    if t.dtype == torch.bfloat16:
+        return QT_BF16
+    raise ValueError(f"{what} must be float32 or bfloat16")
+
+
+def _is(t, shape, dtype, what):
+    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+        raise ValueError(f"{what} must be {dtype} of shape {tuple(shape)}")
+
+
+def _weight(w, I, what):
+    """(packed, scales [O, G], bits) of an O x I matrix, checked -> O."""
+    packed, scales, bits = w
+    if bits not in (3, 4):
+        raise ValueError(f"{what}: bits must be 3 or 4")
+    if scales.dim() != 2 or scales.dtype != torch.float32 or scales.shape[1] != -(-I // 64):
+        raise ValueError(f"{what}: scales must be float32 [O, ceil({I}/64)]")
+    O, G = scales.shape
+    if packed.dtype != torch.uint8 or packed.numel() != O * G * (24 if bits == 3 else 32):
+        raise ValueError(f"{what}: packed bytes do not match the scales' shape and {bits} bits")
+    return O
+
+
+def _scratch(need, device, workspace):
+    """A workspace of at least need bytes, or (None, 0) where none is needed."""
+    if workspace is None:
+        if need == 0:
+            return None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def qt_ffn_gated_workspace_bytes(T: int, D: int, F: int, xt: int) -> int:
+    return int(lib().qt_ffn_gated_workspace_bytes(T, D, F, xt))
+
+
+def qt_ffn_gated_bwd_workspace_bytes(T: int, D: int, F: int, xt: int, want_dx: bool = True,
+                                     want_dscales: bool = True) -> int:
+    return int(lib().qt_ffn_gated_bwd_workspace_bytes(T, D, F, xt, int(want_dx),
+                                                      int(want_dscales)))
+
+
+def qt_matmul_bwd_workspace_bytes(B: int, I: int, O: int, xt: int, want_dx: bool = True,
+                                  want_dscales: bool = True) -> int:
+    return int(lib().qt_matmul_bwd_workspace_bytes(B, I, O, xt, int(want_dx), int(want_dscales)))
+
+
+def qt_distill_topk_workspace_bytes(T: int, V: int, lt: int) -> int:
+    return int(lib().qt_distill_topk_workspace_bytes(T, V, lt))
+
+
+def _gate_up(gate, up, X, act):
+    if act not in QT_ACT:
+        raise ValueError(f"act must be one of {sorted(QT_ACT)}")
+    if X.dim() != 2:
+        raise ValueError("X must be [T, D]")
+    T, D = X.shape
+    F = _weight(gate, D, "gate")
+    if _weight(up, D, "up") != F:
+        raise ValueError("gate and up must have the same rows")
+    return T, D, F
+
+
+def qt_ffn_gated(gate, up, X, act: str = "silu", H=None, pre=None, want_pre: bool = False,
+                 workspace=None, stream=None):
+    """H [T, F] = act(X Wg^T) * (X Wu^T) for X [T, D] f32 or bf16 and gate, up =
+    (packed, scales [F, G], bits).  With want_pre or a given pre ([2, T, F]
+    f32, the pre-activations that qt_ffn_gated_bwd takes) -> (H, pre)."""
+    T, D, F = _gate_up(gate, up, X, act)
+    xt = _xtype(X, "X")
+    with _on(X.device, stream):
+        if H is None:
+            H = torch.empty((T, F), dtype=X.dtype, device=X.device)
+        if pre is None and want_pre:
+            pre = torch.empty((2, T, F), dtype=torch.float32, device=X.device)
+        workspace, wsb = _scratch(qt_ffn_gated_workspace_bytes(T, D, F, xt), X.device, workspace)
+        _is(H, (T, F), X.dtype, "H")
+        _is(pre, (2, T, F), torch.float32, "pre")
+        dev = _dev(X, gate[0], gate[1], up[0], up[1], H, pre, workspace)
+        _check(lib().qt_ffn_gated(_ptr(gate[0]), _ptr(gate[1]), gate[2], _ptr(up[0]), _ptr(up[1]),
+                                  up[2], F, D, QT_ACT[act], _ptr(X), xt, T, _ptr(H), _ptr(pre),
+                                  _ptr(workspace), wsb, _stream(stream, dev)), "qt_ffn_gated")
+    return H if pre is None else (H, pre)
+
+
+def qt_ffn_gated_bwd(gate, up, pre, dH, X, act: str = "silu", dX=None, dgate_scales=None,
+                     dup_scales=None, want_dx: bool = True, want_dscales: bool = True,
+                     accumulate: bool = False, workspace=None, stream=None):
+    """-> (dX [T, D] or None, dgate_scales [F, G] or None, dup_scales or None)
+    for the pre that qt_ffn_gated kept and dH [T, F].  accumulate adds to the
+    given scales' gradients."""
+    T, D, F = _gate_up(gate, up, X, act)
+    xt = _xtype(X, "X")
+    G = gate[1].shape[1]
+    want_dx = want_dx or dX is not None
+    want_dscales = want_dscales or dgate_scales is not None or dup_scales is not None
+    if accumulate and want_dscales and (dgate_scales is None or dup_scales is None):
+        raise ValueError("accumulate needs dgate_scales and dup_scales")
+    with _on(X.device, stream):
+        if want_dx and dX is None:
+            dX = torch.empty((T, D), dtype=X.dtype, device=X.device)
+        if want_dscales:
+            if dgate_scales is None:
+                dgate_scales = torch.empty((F, G), dtype=torch.float32, device=X.device)
+            if dup_scales is None:
+                dup_scales = torch.empty((F, G), dtype=torch.float32, device=X.device)
+        need = qt_ffn_gated_bwd_workspace_bytes(T, D, F, xt, want_dx, want_dscales)
+        workspace, wsb = _scratch(need, X.device, workspace)
+        _is(pre, (2, T, F), torch.float32, "pre")
+        _is(dH, (T, F), X.dtype, "dH")
+        _is(dX, (T, D), X.dtype, "dX")
+        _is(dgate_scales, (F, G), torch.float32, "dgate_scales")
+        _is(dup_scales, (F, G), torch.float32, "dup_scales")
+        dev = _dev(X, gate[0], gate[1], up[0], up[1], pre, dH, dX, dgate_scales, dup_scales,
+                   workspace)
+        _check(lib().qt_ffn_gated_bwd(_ptr(gate[0]), _ptr(gate[1]), gate[2], _ptr(up[0]),
+                                      _ptr(up[1]), up[2], F, D, QT_ACT[act], _ptr(pre), _ptr(dH),
+                                      _ptr(X), xt, T, _ptr(dX), _ptr(dgate_scales),
+                                      _ptr(dup_scales), int(accumulate), _ptr(workspace), wsb,
+                                      _stream(stream, dev)), "qt_ffn_gated_bwd")
+    return dX, dgate_scales, dup_scales
+
+
+def qt_matmul_bwd(weight, dY, X, dX=None, dscales=None, want_dx: bool = True,
+                  want_dscales: bool = True, accumulate: bool = False, workspace=None,
+                  stream=None):
+    """-> (dX [B, I] or None, dscales [O, G] or None) of Y = X W^T for weight =
+    (packed, scales [O, G], bits), dY [B, O] and X [B, I], each f32 or bf16."""
+    if X.dim() != 2:
+        raise ValueError("X must be [B, I]")
+    B, I = X.shape
+    O = _weight(weight, I, "weight")
+    xt, yt = _xtype(X, "X"), _xtype(dY, "dY")
+    G = weight[1].shape[1]
+    want_dx = want_dx or dX is not None
+    want_dscales = want_dscales or dscales is not None
+    if accumulate and want_dscales and dscales is None:
+        raise ValueError("accumulate needs dscales")
+    with _on(X.device, stream):
+        if want_dx and dX is None:
+            dX = torch.empty((B, I), dtype=X.dtype, device=X.device)
+        if want_dscales and dscales is None:
+            dscales = torch.empty((O, G), dtype=torch.float32, device=X.device)
+        need = qt_matmul_bwd_workspace_bytes(B, I, O, xt, want_dx, want_dscales)
+        workspace, wsb = _scratch(need, X.device, workspace)
+        _is(dY, (B, O), dY.dtype, "dY")
+        _is(dX, (B, I), X.dtype, "dX")
+        _is(dscales, (O, G), torch.float32, "dscales")
+        dev = _dev(X, weight[0], weight[1], dY, dX, dscales, workspace)
+        _check(lib().qt_matmul_bwd(_ptr(weight[0]), _ptr(weight[1]), weight[2], O, I, _ptr(dY), yt,
+                                   _ptr(X), xt, B, _ptr(dX), _ptr(dscales), int(accumulate),
+                                   _ptr(workspace), wsb, _stream(stream, dev)), "qt_matmul_bwd")
+    return dX, dscales
+
+
+def _rows(t, what):
+    """Row stride of a [T, V] tensor whose rows are contiguous (a slice of
+    padded rows, say)."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} must be [T, V] with contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _distill_args(logits, idx, tlogits, gloss, dlogits):
+    ldl = _rows(logits, "logits")
+    T, V = logits.shape
+    if idx.dim() != 2 or idx.shape[0] != T:
+        raise ValueError("idx must be [T, k]")
+    k = idx.shape[1]
+    _is(idx, (T, k), torch.int32, "idx")
+    _is(tlogits, (T, k), torch.float32, "tlogits")
+    _is(gloss, (T,), torch.float32, "gloss")
+    if dlogits is not None:
+        _is(dlogits, (T, V), logits.dtype, "dlogits")
+        if dlogits.device != logits.device:
+            raise ValueError("all tensors must be on the same device")
+    ldd = V if dlogits is None else _rows(dlogits, "dlogits")
+    return T, V, k, ldl, ldd
+
+
+def qt_distill_topk(logits, idx, tlogits, tau: float = 1.0, gloss=None, dlogits=None,
+                    want_dlogits: bool = False, loss=None, lse=None, workspace=None, stream=None):
+    """-> (loss [T], lse [T], dlogits [T, V] or None): KL from the teacher's
+    top-k logits (idx, tlogits [T, k]; idx -1 pads) to softmax(logits / tau),
+    times tau^2, and its gradient times gloss [T] (None: ones).  logits [T, V]
+    f32 or bf16, rows of any stride; dlogits may be logits itself."""
+    lt = _xtype(logits, "logits")
+    with _on(logits.device, stream):
+        if dlogits is None and want_dlogits:
+            dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        T, V, k, ldl, ldd = _distill_args(logits, idx, tlogits, gloss, dlogits)
+        if loss is None:
+            loss = torch.empty(T, dtype=torch.float32, device=logits.device)
+        if lse is None:
+            lse = torch.empty(T, dtype=torch.float32, device=logits.device)
+        _is(loss, (T,), torch.float32, "loss")
+        _is(lse, (T,), torch.float32, "lse")
+        workspace, wsb = _scratch(qt_distill_topk_workspace_bytes(T, V, lt), logits.device,
+                                  workspace)
+        dev = _dev(idx, tlogits, gloss, loss, lse, workspace)
+        if dev != logits.device:
+            raise ValueError("all tensors must be on the same device")
+        _check(lib().qt_distill_topk(_ptr(logits), lt, T, V, ldl, _ptr(idx), _ptr(tlogits), k, tau,
+                                     _ptr(loss), _ptr(lse), _ptr(gloss), _ptr(dlogits), ldd,
+                                     _ptr(workspace), wsb, _stream(stream, dev)),
+               "qt_distill_topk")
+    return loss, lse, dlogits
+
+
+def qt_distill_topk_bwd(logits, idx, tlogits, lse, gloss=None, tau: float = 1.0, dlogits=None,
+                        stream=None):
+    """dlogits [T, V] of qt_distill_topk from its lse, times gloss [T]."""
+    lt = _xtype(logits, "logits")
+    with _on(logits.device, stream):
+        if dlogits is None:
+            dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        T, V, k, ldl, ldd = _distill_args(logits, idx, tlogits, gloss, dlogits)
+        _is(lse, (T,), torch.float32, "lse")
+        dev = _dev(idx, tlogits, gloss, lse)
+        if dev != logits.device:
+            raise ValueError("all tensors must be on the same device")
+        _check(lib().qt_distill_topk_bwd(_ptr(logits), lt, T, V, ldl, _ptr(idx), _ptr(tlogits), k,
+                                         tau, _ptr(lse), _ptr(gloss), _ptr(dlogits), ldd,
+                                         _stream(stream, dev)), "qt_distill_topk_bwd")
+    return dlogits

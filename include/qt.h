@@ -397,6 +397,113 @@ qt_status qt_moe_layer(const float* X, int64_t T, int64_t D, int64_t F, const fl
                        int32_t down_bits, float* out, void* workspace, size_t ws_bytes,
                        void* stream);
 
+/*
+ * Gated feed-forward block on packed weights, first half (the dense form of
+ * the expert layer's gate, up and SwiGLU): with Wg, Wu [F x D], each at
+ * int3-g64 or grouped int4 (bits 3 or 4),
+ *   H[t,f] = act(g[t,f]) * u[t,f],  g = X Wg^T,  u = X Wu^T,
+ *   QT_ACT_SILU: act(z) = z / (1 + e^-z)
+ *   QT_ACT_GELU: act(z) = z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))
+ * The down projection of H is a qt_matvec / qt_matmul call.
+ *   X [T x D] of type xt; H [T x F] of type xt, rounded once at the end
+ *   pre  f32 [2][T][F] (g, then u; what qt_ffn_gated_bwd needs), or NULL
+ * Sums are f32.  f32 inputs, and bf16 calls of up to 64 tokens, take the exact
+ * codes with f32 group sums and scales: g and u within 1e-5 of
+ * sum_i |w_fi X_ti|.  bf16 calls of more tokens take bf16(s v), each weight
+ * rounded once: within 2^-8 of that sum.
+ *   packed 16-byte aligned; X 16-byte aligned where xt is QT_BF16 and D a
+ *   multiple of 64 (its rows are read in place), else at its elements'
+ *   alignment; 1 <= T <= 2^22; 1 <= D, F <= 2^20.
+ *   workspace: qt_ffn_gated_workspace_bytes(T, D, F, xt) bytes (16-byte
+ *   aligned; may be NULL when that size is 0).  Calls that may overlap in
+ *   time need a workspace each (also: graphs captured over one workspace must
+ *   not replay at the same time); the same holds for the calls below.
+ */
+typedef enum { QT_ACT_SILU = 0, QT_ACT_GELU = 1 } qt_act;
+
+size_t qt_ffn_gated_workspace_bytes(int64_t T, int64_t D, int64_t F, qt_dtype xt);
+qt_status qt_ffn_gated(const uint8_t* gate_packed, const float* gate_scales, int32_t gate_bits,
+                       const uint8_t* up_packed, const float* up_scales, int32_t up_bits,
+                       int64_t F, int64_t D, qt_act act, const void* X, qt_dtype xt, int64_t T,
+                       void* H, float* pre, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Backward pass of qt_ffn_gated for frozen codes: the gradients of X and of
+ * both projections' group scales.  With dg = dH u act'(g), du = dH act(g):
+ *   dX = dg Wg + du Wu                                        [T x D] type xt
+ *   dgate_scales[f,G] = sum_t dg[t,f] sum_j v_g[f,64G+j] X[t,64G+j]   f32
+ *   dup_scales likewise from du and the up codes              [F x ceil(D/64)]
+ *   pre as qt_ffn_gated wrote it; dH [T x F] of type xt; X [T x D] (needed for
+ *   the scales' gradients only, else it may be NULL)
+ *   dX may be NULL; dgate_scales and dup_scales may both be NULL; at least
+ *   one kind is wanted.  accumulate = 1 adds to the scales' gradients that
+ *   are there (dX is always written).
+ * bf16: dX takes dg, du and s v rounded once each to bf16, f32 sums and one
+ * rounding at the end.  The scales' gradients are f32 throughout: exact codes
+ * and inputs, f32 dg and du.
+ *   Alignment and sizes as qt_ffn_gated; workspace:
+ *   qt_ffn_gated_bwd_workspace_bytes(T, D, F, xt, dX wanted, scales wanted).
+ */
+size_t qt_ffn_gated_bwd_workspace_bytes(int64_t T, int64_t D, int64_t F, qt_dtype xt,
+                                        int32_t want_dx, int32_t want_dscales);
+qt_status qt_ffn_gated_bwd(const uint8_t* gate_packed, const float* gate_scales,
+                           int32_t gate_bits, const uint8_t* up_packed, const float* up_scales,
+                           int32_t up_bits, int64_t F, int64_t D, qt_act act, const float* pre,
+                           const void* dH, const void* X, qt_dtype xt, int64_t T, void* dX,
+                           float* dgate_scales, float* dup_scales, int32_t accumulate,
+                           void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Backward pass of qt_matmul_i3 / qt_matmul_i4 (bits 3 / 4) for frozen codes:
+ *   dX[b,i] = sum_o dY[b,o] w[o,i]                           [B x I] type xt
+ *   dscales[o,g] = sum_b dY[b,o] sum_j v[o,64g+j] X[b,64g+j]  [O x G] f32
+ *   dY [B x O] of type yt, X [B x I] of type xt (any pair of types)
+ * dX, dscales (not both), X without dscales may be NULL; roundings,
+ * accumulate, alignment and sizes (B, I, O as T, D, F) as qt_ffn_gated_bwd.
+ */
+size_t qt_matmul_bwd_workspace_bytes(int64_t B, int64_t I, int64_t O, qt_dtype xt,
+                                     int32_t want_dx, int32_t want_dscales);
+qt_status qt_matmul_bwd(const uint8_t* packed, const float* scales, int32_t bits, int64_t O,
+                        int64_t I, const void* dY, qt_dtype yt, const void* X, qt_dtype xt,
+                        int64_t B, void* dX, float* dscales, int32_t accumulate,
+                        void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Distillation from a teacher's top-k logits: what a quantized network's
+ * answer z loses against the unquantized network's, and its gradient (the
+ * NeUQI accuracy page measures quantized networks by this divergence; it
+ * drives the tuning of the group scales).  Row t:
+ *   entries j < k with 0 <= idx[t,j] < V count, others are ignored (-1 pads)
+ *   p = softmax over those entries of tlogits[t,j] / tau
+ *   lse[t] = ln sum_v exp(z[t,v] / tau)
+ *   loss[t] = tau^2 sum_j p_j (ln p_j - z[t,idx_j] / tau + lse[t])
+ *   dlogits[t,v] = gloss[t] tau (exp(z[t,v]/tau - lse[t]) - sum_{idx_j = v} p_j)
+ * gloss NULL: all ones.  An index may occur several times.  A row in which no
+ * entry counts, or whose counting entries are all -inf, has loss 0 and a zero
+ * gradient whatever its logits hold.  -inf logits have probability 0 (loss
+ * +inf where the teacher gives them mass); a row with a NaN, a +inf or nothing
+ * but -inf gives NaN.  Unlike the other calls, non-finite inputs are specified.
+ *   logits [T x V] of type lt with rows ldl >= V elements apart; dlogits
+ *   likewise with ldd; columns past V are neither read nor written.  dlogits
+ *   may be logits itself (same stride): the gradient then replaces them.
+ *   idx [T x k] int32, tlogits [T x k] f32; 1 <= k <= 1024; tau > 0 finite;
+ *   loss, lse [T] f32.
+ * qt_distill_topk writes loss and lse, and dlogits unless it is NULL.
+ * workspace: qt_distill_topk_workspace_bytes(T, V, lt) bytes (16-byte
+ * aligned; may be NULL when that size is 0).
+ * qt_distill_topk_bwd writes dlogits alone, from the lse of the former call.
+ *   1 <= T <= 2^22; 1 <= V < 2^31.
+ */
+size_t qt_distill_topk_workspace_bytes(int64_t T, int64_t V, qt_dtype lt);
+qt_status qt_distill_topk(const void* logits, qt_dtype lt, int64_t T, int64_t V, int64_t ldl,
+                          const int32_t* idx, const float* tlogits, int32_t k, float tau,
+                          float* loss, float* lse, const float* gloss, void* dlogits,
+                          int64_t ldd, void* workspace, size_t ws_bytes, void* stream);
+qt_status qt_distill_topk_bwd(const void* logits, qt_dtype lt, int64_t T, int64_t V, int64_t ldl,
+                              const int32_t* idx, const float* tlogits, int32_t k, float tau,
+                              const float* lse, const float* gloss, void* dlogits, int64_t ldd,
+                              void* stream);
+
 #ifdef __cplusplus
 }
 #endif
