@@ -30,22 +30,43 @@
 namespace qt {
 namespace {
 
+typedef f32x4_t f32x4_u __attribute__((aligned(4)));
+typedef u32x2_t u32x2_u __attribute__((aligned(2)));
+typedef u32x4_t u32x4_u __attribute__((aligned(2)));
+
 // ------------------------------------------------------------ input planes
-// X [T x D] -> planes [NP][T][Dp] bf16: the value itself (bf16) or its three
-// pieces (f32), zero past D.
-template <bool BF16>
+// X [T x D] -> bf16 planes: the value itself (bf16) or its three pieces (f32),
+// zero past D.  BLOCKED false: [NP][T][Dp] rows.  BLOCKED true: matrix-operand
+// order, [NP][ceil(T/16)][Dp/32] blocks of 64 lanes x 16 bytes (lane l holds
+// values 8 (l / 16) .. + 7 of token l % 16), zero past T: every operand load of
+// the tiles is then one contiguous kilobyte.  Reading rows in place instead
+// touched 16 half lines per load and measured 715 against 830 TFLOP/s.
+template <bool BF16, bool BLOCKED>
 __global__ __launch_bounds__(256) void planes_kernel(const void* __restrict__ X, int64_t T,
                                                      int64_t D, int64_t Dp,
                                                      uint16_t* __restrict__ P) {
-    const int64_t per = Dp / 8;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= T * per) return;
-    const int64_t t = i / per, d0 = (i - t * per) * 8;
+    const int64_t Tp = BLOCKED ? (T + 15) / 16 * 16 : T;
+    if (i >= Tp * (Dp / 8)) return;
+    int64_t t, d0;
+    if constexpr (BLOCKED) {
+        const int64_t blk = i >> 6, kb = Dp / 32;
+        t = blk / kb * 16 + (i & 15);
+        d0 = blk % kb * 32 + ((i & 63) >> 4) * 8;
+    } else {
+        t = i / (Dp / 8);
+        d0 = i % (Dp / 8) * 8;
+    }
     uint32_t h[8], m[8], l[8];
+    if (BF16 && t < T && d0 + 8 <= D) {
+        const uint16_t* x = reinterpret_cast<const uint16_t*>(X) + t * D + d0;
+        reinterpret_cast<u32x4_t*>(P)[i] = *reinterpret_cast<const u32x4_u*>(x);
+        return;
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const bool in = d0 + e < D;
-        const int64_t at = t * D + (in ? d0 + e : 0);
+        const bool in = t < T && d0 + e < D;
+        const int64_t at = in ? t * D + d0 + e : 0;
         if constexpr (BF16) {
             const uint32_t b = reinterpret_cast<const uint16_t*>(X)[at];
             h[e] = in ? b : 0u;
@@ -55,7 +76,7 @@ __global__ __launch_bounds__(256) void planes_kernel(const void* __restrict__ X,
         }
     }
     auto put = [&](int64_t plane, const uint32_t (&v)[8]) {
-        *reinterpret_cast<u32x4_t*>(P + (plane * T + t) * Dp + d0) =
+        reinterpret_cast<u32x4_t*>(P)[plane * (Tp * Dp / 8) + i] =
             u32x4_t{v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16};
     };
     put(0, h);
@@ -66,44 +87,6 @@ __global__ __launch_bounds__(256) void planes_kernel(const void* __restrict__ X,
 }
 
 // --------------------------------------------------------------- small form
-template <int BITS>
-struct RowGroup;  // one lane's group
-template <>
-struct RowGroup<3> {
-    u32x2_t w[3];
-    __device__ __forceinline__ void load(const uint8_t* __restrict__ p) {
-#pragma unroll
-        for (int i = 0; i < 3; ++i)
-            w[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(p) + i);
-    }
-    // lane row h gets quarter h of the four lane rows' groups
-    __device__ __forceinline__ void quarters(Quarter (&q)[4]) const {
-        uint32_t a[4] = {w[0].x, w[0].y, w[1].x, w[1].y};
-        uint32_t b[4] = {w[2].x, w[2].x, w[2].y, w[2].y};
-        transpose_rows(a);
-        transpose_rows(b);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) q[j] = Quarter{a[j], b[j]};
-    }
-};
-template <>
-struct RowGroup<4> {
-    u32x4_t w[2];
-    __device__ __forceinline__ void load(const uint8_t* __restrict__ p) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            w[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p) + i);
-    }
-    __device__ __forceinline__ void quarters(Quarter (&q)[4]) const {
-        uint32_t a[4] = {w[0].x, w[0].z, w[1].x, w[1].z};
-        uint32_t b[4] = {w[0].y, w[0].w, w[1].y, w[1].w};
-        transpose_rows(a);
-        transpose_rows(b);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) q[j] = Quarter{a[j], b[j]};
-    }
-};
-
 struct SmallArgs {
     const uint8_t *gp, *up;
     const float *gs, *us;
@@ -144,8 +127,8 @@ __global__ __launch_bounds__(1024) void ffn_small_kernel(const SmallArgs a) {
         for (int mt = 0; mt < MT; ++mt) acc[x][mt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
     struct Chunk {
-        RowGroup<GB> g;
-        RowGroup<UB> u;
+        RowGroup<GB, true> g;
+        RowGroup<UB, true> u;
         float sg, su;
     };
     // four groups of the lane's row, one per lane row; past the row a valid
@@ -278,29 +261,18 @@ hipError_t small_mt(const SmallArgs& a, bool bf16, hipStream_t s) {
 
 // ---------------------------------------------------------------- tile form
 constexpr int kThreads = 512;
-constexpr int kNT = kTileN / 16;  // B tiles of a block: even ones gate, odd ones up
 
 struct TileArgs {
     QMat gate, up;
     int64_t F, G;
-    const uint16_t* A;   // planes [NP][T][ld]
-    int64_t ld, T;
+    const uint16_t* A;   // blocked planes [NP][T16][2 G] of 1 KB
+    int64_t T;
     int act, splits;
     int64_t mblk, nblk;  // token and feature blocks
     void* H;
     float* pre;          // [2][T][F] or null
     float* part;         // [splits][2][T][F], splits > 1
 };
-
-// Consecutive block ids run on different XCDs (8 of them, each with its own
-// L2): the ids are remapped so that every XCD takes a contiguous range.
-__device__ __forceinline__ int64_t xcd_range(int64_t lin, int64_t n) {
-    const int64_t x = lin & 7, q = n >> 3, r = n & 7;
-    return x * q + std::min(x, r) + (lin >> 3);
-}
-
-typedef f32x4_t f32x4_u __attribute__((aligned(4)));
-typedef u32x2_t u32x2_u __attribute__((aligned(2)));
 
 // four consecutive values of a row, those before `left` only
 __device__ __forceinline__ void store4(float* p, const f32x4_t& v, int64_t left) {
@@ -322,11 +294,15 @@ __device__ __forceinline__ void store4(__bf16* p, const f32x4_t& v, int64_t left
     }
 }
 
-template <int NP, int MT>
+// NP pieces per input, MT 16-token tiles per wave, NT weight tiles per block;
+// a weight tile is 8 gate rows and 8 up rows of the same features.
+template <int GB, int UB, int NP, int MT, int NT>
 __global__ __launch_bounds__(kThreads) void ffn_tile_kernel(const TileArgs a) {
-    constexpr bool EXACT = NP == 3;
-    __shared__ __attribute__((aligned(16))) u32x4_t ws[2][kNT * 2 * 64];
-    __shared__ __attribute__((aligned(16))) float ss[2][kTileN];
+    // eight weight tiles, one per wave, of which NT are used: every wave runs
+    // the same straight code
+    __shared__ __attribute__((aligned(16))) u32x4_t ws[2][8 * 2 * 64];
+    __shared__ __attribute__((aligned(16))) float ss[2][8 * 16];
+    __shared__ __attribute__((aligned(16))) float turn[8 * 16 * (NT * 16 + 4)];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int h4 = lane >> 4, l16 = lane & 15;
@@ -334,46 +310,33 @@ __global__ __launch_bounds__(kThreads) void ffn_tile_kernel(const TileArgs a) {
     const int64_t n = tile % a.nblk, mm = tile / a.nblk;
     const int64_t m0 = (mm % a.mblk) * (128 * MT);
     const int sp = (int)(mm / a.mblk);
-    const int g0 = (int)(a.G * sp / a.splits), g1 = (int)(a.G * (sp + 1) / a.splits);
+    const int G = (int)a.G;
+    const int g0 = split_begin(G, sp, a.splits), g1 = split_begin(G, sp + 1, a.splits);
 
-    // ---- weights: wave w unpacks B tile w, lane = (quarter, row); rows past
-    // F read a valid row and are not stored
-    const bool is_up = wave & 1;
-    const QMat mat = is_up ? a.up : a.gate;
-    const int q = h4;
-    const int64_t frow = std::min<int64_t>(n * 64 + (wave >> 1) * 16 + l16, a.F - 1);
-    const int gby = mat.bits == 3 ? kGroupBytes : kGroupBytesI4;
-    const uint8_t* wp = mat.packed + frow * a.G * gby;
-    const float* sp_ = mat.scales + frow * a.G;
-    struct Raw {
-        Quarter w;
-        float s;
-    };
-    auto load_raw = [&](int g, Raw& r) {
-        r.w = load_quarter(wp + (int64_t)g * gby, q, mat.bits);
-        r.s = sp_[g];
-    };
-    auto unpack = [&](int buf, const Raw& r) {
+    // ---- weights: wave w unpacks weight tile w (four groups' words at a
+    // time); rows past F read a valid row and are not stored
+    RowFeed<GB, UB> feed;
+    feed.init(a.gate, a.up, l16 >= 8,
+              std::min<int64_t>(n * (NT * 8) + wave * 8 + (l16 & 7), a.F - 1), G, h4);
+    feed.load(g0);
+    // word j of the feed, group g, into LDS buffer buf; groups past the block's
+    // range get the scale 0 and add nothing
+    auto unpack = [&](int buf, int j, int g) {
         u32x4_t lo8, hi8;
-        if constexpr (EXACT) {
-            exact_quarter(r.w, q, mat.bits, lo8, hi8);
-            if (q == 0) ss[buf][wave * 16 + l16] = r.s * code_unit(mat.bits);
-        } else {
-            scaled_quarter(r.w, q, mat.bits, r.s, lo8, hi8);
-        }
-        u32x4_t* d = &ws[buf][(2 * wave + (q >> 1)) * 64 + 32 * (q & 1) + l16];
+        feed.exact(j, h4, lo8, hi8);
+        u32x4_t* d = &ws[buf][(2 * wave + (h4 >> 1)) * 64 + 32 * (h4 & 1) + l16];
         d[0] = lo8;
         d[16] = hi8;
+        ss[buf][wave * 16 + l16] = g < g1 ? feed.scale(j) : 0.0f;  // four lanes, one value
     };
 
-    // ---- inputs: lane's 8 consecutive values of its tokens, both 32-deep
-    // steps of a group; tokens past T read a valid row
+    // ---- inputs: one kilobyte per 16 tokens and 32 inner elements; token
+    // tiles past T read a valid one
+    const int64_t t16 = (a.T + 15) / 16, plane = t16 * 2 * G * 512;
     const uint16_t* ap[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
-        ap[mt] = a.A +
-                 std::min<int64_t>(m0 + wave * (16 * MT) + mt * 16 + l16, a.T - 1) * a.ld + 8 * h4;
-    const int64_t plane = a.T * a.ld;
+        ap[mt] = a.A + std::min<int64_t>(m0 / 16 + wave * MT + mt, t16 - 1) * (2 * G * 512) + 8 * lane;
     struct In {
         u32x4_t v[NP][MT][2];
     };
@@ -385,82 +348,115 @@ __global__ __launch_bounds__(kThreads) void ffn_tile_kernel(const TileArgs a) {
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks)
                     x.v[p][mt][ks] = *reinterpret_cast<const u32x4_t*>(
-                        ap[mt] + p * plane + (int64_t)g * kGroup + 32 * ks);
+                        ap[mt] + p * plane + (int64_t)(2 * g + ks) * 512);
     };
 
-    f32x4_t acc[MT][kNT];
+    f32x4_t acc[MT][NT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) acc[mt][nt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-    // The weights are the first operand: register r of lane l of a product
-    // is feature 4 (l / 16) + r and token l % 16.
-    auto step = [&](int buf, const In& x) {
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) {
-            bf16x8_t b[2];
+    // One group: products of the inputs x and LDS buffer buf, and the unpacking
+    // of word j of the feed into the other buffer.  Register r of lane l of a
+    // product is token 4 (l / 16) + r and weight row l % 16, so a lane needs one
+    // scale per weight tile (the other way round it needs four, and their LDS
+    // reads took half as long as the operands').  A weight tile's operands are
+    // read one tile ahead, a product's scale FMAs follow two products later,
+    // and the scheduling groups ask for vector instructions after every matrix
+    // instruction: they fill the matrix core's shadow.
+    auto step = [&](int buf, const In& x, int j, int gnext) {
+        bf16x8_t b[2][2];
+        float sc[NT];
+        f32x4_t part[3];
+        auto read_b = [&](int nt) {
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks)
-                b[ks] = __builtin_bit_cast(bf16x8_t, ws[buf][(2 * nt + ks) * 64 + lane]);
-            f32x4_t sc;
-            if constexpr (EXACT) sc = *reinterpret_cast<const f32x4_t*>(&ss[buf][nt * 16 + 4 * h4]);
+                b[nt & 1][ks] = __builtin_bit_cast(bf16x8_t, ws[buf][(2 * nt + ks) * 64 + lane]);
+        };
+        read_b(0);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                f32x4_t part;
-                if constexpr (EXACT) part = f32x4_t{0.f, 0.f, 0.f, 0.f};
-                else part = acc[mt][nt];
+        for (int nt = 0; nt < NT; ++nt) sc[nt] = ss[buf][nt * 16 + l16];
 #pragma unroll
-                for (int p = 0; p < NP; ++p)
+        for (int q = 0; q < NT * MT + 2; ++q) {
+            const int nt = q / MT, mt = q % MT, pn = (q - 2) / MT, pm = (q - 2) % MT;
+            if (mt == 0 && nt + 1 < NT) read_b(nt + 1);
+            if (q < NT * MT) {
+                f32x4_t p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int pc = 0; pc < NP; ++pc)
 #pragma unroll
                     for (int ks = 0; ks < 2; ++ks)
-                        part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            b[ks], __builtin_bit_cast(bf16x8_t, x.v[p][mt][ks]), part, 0, 0, 0);
-                if constexpr (EXACT) {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        acc[mt][nt][r] = __builtin_fmaf(sc[r], part[r], acc[mt][nt][r]);
-                } else {
-                    acc[mt][nt] = part;
-                }
+                        p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            __builtin_bit_cast(bf16x8_t, x.v[pc][mt][ks]), b[nt & 1][ks], p, 0, 0,
+                            0);
+                part[q % 3] = p;
             }
+            if (q >= 2) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    acc[pm][pn][r] = __builtin_fmaf(sc[pn], part[(q - 2) % 3][r], acc[pm][pn][r]);
+            }
+            if (q == NT * MT / 2) unpack(1 - buf, j, gnext);
+        }
+        // 0x8: matrix instruction, 0x2: other vector instruction
+#pragma unroll
+        for (int i = 0; i < 2 * NP * NT * MT; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x2, 2, 0);
         }
     };
 
     // group g: inputs in registers, weights in LDS buffer (g - g0) & 1; the
-    // loads of the next group's inputs and of the weights two groups ahead
-    // are in flight meanwhile (past the last group they repeat it)
+    // loads of the next group's inputs are in flight meanwhile (past the last
+    // group of the row they repeat it).  The feed's words of four groups are exchanged in
+    // every fourth step, when the words of the four before are used up, and
+    // the loads of the next four are issued.
     In x0, x1;
-    Raw r0, r1;
-    const int last = g1 - 1;
-    load_raw(g0, r0);
     load_a(g0, x0);
-    load_raw(std::min(g0 + 1, last), r1);
-    unpack(0, r0);
+    feed.take();
+    feed.load(g0 + 4);
+    unpack(0, 0, g0);
     lds_barrier();
-    auto group = [&](int g, int buf, const In& xc, In& xn, Raw& rl, const Raw& ru) {
-        load_a(std::min(g + 1, last), xn);
-        load_raw(std::min(g + 2, last), rl);
-        step(buf, xc);
-        unpack(1 - buf, ru);
+    auto group = [&](int g, int j, const In& xc, In& xn) {
+        load_a(std::min(g + 1, G - 1), xn);
+        if (j == 3) {
+            feed.take();
+            feed.load(g + 5);
+        }
+        step(j & 1, xc, (j + 1) & 3, g + 1);
         lds_barrier();
-        return g + 1 >= g1;
     };
-    for (int g = g0;; g += 2) {
-        if (group(g, 0, x0, x1, r0, r1)) break;
-        if (group(g + 1, 1, x1, x0, r1, r0)) break;
+    // four groups per turn with one exit (several exits with the accumulators
+    // live made the compiler spill them)
+    for (int g = g0; g < g1; g += 4) {
+        group(g, 0, x0, x1);
+        group(g + 1, 1, x1, x0);
+        group(g + 2, 2, x0, x1);
+        group(g + 3, 3, x1, x0);
     }
 
+    // Each wave turns 16 tokens at a time through LDS, so that a lane ends with
+    // four consecutive features of a token, gate and up.
+    constexpr int kRow = NT * 16 + 4;
+    float* tl = turn + wave * 16 * kRow;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-        const int64_t t = m0 + wave * (16 * MT) + mt * 16 + l16;
-        if (t >= a.T) continue;
 #pragma unroll
-        for (int j = 0; j < kNT / 2; ++j) {
-            const int64_t f = n * 64 + j * 16 + 4 * h4;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                tl[(4 * h4 + r) * kRow + nt * 16 + l16] = acc[mt][nt][r];
+#pragma unroll
+        for (int i = 0; i < NT / 2; ++i) {
+            const int k = i * 64 + lane, tt = k / (2 * NT), qd = k % (2 * NT);
+            const f32x4_t* at =
+                reinterpret_cast<const f32x4_t*>(&tl[tt * kRow + (qd >> 1) * 16 + (qd & 1) * 4]);
+            const f32x4_t g = at[0], u = at[2];
+            const int64_t t = m0 + wave * (16 * MT) + mt * 16 + tt;
+            const int64_t f = n * (NT * 8) + 4 * qd;
             const int64_t left = a.F - f, o = t * a.F + f;
-            if (left <= 0) continue;
-            const f32x4_t g = acc[mt][2 * j], u = acc[mt][2 * j + 1];
+            if (t >= a.T || left <= 0) continue;
             if (a.splits > 1) {
                 float* p = a.part + (int64_t)sp * 2 * a.T * a.F + o;
                 store4(p, g, left);
@@ -513,27 +509,39 @@ __global__ __launch_bounds__(256) void ffn_join_kernel(const float* __restrict__
     else store4(static_cast<float*>(H) + i, h, left);
 }
 
-template <int NP, int MT>
+template <int GB, int UB, int NP, int MT>
 hipError_t run_tile(const TileArgs& a, hipStream_t s) {
     const int64_t nb = a.mblk * a.nblk * a.splits;
     if (nb > 0x7FFFFFFF) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((ffn_tile_kernel<NP, MT>), dim3((unsigned)nb), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((ffn_tile_kernel<GB, UB, NP, MT, tile_nt(MT)>), dim3((unsigned)nb),
+                       dim3(kThreads), 0, s, a);
     return hipGetLastError();
+}
+template <int NP, int MT>
+hipError_t tile_bits(const TileArgs& a, hipStream_t s) {
+    if (a.gate.bits == 3)
+        return a.up.bits == 3 ? run_tile<3, 3, NP, MT>(a, s) : run_tile<3, 4, NP, MT>(a, s);
+    return a.up.bits == 3 ? run_tile<4, 3, NP, MT>(a, s) : run_tile<4, 4, NP, MT>(a, s);
 }
 
 }  // namespace
 
-hipError_t launch_x_planes(const void* X, bool bf16, int64_t T, int64_t D, uint16_t* planes,
-                           hipStream_t s) {
+hipError_t launch_x_planes(const void* X, bool bf16, bool blocked, int64_t T, int64_t D,
+                           uint16_t* planes, hipStream_t s) {
     const int64_t Dp = pad_to(D, kGroup);
-    const int64_t nb = cdiv(T * (Dp / 8), 256);
+    const int64_t nb = cdiv((blocked ? pad_to(T, 16) : T) * (Dp / 8), 256);
     if (nb > 0x7FFFFFFF) return hipErrorInvalidValue;
-    if (bf16)
-        hipLaunchKernelGGL((planes_kernel<true>), dim3((unsigned)nb), dim3(256), 0, s, X, T, D, Dp,
-                           planes);
-    else
-        hipLaunchKernelGGL((planes_kernel<false>), dim3((unsigned)nb), dim3(256), 0, s, X, T, D, Dp,
-                           planes);
+    const dim3 grid((unsigned)nb), block(256);
+#define QT_PLANES(B, K) \
+    hipLaunchKernelGGL((planes_kernel<B, K>), grid, block, 0, s, X, T, D, Dp, planes)
+    if (bf16) {
+        if (blocked) QT_PLANES(true, true);
+        else QT_PLANES(true, false);
+    } else {
+        if (blocked) QT_PLANES(false, true);
+        else QT_PLANES(false, false);
+    }
+#undef QT_PLANES
     return hipGetLastError();
 }
 
@@ -545,7 +553,7 @@ hipError_t launch_ffn_gated(const FfnArgs& a, void* workspace, hipStream_t s) {
     char* w = static_cast<char*>(workspace);
     if (p.planes) {
         uint16_t* planes = reinterpret_cast<uint16_t*>(w + p.planes_off);
-        const hipError_t e = launch_x_planes(a.X, a.bf16, a.T, a.D, planes, s);
+        const hipError_t e = launch_x_planes(a.X, a.bf16, !p.small, a.T, a.D, planes, s);
         if (e != hipSuccess) return e;
         A = planes;
     }
@@ -556,15 +564,15 @@ hipError_t launch_ffn_gated(const FfnArgs& a, void* workspace, hipStream_t s) {
             return a.up.bits == 3 ? small_mt<3, 3>(sa, a.bf16, s) : small_mt<3, 4>(sa, a.bf16, s);
         return a.up.bits == 3 ? small_mt<4, 3>(sa, a.bf16, s) : small_mt<4, 4>(sa, a.bf16, s);
     }
-    TileArgs ta{a.gate, a.up, a.F, G, A, Dp, a.T, a.act, p.splits, cdiv(a.T, 128 * p.mt),
-                cdiv(a.F, kTileN / 2), a.H, a.pre,
+    TileArgs ta{a.gate, a.up, a.F, G, A, a.T, a.act, p.splits, cdiv(a.T, 128 * p.mt),
+                cdiv(a.F, 8 * tile_nt(p.mt)), a.H, a.pre,
                 p.splits > 1 ? reinterpret_cast<float*>(w + p.part_off) : nullptr};
     hipError_t e;
     if (a.bf16)
-        e = p.mt == 1 ? run_tile<1, 1>(ta, s) : p.mt == 2 ? run_tile<1, 2>(ta, s)
-                                                          : run_tile<1, 4>(ta, s);
+        e = p.mt == 1 ? tile_bits<1, 1>(ta, s) : p.mt == 2 ? tile_bits<1, 2>(ta, s)
+                                                           : tile_bits<1, 4>(ta, s);
     else
-        e = p.mt == 1 ? run_tile<3, 1>(ta, s) : run_tile<3, 2>(ta, s);
+        e = p.mt == 1 ? tile_bits<3, 1>(ta, s) : tile_bits<3, 2>(ta, s);
     if (e != hipSuccess || p.splits == 1) return e;
     const int64_t n = a.T * a.F, nb = cdiv(n, 1024);
     if (nb > 0x7FFFFFFF) return hipErrorInvalidValue;

@@ -37,14 +37,14 @@ constexpr int kSmallRows = 64;
 inline int ffn_pieces(bool bf16) { return bf16 ? 1 : 3; }
 inline bool ffn_small(int64_t T, bool bf16) { return T * ffn_pieces(bf16) <= kSmallRows; }
 
-// Inputs are copied into padded bf16 planes when they are f32 or their rows
-// are not whole groups (the plane's padding is zero).
-inline bool x_planes_needed(int64_t D, bool bf16) { return !bf16 || D % kGroup != 0; }
-inline int64_t x_planes_bytes(int64_t T, int64_t D, bool bf16) {
-    return sect(T * ffn_pieces(bf16) * pad_to(D, kGroup) * 2);
+// Bytes of the input's bf16 planes: rows of whole groups (the small form,
+// where bf16 rows that are whole groups already are read in place instead), or
+// operand blocks of 16 tokens (the tiles).
+inline int64_t x_planes_bytes(int64_t T, int64_t D, bool bf16, bool blocked) {
+    return sect(ffn_pieces(bf16) * (blocked ? pad_to(T, 16) : T) * pad_to(D, kGroup) * 2);
 }
 
-constexpr int kTileN = 128;  // B columns of a block tile
+constexpr int kTileN = 128;  // input columns of a block tile of the input gradient
 constexpr int kTileK = 64;   // inner elements of a step
 // 16-token tiles per wave of the 8-wave block tile: 1, 2 or 4
 inline int tile_mt(int64_t T, int most) {
@@ -52,21 +52,32 @@ inline int tile_mt(int64_t T, int most) {
     while (mt < most && 128 * mt < T) mt *= 2;
     return mt;
 }
+// Weight tiles (16 rows) per block: what the registers hold beside the inputs.
+constexpr int tile_nt(int mt) { return mt == 4 ? 6 : 8; }
 
 // Splits of the inner axis, so that the blocks fill the CUs: the count (at
-// most `most`) with the least work on the busiest CU, a split costing 1/16 of
-// the whole (its partial sums are written, read and joined).
-inline int inner_splits(int64_t blocks, int64_t steps, int most) {
+// most `most`) with the least estimated time.  A step of a block tile takes
+// about step_us; the splits' partial sums (part_bytes each) are written and
+// read back at about 4 TB/s by a further launch of 5 us.
+inline int inner_splits(int64_t blocks, int64_t steps, int most, double step_us,
+                        double part_bytes) {
     int best = 1;
     double cost = 1e30;
     for (int s = 1; s <= most && (s == 1 || steps / s >= 4); ++s) {
-        const double c = (double)cdiv(blocks * s, kCUs) / s + (s > 1 ? 0.0625 * s : 0.0);
-        if (c < cost - 1e-9) {
+        const double c = (double)cdiv(blocks * s, kCUs) * (double)cdiv(steps, s) * step_us +
+                         (s > 1 ? 5.0 + 2.0 * s * part_bytes / 4e6 : 0.0);
+        if (c < cost) {
             cost = c;
             best = s;
         }
     }
     return best;
+}
+
+// First group of split sp of a walk over G groups, which goes four at a time.
+__host__ __device__ inline int split_begin(int G, int sp, int splits) {
+    const int b = (int)((int64_t)((G + 3) / 4) * sp / splits) * 4;
+    return b < G ? b : G;
 }
 
 struct FfnPlan {
@@ -79,14 +90,15 @@ struct FfnPlan {
 inline FfnPlan ffn_plan(int64_t T, int64_t D, int64_t F, bool bf16) {
     FfnPlan p{};
     p.small = ffn_small(T, bf16);
-    p.planes = x_planes_needed(D, bf16);
+    p.planes = !p.small || !bf16 || D % kGroup != 0;
     p.splits = 1;
     if (!p.small) {
         p.mt = tile_mt(T, bf16 ? 4 : 2);
-        p.splits = inner_splits(cdiv(T, 128 * p.mt) * cdiv(F, kTileN / 2), cdiv(D, kGroup), 8);
+        p.splits = inner_splits(cdiv(T, 128 * p.mt) * cdiv(F, 8 * tile_nt(p.mt)), cdiv(D, kGroup),
+                                8, 0.35 * p.mt * (bf16 ? 1 : 3), 2.0 * T * F * 4);
     }
     p.planes_off = 0;
-    p.part_off = p.planes ? x_planes_bytes(T, D, bf16) : 0;
+    p.part_off = p.planes ? x_planes_bytes(T, D, bf16, !p.small) : 0;
     p.bytes = p.part_off + (p.splits > 1 ? sect(p.splits * 2 * T * F * 4) : 0);
     return p;
 }
@@ -102,9 +114,9 @@ struct FfnArgs {
     float* pre;  // [2][T][F] or null
 };
 hipError_t launch_ffn_gated(const FfnArgs& a, void* workspace, hipStream_t s);
-// X [T x D] -> padded bf16 planes (ffn.hip); also the scales' gradient's input.
-hipError_t launch_x_planes(const void* X, bool bf16, int64_t T, int64_t D, uint16_t* planes,
-                           hipStream_t s);
+// X [T x D] -> padded bf16 planes, rows or operand blocks (ffn.hip).
+hipError_t launch_x_planes(const void* X, bool bf16, bool blocked, int64_t T, int64_t D,
+                           uint16_t* planes, hipStream_t s);
 
 // ----------------------------------------------------------- backward pass
 // dX = sum over the matrices of dY_m W_m; dscales of each matrix.  The
@@ -125,10 +137,9 @@ struct BwdArgs {
     int accumulate;
 };
 struct BwdPlan {
-    bool planes;
     int dx_mt, dx_splits;
     int ds_mt, ds_tb, ds_splits;  // token tiles per wave, token blocks, splits of the groups
-    int64_t grad_off, dxpart_off, planes_off, dspart_off, bytes;
+    int64_t grad_off, unscale_off, dxpart_off, planes_off, dspart_off, bytes;
 };
 inline BwdPlan bwd_plan(int64_t T, int64_t I, int64_t O, int nmat, bool bf16, bool want_dx,
                         bool want_ds) {
@@ -137,22 +148,24 @@ inline BwdPlan bwd_plan(int64_t T, int64_t I, int64_t O, int nmat, bool bf16, bo
     int64_t off = 0;
     p.dx_splits = 1;
     if (want_dx) {
-        const int64_t K = nmat * pad_to(O, kTileK);
+        const int64_t K = nmat * pad_to(O, 2 * kTileK);
         p.dx_mt = tile_mt(T, bf16 ? 4 : 2);
-        p.dx_splits = inner_splits(cdiv(T, 128 * p.dx_mt) * cdiv(I, kTileN), K / kTileK, 16);
+        p.dx_splits = inner_splits(cdiv(T, 128 * p.dx_mt) * cdiv(I, kTileN), K / kTileK, 16,
+                                   (bf16 ? 0.35 : 3.0) * p.dx_mt, 1.0 * T * I * 4);
         p.grad_off = off;
-        off += sect(T * K * (bf16 ? 2 : 4));
+        off += sect(pad_to(T, 16) * K * (bf16 ? 2 : 4));
+        p.unscale_off = off;
+        off += sect((T + 64) * 4);  // the tokens' factors and 64 partial maxima
         p.dxpart_off = off;
         off += p.dx_splits > 1 ? sect(p.dx_splits * T * I * 4) : 0;
     }
     if (want_ds) {
-        p.planes = x_planes_needed(I, bf16);
         p.planes_off = off;
-        off += p.planes ? x_planes_bytes(T, I, bf16) : 0;
+        off += x_planes_bytes(T, I, bf16, true);
         p.ds_mt = tile_mt(T, bf16 ? 4 : 2);
         p.ds_tb = (int)cdiv(T, 128 * p.ds_mt);
         // the groups split freely: every block writes its own groups' sums
-        const int64_t blocks = nmat * cdiv(O, kTileN) * p.ds_tb;
+        const int64_t blocks = nmat * cdiv(O, 16 * tile_nt(p.ds_mt)) * p.ds_tb;
         p.ds_splits = 1;
         while (p.ds_splits < 16 && blocks * p.ds_splits < kCUs && G / (2 * p.ds_splits) >= 4)
             p.ds_splits *= 2;

@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "tune.h"
+
 namespace qt {
 namespace {
 
@@ -126,41 +128,52 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
     return __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)a, (__bf16)b});
 }
 
-// The same codes times the group's scale s, each product rounded once to
-// bf16.  int3 has eight possible products per group: bf16(s), bf16(2s),
-// bf16(3s), bf16(4s) and their negatives, whose high and low bytes make two
-// byte tables.
-__device__ __forceinline__ void scaled_quarter(const Quarter& qd, int q, int bits, float s,
-                                               u32x4_t& lo8, u32x4_t& hi8) {
+// The same codes times s in f16.  int3: a byte table gives f16(v), whose low
+// byte is zero, and a packed product multiplies two codes by f16(s).  int4: the
+// f16 word 0x6400 | u is 1024 + u and 0x5400 | u at bits 4..7 is 64 + u, both
+// exact, and a packed subtraction leaves v = u - 8.  Two roundings of 2^-12.
+__device__ __forceinline__ void scaled_quarter_f16(const Quarter& qd, int q, int bits, float s,
+                                                   u32x4_t& lo8, u32x4_t& hi8) {
+    typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+    const h2 s2 = {(_Float16)s, (_Float16)s};
+    auto mul = [&](uint32_t pair) {
+        return __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, pair) * s2);
+    };
     if (bits == 3) {
         uint32_t w[4];
         unpack_i3(qd.a, qd.b, high_sel(q), w);
-        const uint32_t p12 = bf16_pair(s, 2.0f * s), p34 = bf16_pair(3.0f * s, 4.0f * s);
-        // entries u = 0..3 are -4s -3s -2s -s, u = 4..7 are 0 s 2s 3s
-        const uint32_t lo_n = __builtin_amdgcn_perm(p34, p12, 0x00020406u);
-        const uint32_t hi_n = __builtin_amdgcn_perm(p34, p12, 0x01030507u) ^ 0x80808080u;
-        const uint32_t lo_p = __builtin_amdgcn_perm(p34, p12, 0x0402000Cu);
-        const uint32_t hi_p = __builtin_amdgcn_perm(p34, p12, 0x0503010Cu);
-        uint32_t d[4][2];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t hi = __builtin_amdgcn_perm(hi_p, hi_n, w[i]);
-            const uint32_t lo = __builtin_amdgcn_perm(lo_p, lo_n, w[i]);
-            d[i][0] = __builtin_amdgcn_perm(hi, lo, 0x05010400u);
-            d[i][1] = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
+            // high bytes of f16(v), u = 0..3: c4 c2 c0 bc, u = 4..7: 00 3c 40 42
+            const uint32_t hb = __builtin_amdgcn_perm(0x42403C00u, 0xBCC0C2C4u, w[i]);
+            w[i] = hb;
         }
-        lo8 = u32x4_t{d[0][0], d[1][0], d[0][1], d[1][1]};
-        hi8 = u32x4_t{d[2][0], d[3][0], d[2][1], d[3][1]};
+        auto lo = [&](uint32_t hb) { return mul(__builtin_amdgcn_perm(hb, hb, 0x010C000Cu)); };
+        auto hi = [&](uint32_t hb) { return mul(__builtin_amdgcn_perm(hb, hb, 0x030C020Cu)); };
+        lo8 = u32x4_t{lo(w[0]), lo(w[1]), hi(w[0]), hi(w[1])};
+        hi8 = u32x4_t{lo(w[2]), lo(w[3]), hi(w[2]), hi(w[3])};
     } else {
-        float a[8], b[8];
-        unpack_i4(qd.a, a);
-        unpack_i4(qd.b, b);
-        const float s16 = 16.0f * s;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            lo8[i] = bf16_pair(a[2 * i] * s16, a[2 * i + 1] * s16);
-            hi8[i] = bf16_pair(b[2 * i] * s16, b[2 * i + 1] * s16);
-        }
+        const h2 lo_off = {(_Float16)1032.0f, (_Float16)1032.0f};
+        const h2 hi_off = {(_Float16)72.0f, (_Float16)72.0f};
+        auto word = [&](uint32_t W, u32x4_t& o) {
+            // nibbles n of the word in pairs (n, n + 4): 04 15 26 37
+            const uint32_t W8 = W >> 8;
+            uint32_t p[4];
+            p[0] = __builtin_bit_cast(
+                uint32_t, (__builtin_bit_cast(h2, (W & 0x000F000Fu) | 0x64006400u) - lo_off) * s2);
+            p[1] = __builtin_bit_cast(
+                uint32_t, (__builtin_bit_cast(h2, (W & 0x00F000F0u) | 0x54005400u) - hi_off) * s2);
+            p[2] = __builtin_bit_cast(
+                uint32_t, (__builtin_bit_cast(h2, (W8 & 0x000F000Fu) | 0x64006400u) - lo_off) * s2);
+            p[3] = __builtin_bit_cast(
+                uint32_t, (__builtin_bit_cast(h2, (W8 & 0x00F000F0u) | 0x54005400u) - hi_off) * s2);
+            o = u32x4_t{__builtin_amdgcn_perm(p[1], p[0], 0x05040100u),
+                        __builtin_amdgcn_perm(p[3], p[2], 0x05040100u),
+                        __builtin_amdgcn_perm(p[1], p[0], 0x07060302u),
+                        __builtin_amdgcn_perm(p[3], p[2], 0x07060302u)};
+        };
+        word(qd.a, lo8);
+        word(qd.b, hi8);
     }
 }
 
@@ -214,6 +227,138 @@ __device__ __forceinline__ void transpose_rows(uint32_t (&v)[4]) {
     v[1] = c[1];
     v[2] = d[0];
     v[3] = d[1];
+}
+
+template <bool STREAM, typename T>
+__device__ __forceinline__ T load_stream(const T* p) {
+    if constexpr (STREAM) return __builtin_nontemporal_load(p);
+    else return *p;
+}
+
+// One lane's whole group of a row.  Where the four lane rows of a wave hold
+// four consecutive groups of the same 16 matrix rows, quarters() exchanges
+// them: lane row h gets quarter h of all four groups.
+// STREAM: the weights are read once per call (non-temporal loads).
+template <int BITS, bool STREAM>
+struct RowGroup;
+template <bool STREAM>
+struct RowGroup<3, STREAM> {
+    u32x2_t w[3];
+    __device__ __forceinline__ void load(const uint8_t* __restrict__ p) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            w[i] = load_stream<STREAM>(reinterpret_cast<const u32x2_t*>(p) + i);
+    }
+    __device__ __forceinline__ void quarters(Quarter (&q)[4]) const {
+        uint32_t a[4] = {w[0].x, w[0].y, w[1].x, w[1].y};
+        uint32_t b[4] = {w[2].x, w[2].x, w[2].y, w[2].y};
+        transpose_rows(a);
+        transpose_rows(b);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = Quarter{a[j], b[j]};
+    }
+};
+template <bool STREAM>
+struct RowGroup<4, STREAM> {
+    u32x4_t w[2];
+    __device__ __forceinline__ void load(const uint8_t* __restrict__ p) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            w[i] = load_stream<STREAM>(reinterpret_cast<const u32x4_t*>(p) + i);
+    }
+    __device__ __forceinline__ void quarters(Quarter (&q)[4]) const {
+        uint32_t a[4] = {w[0].x, w[0].z, w[1].x, w[1].z};
+        uint32_t b[4] = {w[0].y, w[0].w, w[1].y, w[1].w};
+        transpose_rows(a);
+        transpose_rows(b);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = Quarter{a[j], b[j]};
+    }
+};
+
+// The weights of one 16-row tile for a walk over the groups, four at a time:
+// load(g) issues the loads of groups g .. g+3 (one per lane row; past the row
+// a valid group is read), take() exchanges what the last load brought, so that
+// word j of lane row h is quarter h of group g + j.  Lanes with `second` set
+// read the second matrix; B1 and B2 are the matrices' bits.
+template <int B1, int B2>
+struct RowFeed {
+    static constexpr int kBytes1 = B1 == 3 ? kGroupBytes : kGroupBytesI4;
+    static constexpr int kBytes2 = B2 == 3 ? kGroupBytes : kGroupBytesI4;
+    const uint8_t* p;
+    const float* s;
+    int G, h;
+    bool second, four;  // this lane's matrix; whether its groups are int4
+    RowGroup<B1, false> r;  // B1 == B2
+    u32x2_t w[4];           // else: both formats' groups in 8-byte pieces
+    float rs;
+    Quarter q[4];
+    uint32_t sc[4];
+
+    __device__ __forceinline__ void init(const QMat& a, const QMat& b, bool sec, int64_t row,
+                                         int G_, int h_) {
+        second = sec;
+        four = (sec ? B2 : B1) == 4;
+        G = G_;
+        h = h_;
+        p = sec ? b.packed + row * G * kBytes2 : a.packed + row * G * kBytes1;
+        s = (sec ? b.scales : a.scales) + row * G;
+    }
+    __device__ __forceinline__ void load(int g) {
+        const int64_t i = g + h < G ? g + h : G - 1;
+        if constexpr (B1 == B2) {
+            r.load(p + i * kBytes1);
+        } else {
+            // no branch: an int3 group's fourth piece repeats its third
+            const u32x2_t* d =
+                reinterpret_cast<const u32x2_t*>(p + i * (second ? kBytes2 : kBytes1));
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                w[k] = d[k == 3 && !four ? 2 : k];
+        }
+        rs = s[i];
+    }
+    __device__ __forceinline__ void take() {
+        if constexpr (B1 == B2) {
+            r.quarters(q);
+        } else {
+            uint32_t a[4] = {w[0].x, four ? w[1].x : w[0].y, four ? w[2].x : w[1].x,
+                             four ? w[3].x : w[1].y};
+            uint32_t b[4] = {four ? w[0].y : w[2].x, four ? w[1].y : w[2].x,
+                             four ? w[2].y : w[2].y, four ? w[3].y : w[2].y};
+            transpose_rows(a);
+            transpose_rows(b);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) q[j] = Quarter{a[j], b[j]};
+        }
+        const float u = rs * (second ? code_unit(B2) : code_unit(B1));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sc[j] = __float_as_uint(u);
+        transpose_rows(sc);
+    }
+    __device__ __forceinline__ void exact(int j, int qn, u32x4_t& lo8, u32x4_t& hi8) const {
+        if constexpr (B1 == B2) {
+            exact_quarter(q[j], qn, B1, lo8, hi8);
+        } else {
+            u32x4_t l4, h4;
+            exact_quarter(q[j], qn, 3, lo8, hi8);
+            exact_quarter(q[j], qn, 4, l4, h4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                lo8[i] = four ? l4[i] : lo8[i];
+                hi8[i] = four ? h4[i] : hi8[i];
+            }
+        }
+    }
+    // the scale times what the exact operand's codes are multiplied by
+    __device__ __forceinline__ float scale(int j) const { return __uint_as_float(sc[j]); }
+};
+
+// Consecutive block ids run on different XCDs (8 of them, each with its own
+// L2): the ids are remapped so that every XCD takes a contiguous range.
+__device__ __forceinline__ int64_t xcd_range(int64_t lin, int64_t n) {
+    const int64_t x = lin & 7, q = n >> 3, r = n & 7;
+    return x * q + (x < r ? x : r) + (lin >> 3);
 }
 
 // ------------------------------------------------------------- activations
