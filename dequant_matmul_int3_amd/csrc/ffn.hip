@@ -90,17 +90,24 @@ __global__ __launch_bounds__(256) void planes_kernel(const void* __restrict__ X,
 struct SmallArgs {
     const uint8_t *gp, *up;
     const float *gs, *us;
-    int64_t F, G, ld;     // ld: row stride of A in elements
-    const uint16_t* A;    // [R] rows
-    int32_t R, T, act;
+    int64_t F, G, D;
+    const void* X;        // rows: bf16 rows of whole groups, 16-byte aligned; else [T x D]
+    int32_t R, T, act;    // R: rows of A, the pieces of the T tokens
     void* H;
     float* pre;
     int64_t pre_stride;   // T * F
 };
 
-template <int GB, int UB, int MT, bool BF16OUT>
+// Where the rows of A come from: bf16 rows in global memory, or LDS, where
+// every block copies the (few) tokens' values or pieces first.
+enum Rows { kGlobalRows, kStagedBf16, kStagedF32 };
+// LDS row of a staged row, in bf16 elements (16 bytes apart in the banks)
+__host__ __device__ inline int64_t staged_row(int64_t G) { return G * kGroup + 8; }
+
+template <int GB, int UB, int MT, Rows ROWS, bool BF16OUT>
 __global__ __launch_bounds__(1024) void ffn_small_kernel(const SmallArgs a) {
-    extern __shared__ __attribute__((aligned(16))) float red[];  // [W][2][MT][64] f32x4
+    // the staged rows, then [W][2][MT][64] f32x4 sums
+    extern __shared__ __attribute__((aligned(16))) float red[];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, W = blockDim.x >> 6;
     const int h4 = lane >> 4, l16 = lane & 15;
     const int64_t f0 = (int64_t)blockIdx.x * 16;
@@ -112,9 +119,16 @@ __global__ __launch_bounds__(1024) void ffn_small_kernel(const SmallArgs a) {
     const float* gs = a.gs + row * a.G;
     const float* us = a.us + row * a.G;
     const uint16_t* arow[MT];
+    uint16_t* stage = reinterpret_cast<uint16_t*>(red);
+    const int srow = (int)staged_row(a.G);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-        arow[mt] = a.A + (int64_t)std::min(16 * mt + l16, a.R - 1) * a.ld + 16 * h4;
+    for (int mt = 0; mt < MT; ++mt) {
+        const int64_t r = std::min(16 * mt + l16, a.R - 1);
+        if constexpr (ROWS == kGlobalRows)
+            arow[mt] = static_cast<const uint16_t*>(a.X) + r * a.G * kGroup + 16 * h4;
+        else
+            arow[mt] = stage + r * srow + 16 * h4;
+    }
 
     const int G = (int)a.G;
     const int nchunk = (G + 3) / 4;
@@ -126,10 +140,13 @@ __global__ __launch_bounds__(1024) void ffn_small_kernel(const SmallArgs a) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) acc[x][mt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
+    // rows in global memory are loaded with the weights of their chunk
+    constexpr bool AHEAD = ROWS == kGlobalRows && MT == 1;
     struct Chunk {
-        RowGroup<GB, true> g;
-        RowGroup<UB, true> u;
+        RowGroup<GB, false> g;
+        RowGroup<UB, false> u;
         float sg, su;
+        u32x4_t x[AHEAD ? 8 : 1];
     };
     // four groups of the lane's row, one per lane row; past the row a valid
     // group is read and not used
@@ -139,6 +156,15 @@ __global__ __launch_bounds__(1024) void ffn_small_kernel(const SmallArgs a) {
         k.u.load(up + (int64_t)g * UBY);
         k.sg = gs[g];
         k.su = us[g];
+        if constexpr (AHEAD) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const u32x4_t* p = reinterpret_cast<const u32x4_t*>(
+                    arow[0] + std::min(4 * c + j, G - 1) * kGroup);
+                k.x[2 * j] = p[0];
+                k.x[2 * j + 1] = p[1];
+            }
+        }
     };
     auto mul = [&](int c, const Chunk& k) {
         Quarter qg[4], qu[4];
@@ -160,10 +186,18 @@ __global__ __launch_bounds__(1024) void ffn_small_kernel(const SmallArgs a) {
                 exact_quarter(qu[j], h4, UB, wl[1], wh[1]);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
-                    const u32x4_t* ap =
-                        reinterpret_cast<const u32x4_t*>(arow[mt] + (int64_t)(4 * c + j) * kGroup);
-                    const bf16x8_t alo = __builtin_bit_cast(bf16x8_t, ap[0]);
-                    const bf16x8_t ahi = __builtin_bit_cast(bf16x8_t, ap[1]);
+                    u32x4_t x0, x1;
+                    if constexpr (AHEAD) {
+                        x0 = k.x[2 * j];
+                        x1 = k.x[2 * j + 1];
+                    } else {
+                        const u32x4_t* p =
+                            reinterpret_cast<const u32x4_t*>(arow[mt] + (4 * c + j) * kGroup);
+                        x0 = p[0];
+                        x1 = p[1];
+                    }
+                    const bf16x8_t alo = __builtin_bit_cast(bf16x8_t, x0);
+                    const bf16x8_t ahi = __builtin_bit_cast(bf16x8_t, x1);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         f32x4_t p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
@@ -180,9 +214,30 @@ __global__ __launch_bounds__(1024) void ffn_small_kernel(const SmallArgs a) {
             }
         }
     };
+    Chunk k0, k1;
+    if (c0 < c1) load(c0, k0);
+    if constexpr (ROWS != kGlobalRows) {
+        // the first chunk's weights are in flight meanwhile
+        const int Dp = G * kGroup;
+        for (int i = tid; i < a.T * Dp; i += blockDim.x) {
+            const int t = i / Dp, d = i - t * Dp;
+            const bool in = d < a.D;
+            const int64_t at = in ? (int64_t)t * a.D + d : 0;
+            if constexpr (ROWS == kStagedBf16) {
+                const uint16_t v = static_cast<const uint16_t*>(a.X)[at];
+                stage[t * srow + d] = in ? v : (uint16_t)0;
+            } else {
+                const float v = static_cast<const float*>(a.X)[at];
+                uint32_t h, m, l;
+                split3(in ? v : 0.0f, h, m, l);
+                stage[t * srow + d] = (uint16_t)h;
+                stage[(a.T + t) * srow + d] = (uint16_t)m;
+                stage[(2 * a.T + t) * srow + d] = (uint16_t)l;
+            }
+        }
+        __syncthreads();
+    }
     if (c0 < c1) {
-        Chunk k0, k1;
-        load(c0, k0);
         for (int c = c0; c < c1; c += 2) {
             load(std::min(c + 1, c1 - 1), k1);
             mul(c, k0);
@@ -191,6 +246,7 @@ __global__ __launch_bounds__(1024) void ffn_small_kernel(const SmallArgs a) {
             mul(c + 1, k1);
         }
     }
+    if constexpr (ROWS != kGlobalRows) __syncthreads();  // the sums take the rows' place
     // the waves' sums in wave order, then rows [m][16] of both projections
     f32x4_t* r4 = reinterpret_cast<f32x4_t*>(red);
 #pragma unroll
@@ -231,8 +287,8 @@ __global__ __launch_bounds__(1024) void ffn_small_kernel(const SmallArgs a) {
     }
 }
 
-template <int GB, int UB, int MT>
-hipError_t run_small(const SmallArgs& a, bool bf16, hipStream_t s) {
+template <int GB, int UB, int MT, Rows ROWS, bool BF16OUT>
+hipError_t run_small(const SmallArgs& a, hipStream_t s) {
     const int64_t blocks = cdiv(a.F, 16);
     // waves per block: enough that a CU holds about 16 of them, no more than
     // there are chunks of four groups, and what the sums' LDS allows
@@ -240,23 +296,27 @@ hipError_t run_small(const SmallArgs& a, bool bf16, hipStream_t s) {
     int W = 4;
     while (W < 16 && blocks * W < 16 * kCUs) W *= 2;
     W = std::min(W, most);
-    const size_t lds = (size_t)W * 2 * MT * 64 * 16;
-    if (bf16)
-        hipLaunchKernelGGL((ffn_small_kernel<GB, UB, MT, true>), dim3((unsigned)blocks),
-                           dim3(64 * W), lds, s, a);
-    else
-        hipLaunchKernelGGL((ffn_small_kernel<GB, UB, MT, false>), dim3((unsigned)blocks),
-                           dim3(64 * W), lds, s, a);
+    size_t lds = (size_t)W * 2 * MT * 64 * 16;
+    if (ROWS != kGlobalRows) lds = std::max(lds, (size_t)(a.R * staged_row(a.G) * 2));
+    hipLaunchKernelGGL((ffn_small_kernel<GB, UB, MT, ROWS, BF16OUT>), dim3((unsigned)blocks),
+                       dim3(64 * W), lds, s, a);
     return hipGetLastError();
 }
 
 template <int GB, int UB>
-hipError_t small_mt(const SmallArgs& a, bool bf16, hipStream_t s) {
+hipError_t small_bits(const SmallArgs& a, bool bf16, bool staged, hipStream_t s) {
+    if (staged)
+        return bf16 ? run_small<GB, UB, 1, kStagedBf16, true>(a, s)
+                    : run_small<GB, UB, 1, kStagedF32, false>(a, s);
     const int mt = (a.R + 15) / 16;
-    if (mt == 1) return run_small<GB, UB, 1>(a, bf16, s);
-    if (mt == 2) return run_small<GB, UB, 2>(a, bf16, s);
-    if (mt == 3) return run_small<GB, UB, 3>(a, bf16, s);
-    return run_small<GB, UB, 4>(a, bf16, s);
+#define QT_SMALL(M)                                                   \
+    return bf16 ? run_small<GB, UB, M, kGlobalRows, true>(a, s)       \
+                : run_small<GB, UB, M, kGlobalRows, false>(a, s)
+    if (mt == 1) QT_SMALL(1);
+    if (mt == 2) QT_SMALL(2);
+    if (mt == 3) QT_SMALL(3);
+    QT_SMALL(4);
+#undef QT_SMALL
 }
 
 // ---------------------------------------------------------------- tile form
@@ -558,11 +618,13 @@ hipError_t launch_ffn_gated(const FfnArgs& a, void* workspace, hipStream_t s) {
         A = planes;
     }
     if (p.small) {
-        const SmallArgs sa{a.gate.packed, a.up.packed, a.gate.scales, a.up.scales, a.F, G, Dp, A,
+        const SmallArgs sa{a.gate.packed, a.up.packed, a.gate.scales, a.up.scales, a.F, G, a.D, A,
                            (int32_t)(np * a.T), (int32_t)a.T, a.act, a.H, a.pre, a.T * a.F};
         if (a.gate.bits == 3)
-            return a.up.bits == 3 ? small_mt<3, 3>(sa, a.bf16, s) : small_mt<3, 4>(sa, a.bf16, s);
-        return a.up.bits == 3 ? small_mt<4, 3>(sa, a.bf16, s) : small_mt<4, 4>(sa, a.bf16, s);
+            return a.up.bits == 3 ? small_bits<3, 3>(sa, a.bf16, p.staged, s)
+                                  : small_bits<3, 4>(sa, a.bf16, p.staged, s);
+        return a.up.bits == 3 ? small_bits<4, 3>(sa, a.bf16, p.staged, s)
+                              : small_bits<4, 4>(sa, a.bf16, p.staged, s);
     }
     TileArgs ta{a.gate, a.up, a.F, G, A, a.T, a.act, p.splits, cdiv(a.T, 128 * p.mt),
                 cdiv(a.F, 8 * tile_nt(p.mt)), a.H, a.pre,

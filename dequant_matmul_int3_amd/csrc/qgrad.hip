@@ -14,8 +14,8 @@
 //   bf16: both operands are rounded to f16, whose eight times finer step keeps
 //   the result within its own bf16 rounding (operands in bf16 left it 1.7 times
 //   as far off).  Exact powers of two bring them into f16's range and are taken
-//   back from the sums: every token's dY is scaled by its largest magnitude to
-//   2^14 .. 2^15, the scales of both matrices by the largest of them to 2^11 ..
+//   back from the sums: every token's dY is scaled by (a bound of) its largest magnitude
+//   to 2^14 .. 2^15, the scales of both matrices by the largest of them to 2^11 ..
 //   2^12.  Values within 2^26 of those largest ones keep all 11 bits, smaller
 //   ones an absolute error of 2^-39 of them.  The operands come out of LDS
 //   through the transposing reads of gfx950, four rows of 16 columns at a
@@ -57,24 +57,17 @@ __device__ __forceinline__ float load_dy(const GradSrc& s, int64_t at) {
         return __uint_as_float((uint32_t) static_cast<const uint16_t*>(s.dY)[at] << 16);
     return static_cast<const float*>(s.dY)[at];
 }
-// dY_m[t, o]
-__device__ __forceinline__ float grad_at(const GradSrc& s, int m, int64_t t, int64_t o) {
-    const int64_t at = t * s.O + o;
-    const float d = load_dy(s, at);
-    if (s.nmat == 1) return d;
-    float dg, du;
-    act_grads(s.pre[at], s.pre[s.T * s.O + at], d, s.act, dg, du);
-    return m == 0 ? dg : du;
-}
-
 // ----------------------------------------------------------- gradient plane
 // Operand blocks [T16][K / 32][16 tokens][32], K = nmat Op, matrix m at inner
 // elements m Op .., zero past O.  bf16 calls: f16 times the token's power of
 // two, position 8h + e of a block is row 4h + (e & 3) + 16 (e >> 2); f32 calls:
-// f32 in order.  Block t < T writes token t; blocks past T leave the largest
-// magnitude of their part of the scales (bf16 calls).
+// f32 in order.  A block writes kPlaneTok tokens, whose rows lie next to each
+// other in the blocks (one token's 64 bytes at a time left lines half written);
+// kMaxParts further blocks leave the largest magnitude of their part of the
+// scales (bf16 calls).
 constexpr int kMaxParts = 64;
 constexpr int kPlaneThreads = 256;
+constexpr int kPlaneTok = 4;
 
 __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
@@ -100,34 +93,38 @@ __global__ __launch_bounds__(kPlaneThreads) void grad_plane_kernel(
     const GradSrc src, int64_t Op, void* __restrict__ P, float* __restrict__ unscale,
     const float* __restrict__ s0, const float* __restrict__ s1, int64_t nscales,
     float* __restrict__ smax) {
-    __shared__ float wm[kPlaneThreads / 64];
+    __shared__ float wm[kPlaneThreads / 64][kPlaneTok];
     const int tid = threadIdx.x;
-    auto block_max = [&](float m) {
-        m = wave_max(m);
-        if ((tid & 63) == 0) wm[tid >> 6] = m;
-        __syncthreads();
-        m = wm[0];
-#pragma unroll
-        for (int w = 1; w < kPlaneThreads / 64; ++w) m = fmaxf(m, wm[w]);
-        return m;
-    };
-    const int64_t t = blockIdx.x;
-    if (!F32 && t >= src.T) {
-        const int part = (int)(t - src.T);
+    const int64_t tblocks = (src.T + kPlaneTok - 1) / kPlaneTok;
+    if (!F32 && blockIdx.x >= tblocks) {
+        const int part = (int)(blockIdx.x - tblocks);
         float m = 0.0f;
         for (int64_t i = (int64_t)part * kPlaneThreads + tid; i < nscales;
              i += kMaxParts * kPlaneThreads)
             m = fmaxf(m, fmaxf(fabsf(s0[i]), s1 ? fabsf(s1[i]) : 0.0f));
-        m = block_max(m);
-        if (tid == 0) smax[part] = m;
+        m = wave_max(m);
+        if ((tid & 63) == 0) wm[tid >> 6][0] = m;
+        __syncthreads();
+        if (tid == 0) {
+#pragma unroll
+            for (int w = 1; w < kPlaneThreads / 64; ++w) m = fmaxf(m, wm[w][0]);
+            smax[part] = m;
+        }
         return;
     }
+    // four threads take a token's 32 inner elements, the next four the next
+    // token's; tokens past T read a valid one and write nothing
+    const int tk = (tid >> 2) % kPlaneTok;
+    const int64_t c0 = tid / (4 * kPlaneTok) * 4 + (tid & 3);
+    constexpr int kStep = kPlaneThreads / kPlaneTok;
+    const int64_t tw = (int64_t)blockIdx.x * kPlaneTok + tk;
+    const bool live = tw < src.T;
+    const int64_t t = live ? tw : src.T - 1;
     const int64_t per = Op / 8;
-    // the eight gradients of chunk c, of both matrices
-    auto chunk = [&](int64_t c, float (&v)[2][8]) {
+    // what the eight gradients of chunk c are formed from, zero past O
+    auto fetch = [&](int64_t c, float (&d)[8], float (&g)[8], float (&u)[8]) {
         const int64_t p0 = c * 8;
         const int64_t o0 = F32 ? p0 : (p0 & ~31LL) + ((p0 & 31) >> 1);
-        float d[8], g[8], u[8];
         auto get4 = [&](int k, int64_t o) {  // elements k .. k+3 from row o
             const int64_t at = t * src.O + o;
             if (o + 4 <= src.O) {
@@ -166,6 +163,37 @@ __global__ __launch_bounds__(kPlaneThreads) void grad_plane_kernel(
         };
         get4(0, o0);
         get4(4, o0 + (F32 ? 4 : 16));
+    };
+    // The factor comes from a bound of the gradients (|act'| <= 1.13, |act(g)|
+    // <= |g| + 0.3), which costs no exponential.
+    float f = 1.0f;
+    if constexpr (!F32) {
+        float m = 0.0f;
+        for (int64_t c = c0; c < per; c += kStep) {
+            float d[8], g[8], u[8];
+            fetch(c, d, g, u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                m = fmaxf(m, src.nmat == 1 ? fabsf(d[e])
+                                           : fabsf(d[e]) * fmaxf(1.13f * fabsf(u[e]),
+                                                                 fabsf(g[e]) + 0.3f));
+        }
+        // over the lanes of the token, then the waves
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1)
+            if (d < 4 || d >= 4 * kPlaneTok) m = fmaxf(m, __shfl_xor(m, d));
+        if ((tid & 63) < 4 * kPlaneTok && (tid & 3) == 0) wm[tid >> 6][tk] = m;
+        __syncthreads();
+        m = wm[0][tk];
+#pragma unroll
+        for (int w = 1; w < kPlaneThreads / 64; ++w) m = fmaxf(m, wm[w][tk]);
+        f = range_factor(m, 14);
+        if (tid < 4 * kPlaneTok && (tid & 3) == 0 && live) unscale[t] = 1.0f / f;
+    }
+    const int64_t row = (t >> 4) * (src.nmat * Op) * 16 + (t & 15) * 32;  // block 0, this token
+    for (int64_t c = c0; c < per; c += kStep) {
+        float d[8], g[8], u[8], v[2][8];
+        fetch(c, d, g, u);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             if (src.nmat == 1) {
@@ -175,24 +203,9 @@ __global__ __launch_bounds__(kPlaneThreads) void grad_plane_kernel(
                 act_grads(g[e], u[e], d[e], src.act, v[0][e], v[1][e]);
             }
         }
-    };
-    float f = 1.0f;
-    if constexpr (!F32) {
-        float m = 0.0f;
-        for (int64_t c = tid; c < per; c += kPlaneThreads) {
-            float v[2][8];
-            chunk(c, v);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(fabsf(v[0][e]), fabsf(v[1][e])));
-        }
-        f = range_factor(block_max(m), 14);
-        if (tid == 0) unscale[t] = 1.0f / f;
-    }
-    const int64_t row = (t >> 4) * (src.nmat * Op) * 16 + (t & 15) * 32;  // block 0, this token
-    for (int64_t c = tid; c < per; c += kPlaneThreads) {
-        float v[2][8];
-        chunk(c, v);
-        for (int m = 0; m < src.nmat; ++m) {
+        for (int m = 0; m < 2; ++m) {
+            if (m >= src.nmat || !live) break;
             const int64_t at = row + ((m * Op + c * 8) >> 5) * 512 + (c & 3) * 8;
             if constexpr (F32) {
                 f32x4_t* d = reinterpret_cast<f32x4_t*>(static_cast<float*>(P) + at);
@@ -534,17 +547,46 @@ __global__ __launch_bounds__(kThreads) void ds_tile_kernel(const DsArgs a, const
     };
 
     // dY of the tile, where the products will lie: register r of lane l is
-    // token 4 (l / 16) + r, row l % 16; zero past T and O
+    // token 4 (l / 16) + r, row l % 16; zero past T and O.  Loads without
+    // branches (past the ends a valid element), a token tile's all in flight.
     f32x4_t dy[MT][NT];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int mt = 0; mt < MT; ++mt) {
+        auto each = [&](auto load) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int64_t t = t0 + mt * 16 + 4 * h4 + r, o = o0 + nt * 16 + l16;
-                dy[mt][nt][r] = t < T && o < O ? grad_at(a.src, m, t, o) * code_unit(BITS) : 0.0f;
-            }
+                for (int r = 0; r < 4; ++r) {
+                    const int64_t t = t0 + mt * 16 + 4 * h4 + r, o = o0 + nt * 16 + l16;
+                    load(nt, r, std::min(t, T - 1) * O + std::min(o, O - 1), t < T && o < O);
+                }
+        };
+        float d[NT][4];
+        if (a.src.dy_bf16)
+            each([&](int nt, int r, int64_t at, bool) {
+                d[nt][r] = __uint_as_float(
+                    (uint32_t) static_cast<const uint16_t*>(a.src.dY)[at] << 16);
+            });
+        else
+            each([&](int nt, int r, int64_t at, bool) {
+                d[nt][r] = static_cast<const float*>(a.src.dY)[at];
+            });
+        if (a.src.nmat == 2) {
+            float g[NT][4], u[NT][4];
+            each([&](int nt, int r, int64_t at, bool) {
+                g[nt][r] = a.src.pre[at];
+                u[nt][r] = a.src.pre[T * O + at];
+            });
+            each([&](int nt, int r, int64_t, bool) {
+                float dg, du;
+                act_grads(g[nt][r], u[nt][r], d[nt][r], a.src.act, dg, du);
+                d[nt][r] = m == 0 ? dg : du;
+            });
+        }
+        each([&](int nt, int r, int64_t, bool in) {
+            dy[mt][nt][r] = in ? d[nt][r] * code_unit(BITS) : 0.0f;
+        });
+    }
 
     // the tile's sums of one group, per wave over its tokens, and the
     // unpacking of word j of the feed (ordered as in the forward tile)
@@ -708,12 +750,12 @@ hipError_t launch_bwd(const BwdArgs& a, void* workspace, hipStream_t s) {
         float* smax = unscale + a.T;
         const float* s1 = a.nmat == 2 ? a.mat[1].scales : nullptr;
         if (a.bf16)
-            hipLaunchKernelGGL((grad_plane_kernel<false>), dim3((unsigned)(a.T + kMaxParts)),
+            hipLaunchKernelGGL((grad_plane_kernel<false>), dim3((unsigned)(cdiv(a.T, kPlaneTok) + kMaxParts)),
                                dim3(kPlaneThreads), 0, s, src, Op, A, unscale, a.mat[0].scales, s1,
                                a.O * G, smax);
         else
-            hipLaunchKernelGGL((grad_plane_kernel<true>), dim3((unsigned)a.T), dim3(kPlaneThreads),
-                               0, s, src, Op, A, nullptr, nullptr, nullptr, 0, nullptr);
+            hipLaunchKernelGGL((grad_plane_kernel<true>), dim3((unsigned)cdiv(a.T, kPlaneTok)),
+                               dim3(kPlaneThreads), 0, s, src, Op, A, nullptr, nullptr, nullptr, 0, nullptr);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
         const DxArgs d{{a.mat[0], a.mat[1]}, a.O, Op, a.I, G, a.T, a.nmat * Op, A, unscale, smax,

@@ -82,7 +82,8 @@ __host__ __device__ inline int split_begin(int G, int sp, int splits) {
 
 struct FfnPlan {
     bool small;
-    bool planes;       // X is copied into padded planes first
+    bool staged;       // small form: every block copies the rows into LDS
+    bool planes;       // X is copied into planes by a launch of its own first
     int mt;            // tile form: 16-token tiles per wave
     int splits;        // tile form: splits of the groups
     int64_t planes_off, part_off, bytes;
@@ -90,7 +91,10 @@ struct FfnPlan {
 inline FfnPlan ffn_plan(int64_t T, int64_t D, int64_t F, bool bf16) {
     FfnPlan p{};
     p.small = ffn_small(T, bf16);
-    p.planes = !p.small || !bf16 || D % kGroup != 0;
+    // a few rows go through LDS, 16 rows and 48 KB at most (three blocks a CU)
+    const int64_t rows = T * ffn_pieces(bf16);
+    p.staged = p.small && rows <= 16 && rows * (pad_to(D, kGroup) + 8) * 2 <= 48 * 1024;
+    p.planes = !p.staged && (!p.small || !bf16 || D % kGroup != 0);
     p.splits = 1;
     if (!p.small) {
         p.mt = tile_mt(T, bf16 ? 4 : 2);
@@ -165,7 +169,7 @@ inline BwdPlan bwd_plan(int64_t T, int64_t I, int64_t O, int nmat, bool bf16, bo
         p.ds_mt = tile_mt(T, bf16 ? 4 : 2);
         p.ds_tb = (int)cdiv(T, 128 * p.ds_mt);
         // the groups split freely: every block writes its own groups' sums
-        const int64_t blocks = nmat * cdiv(O, 16 * tile_nt(p.ds_mt)) * p.ds_tb;
+        const int64_t blocks = cdiv(O, 16 * tile_nt(p.ds_mt)) * p.ds_tb;  // of one launch
         p.ds_splits = 1;
         while (p.ds_splits < 16 && blocks * p.ds_splits < kCUs && G / (2 * p.ds_splits) >= 4)
             p.ds_splits *= 2;
