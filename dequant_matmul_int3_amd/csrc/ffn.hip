@@ -132,7 +132,6 @@ __global__ __launch_bounds__(1024) void ffn_small_kernel(const SmallArgs a) {
 
     const int G = (int)a.G;
     const int nchunk = (G + 3) / 4;
-    const int c0 = (int)((int64_t)wave * nchunk / W), c1 = (int)((int64_t)(wave + 1) * nchunk / W);
 
     f32x4_t acc[2][MT];
 #pragma unroll
@@ -140,13 +139,10 @@ __global__ __launch_bounds__(1024) void ffn_small_kernel(const SmallArgs a) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) acc[x][mt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-    // rows in global memory are loaded with the weights of their chunk
-    constexpr bool AHEAD = ROWS == kGlobalRows && MT == 1;
     struct Chunk {
         RowGroup<GB, false> g;
         RowGroup<UB, false> u;
         float sg, su;
-        u32x4_t x[AHEAD ? 8 : 1];
     };
     // four groups of the lane's row, one per lane row; past the row a valid
     // group is read and not used
@@ -156,15 +152,6 @@ __global__ __launch_bounds__(1024) void ffn_small_kernel(const SmallArgs a) {
         k.u.load(up + (int64_t)g * UBY);
         k.sg = gs[g];
         k.su = us[g];
-        if constexpr (AHEAD) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const u32x4_t* p = reinterpret_cast<const u32x4_t*>(
-                    arow[0] + std::min(4 * c + j, G - 1) * kGroup);
-                k.x[2 * j] = p[0];
-                k.x[2 * j + 1] = p[1];
-            }
-        }
     };
     auto mul = [&](int c, const Chunk& k) {
         Quarter qg[4], qu[4];
@@ -173,78 +160,141 @@ __global__ __launch_bounds__(1024) void ffn_small_kernel(const SmallArgs a) {
         uint32_t sg[4], su[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            sg[j] = __float_as_uint(k.sg * code_unit(GB));
-            su[j] = __float_as_uint(k.su * code_unit(UB));
+            sg[j] = 4 * c + h4 < G ? __float_as_uint(k.sg * code_unit(GB)) : 0u;
+            su[j] = 4 * c + h4 < G ? __float_as_uint(k.su * code_unit(UB)) : 0u;
         }
         transpose_rows(sg);
         transpose_rows(su);
+        // the rows of group j + 1 are read while group j is multiplied; groups
+        // past the row read a valid one and have the scale 0
+        u32x4_t x[2][MT][2];
+        auto read_x = [&](int j) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                const u32x4_t* p = reinterpret_cast<const u32x4_t*>(
+                    arow[mt] + std::min(4 * c + j, G - 1) * kGroup);
+                x[j & 1][mt][0] = p[0];
+                x[j & 1][mt][1] = p[1];
+            }
+        };
+        read_x(0);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            if (4 * c + j < G) {  // uniform
+            if (j < 3) read_x(j + 1);
+            {
                 u32x4_t wl[2], wh[2];
                 exact_quarter(qg[j], h4, GB, wl[0], wh[0]);
                 exact_quarter(qu[j], h4, UB, wl[1], wh[1]);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
-                    u32x4_t x0, x1;
-                    if constexpr (AHEAD) {
-                        x0 = k.x[2 * j];
-                        x1 = k.x[2 * j + 1];
-                    } else {
-                        const u32x4_t* p =
-                            reinterpret_cast<const u32x4_t*>(arow[mt] + (4 * c + j) * kGroup);
-                        x0 = p[0];
-                        x1 = p[1];
-                    }
-                    const bf16x8_t alo = __builtin_bit_cast(bf16x8_t, x0);
-                    const bf16x8_t ahi = __builtin_bit_cast(bf16x8_t, x1);
+                    const bf16x8_t alo = __builtin_bit_cast(bf16x8_t, x[j & 1][mt][0]);
+                    const bf16x8_t ahi = __builtin_bit_cast(bf16x8_t, x[j & 1][mt][1]);
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
+                    for (int i = 0; i < 2; ++i) {
                         f32x4_t p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            alo, __builtin_bit_cast(bf16x8_t, wl[x]), f32x4_t{0.f, 0.f, 0.f, 0.f},
+                            alo, __builtin_bit_cast(bf16x8_t, wl[i]), f32x4_t{0.f, 0.f, 0.f, 0.f},
                             0, 0, 0);
                         p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            ahi, __builtin_bit_cast(bf16x8_t, wh[x]), p, 0, 0, 0);
-                        const float s = __uint_as_float(x == 0 ? sg[j] : su[j]);
+                            ahi, __builtin_bit_cast(bf16x8_t, wh[i]), p, 0, 0, 0);
+                        const float s = __uint_as_float(i == 0 ? sg[j] : su[j]);
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
-                            acc[x][mt][r] = __builtin_fmaf(s, p[r], acc[x][mt][r]);
+                            acc[i][mt][r] = __builtin_fmaf(s, p[r], acc[i][mt][r]);
                     }
                 }
             }
         }
     };
     Chunk k0, k1;
-    if (c0 < c1) load(c0, k0);
+    load(std::min(wave, nchunk - 1), k0);
     if constexpr (ROWS != kGlobalRows) {
         // the first chunk's weights are in flight meanwhile
-        const int Dp = G * kGroup;
-        for (int i = tid; i < a.T * Dp; i += blockDim.x) {
-            const int t = i / Dp, d = i - t * Dp;
-            const bool in = d < a.D;
-            const int64_t at = in ? (int64_t)t * a.D + d : 0;
-            if constexpr (ROWS == kStagedBf16) {
-                const uint16_t v = static_cast<const uint16_t*>(a.X)[at];
-                stage[t * srow + d] = in ? v : (uint16_t)0;
+        const int nv = G * kGroup / 8;  // eight values at a time
+        constexpr int ESZ = ROWS == kStagedBf16 ? 2 : 4, N4 = ESZ / 2;
+        const bool vec = a.D % 8 == 0 && (reinterpret_cast<uintptr_t>(a.X) & 15) == 0;
+        for (int t = 0; t < a.T; ++t) {
+            const char* x = static_cast<const char*>(a.X) + (int64_t)t * a.D * ESZ;
+            auto put = [&](int v, const u32x4_t* w) {
+                if constexpr (ROWS == kStagedBf16) {
+                    *reinterpret_cast<u32x4_t*>(stage + t * srow + 8 * v) = w[0];
+                } else {
+                    u32x4_t o[3];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t h[2], m[2], l[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            split3(__uint_as_float(w[e >> 1][2 * (e & 1) + i]), h[i], m[i], l[i]);
+                        o[0][e] = h[0] | h[1] << 16;
+                        o[1][e] = m[0] | m[1] << 16;
+                        o[2][e] = l[0] | l[1] << 16;
+                    }
+#pragma unroll
+                    for (int pc = 0; pc < 3; ++pc)
+                        *reinterpret_cast<u32x4_t*>(stage + (pc * a.T + t) * srow + 8 * v) = o[pc];
+                }
+            };
+            if (vec) {
+                // four pieces in flight; those past D read the row's first and
+                // become zero
+                for (int v0 = tid; v0 < nv; v0 += 4 * blockDim.x) {
+                    u32x4_t w[4][N4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int v = v0 + k * blockDim.x;
+                        const bool in = 8 * (int64_t)v < a.D;
+#pragma unroll
+                        for (int i = 0; i < N4; ++i)
+                            w[k][i] = *reinterpret_cast<const u32x4_t*>(
+                                x + (in ? (int64_t)v * 8 * ESZ : 0) + 16 * i);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int v = v0 + k * blockDim.x;
+                        if (8 * (int64_t)v >= a.D)
+#pragma unroll
+                            for (int i = 0; i < N4; ++i) w[k][i] = u32x4_t{0u, 0u, 0u, 0u};
+                        if (v < nv) put(v, w[k]);
+                    }
+                }
             } else {
-                const float v = static_cast<const float*>(a.X)[at];
-                uint32_t h, m, l;
-                split3(in ? v : 0.0f, h, m, l);
-                stage[t * srow + d] = (uint16_t)h;
-                stage[(a.T + t) * srow + d] = (uint16_t)m;
-                stage[(2 * a.T + t) * srow + d] = (uint16_t)l;
+                for (int v = tid; v < nv; v += blockDim.x) {
+                    uint32_t e[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int64_t d = std::min<int64_t>(8 * (int64_t)v + i, a.D - 1);
+                        if constexpr (ROWS == kStagedBf16)
+                            e[i] = reinterpret_cast<const uint16_t*>(x)[d];
+                        else
+                            e[i] = reinterpret_cast<const uint32_t*>(x)[d];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (8 * (int64_t)v + i >= a.D) e[i] = 0u;
+                    u32x4_t w[N4];
+                    if constexpr (ROWS == kStagedBf16) {
+                        w[0] = u32x4_t{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16,
+                                       e[6] | e[7] << 16};
+                    } else {
+                        w[0] = u32x4_t{e[0], e[1], e[2], e[3]};
+                        w[N4 - 1] = u32x4_t{e[4], e[5], e[6], e[7]};
+                    }
+                    put(v, w);
+                }
             }
         }
         __syncthreads();
     }
-    if (c0 < c1) {
-        for (int c = c0; c < c1; c += 2) {
-            load(std::min(c + 1, c1 - 1), k1);
-            mul(c, k0);
-            if (c + 1 >= c1) break;
-            load(std::min(c + 2, c1 - 1), k0);
-            mul(c + 1, k1);
-        }
+    // The waves take the chunks in turn, so that a block reads a row's bytes in
+    // order: a chunk of 96 bytes ends inside a line, and waves that each took a
+    // range of their own fetched most lines twice (for 12 tokens of
+    // 18432 x 7168 85 us against 56).
+    for (int c = wave; c < nchunk; c += 2 * W) {
+        load(std::min(c + W, nchunk - 1), k1);
+        mul(c, k0);
+        if (c + W >= nchunk) break;
+        load(std::min(c + 2 * W, nchunk - 1), k0);
+        mul(c + W, k1);
     }
     if constexpr (ROWS != kGlobalRows) __syncthreads();  // the sums take the rows' place
     // the waves' sums in wave order, then rows [m][16] of both projections
