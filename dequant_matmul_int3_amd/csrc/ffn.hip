@@ -404,8 +404,8 @@ __device__ __forceinline__ void store4(__bf16* p, const f32x4_t& v, int64_t left
     }
 }
 
-// NP pieces per input, MT 16-token tiles per wave, NT weight tiles per block;
-// a weight tile is 8 gate rows and 8 up rows of the same features.
+// NP pieces per input, MT 16-token tiles per wave, NT weight tiles (an
+// even number) per block; a weight tile is 8 gate rows and 8 up rows of the same features.
 template <int GB, int UB, int NP, int MT, int NT>
 __global__ __launch_bounds__(kThreads) void ffn_tile_kernel(const TileArgs a) {
     // eight weight tiles, one per wave, of which NT are used: every wave runs
@@ -619,19 +619,19 @@ __global__ __launch_bounds__(256) void ffn_join_kernel(const float* __restrict__
     else store4(static_cast<float*>(H) + i, h, left);
 }
 
-template <int GB, int UB, int NP, int MT>
+template <int GB, int UB, int NP, int MT, int NT>
 hipError_t run_tile(const TileArgs& a, hipStream_t s) {
     const int64_t nb = a.mblk * a.nblk * a.splits;
     if (nb > 0x7FFFFFFF) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((ffn_tile_kernel<GB, UB, NP, MT, tile_nt(MT)>), dim3((unsigned)nb),
+    hipLaunchKernelGGL((ffn_tile_kernel<GB, UB, NP, MT, NT>), dim3((unsigned)nb),
                        dim3(kThreads), 0, s, a);
     return hipGetLastError();
 }
-template <int NP, int MT>
+template <int NP, int MT, int NT>
 hipError_t tile_bits(const TileArgs& a, hipStream_t s) {
     if (a.gate.bits == 3)
-        return a.up.bits == 3 ? run_tile<3, 3, NP, MT>(a, s) : run_tile<3, 4, NP, MT>(a, s);
-    return a.up.bits == 3 ? run_tile<4, 3, NP, MT>(a, s) : run_tile<4, 4, NP, MT>(a, s);
+        return a.up.bits == 3 ? run_tile<3, 3, NP, MT, NT>(a, s) : run_tile<3, 4, NP, MT, NT>(a, s);
+    return a.up.bits == 3 ? run_tile<4, 3, NP, MT, NT>(a, s) : run_tile<4, 4, NP, MT, NT>(a, s);
 }
 
 }  // namespace
@@ -677,14 +677,15 @@ hipError_t launch_ffn_gated(const FfnArgs& a, void* workspace, hipStream_t s) {
                               : small_bits<4, 4>(sa, a.bf16, p.staged, s);
     }
     TileArgs ta{a.gate, a.up, a.F, G, A, a.T, a.act, p.splits, cdiv(a.T, 128 * p.mt),
-                cdiv(a.F, 8 * tile_nt(p.mt)), a.H, a.pre,
+                cdiv(a.F, 8 * p.nt), a.H, a.pre,
                 p.splits > 1 ? reinterpret_cast<float*>(w + p.part_off) : nullptr};
     hipError_t e;
     if (a.bf16)
-        e = p.mt == 1 ? tile_bits<1, 1>(ta, s) : p.mt == 2 ? tile_bits<1, 2>(ta, s)
-                                                           : tile_bits<1, 4>(ta, s);
+        e = p.mt == 1   ? tile_bits<1, 1, 8>(ta, s)
+            : p.mt == 2 ? tile_bits<1, 2, 8>(ta, s)
+                        : tile_bits<1, 4, 6>(ta, s);
     else
-        e = p.mt == 1 ? tile_bits<3, 1>(ta, s) : tile_bits<3, 2>(ta, s);
+        e = p.mt == 1 ? tile_bits<3, 1, 8>(ta, s) : tile_bits<3, 2, 8>(ta, s);
     if (e != hipSuccess || p.splits == 1) return e;
     const int64_t n = a.T * a.F, nb = cdiv(n, 1024);
     if (nb > 0x7FFFFFFF) return hipErrorInvalidValue;

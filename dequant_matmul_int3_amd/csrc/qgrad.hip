@@ -7,8 +7,9 @@
 // pre-activations g, u that the forward pass kept in f32.
 //
 // Input gradient.  A matrix product with the weights' rows as its inner axis:
-// a block of 8 waves owns 128 MT tokens x 128 inputs and walks the rows of
-// both matrices 64 at a time.  dY is first written as one padded plane in
+// a block of 8 waves owns 128 MT tokens x 128 inputs (MT 1 or 2: with 4 the
+// registers had no room for the weights' loads four steps ahead, 1.76 against
+// 1.54 ms) and walks the rows of both matrices 64 at a time.  dY is first written as one padded plane in
 // operand blocks; the weights are unpacked once per block into LDS row by row
 // and read back as matrix operands.
 //   bf16: both operands are rounded to f16, whose eight times finer step keeps
@@ -61,13 +62,13 @@ __device__ __forceinline__ float load_dy(const GradSrc& s, int64_t at) {
 // Operand blocks [T16][K / 32][16 tokens][32], K = nmat Op, matrix m at inner
 // elements m Op .., zero past O.  bf16 calls: f16 times the token's power of
 // two, position 8h + e of a block is row 4h + (e & 3) + 16 (e >> 2); f32 calls:
-// f32 in order.  A block writes kPlaneTok tokens, whose rows lie next to each
-// other in the blocks (one token's 64 bytes at a time left lines half written);
-// kMaxParts further blocks leave the largest magnitude of their part of the
-// scales (bf16 calls).
+// f32 in order.  A block writes TOK tokens, 256 threads each, whose rows lie next
+// to each other in the blocks: four from 1024 tokens on (one token's 64 bytes
+// leave lines half written: 0.39 against 0.45 ms for 4096 tokens of 2 x 17408,
+// 82 against 115 us for 1024 tokens of 50257), else one, for the sake of more
+// blocks (8 against 15 us for 200 tokens of 2 x 2048).  kMaxParts further
+// blocks leave the largest magnitude of their part of the scales (bf16 calls).
 constexpr int kMaxParts = 64;
-constexpr int kPlaneThreads = 256;
-constexpr int kPlaneTok = 4;
 
 __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
@@ -88,11 +89,12 @@ __device__ __forceinline__ uint32_t f16_pair(float a, float b) {
     return __builtin_bit_cast(uint32_t, f16x2_t{(_Float16)a, (_Float16)b});
 }
 
-template <bool F32>
-__global__ __launch_bounds__(kPlaneThreads) void grad_plane_kernel(
+template <bool F32, int TOK>
+__global__ __launch_bounds__(TOK * 256) void grad_plane_kernel(
     const GradSrc src, int64_t Op, void* __restrict__ P, float* __restrict__ unscale,
     const float* __restrict__ s0, const float* __restrict__ s1, int64_t nscales,
     float* __restrict__ smax) {
+    constexpr int kPlaneThreads = TOK * 256, kPlaneTok = TOK;
     __shared__ float wm[kPlaneThreads / 64][kPlaneTok];
     const int tid = threadIdx.x;
     const int64_t tblocks = (src.T + kPlaneTok - 1) / kPlaneTok;
@@ -249,9 +251,9 @@ __global__ __launch_bounds__(kThreads) void dx_tile_kernel(const DxArgs a) {
     const int64_t n = tile % a.nblk, mm = tile / a.nblk;
     const int64_t m0 = (mm % a.mblk) * (128 * MT);
     const int sp = (int)(mm / a.mblk);
-    const int steps = (int)(a.K / kTileK), half = (int)(a.Op / kTileK);  // both even
-    const int k0 = (int)((int64_t)(steps / 2) * sp / a.splits) * 2;
-    const int k1 = (int)((int64_t)(steps / 2) * (sp + 1) / a.splits) * 2;
+    const int steps = (int)(a.K / kTileK), half = (int)(a.Op / kTileK);  // multiples of 4
+    const int k0 = (int)((int64_t)(steps / 4) * sp / a.splits) * 4;
+    const int k1 = (int)((int64_t)(steps / 4) * (sp + 1) / a.splits) * 4;
 
     float sf = 1.0f;  // the scales' power of two
     if constexpr (!F32) sf = range_factor(wave_max(a.smax[lane]), 11);
@@ -397,24 +399,27 @@ __global__ __launch_bounds__(kThreads) void dx_tile_kernel(const DxArgs a) {
         }
     };
 
-    // weights two steps ahead in registers, dY one; past the last step of the
-    // plane the loads repeat it
+    // weights four steps ahead in registers (every step reads new rows: two
+    // steps ahead left a quarter of the time waiting for them), dY one; past
+    // the last step of the plane the loads repeat it
     In x0, x1;
-    Raw r0, r1;
-    load_raw(k0, r0);
+    Raw raw[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) load_raw(k0 + j, raw[j]);
     load_a(k0, x0);
-    load_raw(k0 + 1, r1);
-    unpack(0, k0, r0);
+    unpack(0, k0, raw[0]);
     lds_barrier();
-    auto body = [&](int k, int buf, const In& xc, In& xn, Raw& rld, const Raw& ru) {
+    auto body = [&](int k, int j, const In& xc, In& xn) {
         load_a(k + 1, xn);
-        load_raw(k + 2, rld);
-        step(buf, xc, k + 1, ru);
+        load_raw(k + 4, raw[j]);
+        step(j & 1, xc, k + 1, raw[(j + 1) & 3]);
         lds_barrier();
     };
-    for (int k = k0; k < k1; k += 2) {
-        body(k, 0, x0, x1, r0, r1);
-        body(k + 1, 1, x1, x0, r1, r0);
+    for (int k = k0; k < k1; k += 4) {
+        body(k, 0, x0, x1);
+        body(k + 1, 1, x1, x0);
+        body(k + 2, 2, x0, x1);
+        body(k + 3, 3, x1, x0);
     }
 
 #pragma unroll
@@ -652,6 +657,11 @@ __global__ __launch_bounds__(kThreads) void ds_tile_kernel(const DsArgs a, const
             const float z = quarter(w, w);
             if (!(h4 & 1)) rd[wave][(NT - 2 + (h4 >> 1)) * 16 + l16] = z;
         }
+        if constexpr (NT % 4 == 1) {
+            const float w = half(v[NT - 1], v[NT - 1]);
+            const float z = quarter(w, w);
+            if (h4 == 0) rd[wave][(NT - 1) * 16 + l16] = z;
+        }
     };
     // four groups' sums over the waves, in wave order, once per turn: thread
     // (row, group)
@@ -706,16 +716,16 @@ hipError_t run_dx(const DxArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 // one launch per matrix: their bits may differ
-template <int NP, int MT>
+template <int NP, int MT, int NT>
 hipError_t run_ds(const DsArgs& a, hipStream_t s) {
     const int64_t nb = a.oblk * a.tblk * a.splits;
     if (nb > 0x7FFFFFFF) return hipErrorInvalidValue;
     for (int m = 0; m < a.src.nmat; ++m) {
         if (a.mat[m].bits == 3)
-            hipLaunchKernelGGL((ds_tile_kernel<3, NP, MT, tile_nt(MT)>), dim3((unsigned)nb),
+            hipLaunchKernelGGL((ds_tile_kernel<3, NP, MT, NT>), dim3((unsigned)nb),
                                dim3(kThreads), 0, s, a, m);
         else
-            hipLaunchKernelGGL((ds_tile_kernel<4, NP, MT, tile_nt(MT)>), dim3((unsigned)nb),
+            hipLaunchKernelGGL((ds_tile_kernel<4, NP, MT, NT>), dim3((unsigned)nb),
                                dim3(kThreads), 0, s, a, m);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
@@ -741,7 +751,7 @@ hipError_t launch_bwd(const BwdArgs& a, void* workspace, hipStream_t s) {
     const bool want_dx = a.dX != nullptr, want_ds = a.dscales[0] != nullptr;
     const BwdPlan p = bwd_plan(a.T, a.I, a.O, a.nmat, a.bf16, want_dx, want_ds);
     char* w = static_cast<char*>(workspace);
-    const int64_t G = cdiv(a.I, kGroup), Op = pad_to(a.O, 2 * kTileK);
+    const int64_t G = cdiv(a.I, kGroup), Op = pad_to(a.O, 4 * kTileK);
     const GradSrc src{a.nmat, a.act, a.dy_bf16, a.dY, a.pre, a.T, a.O};
     hipError_t e;
     if (want_dx) {
@@ -749,21 +759,26 @@ hipError_t launch_bwd(const BwdArgs& a, void* workspace, hipStream_t s) {
         float* unscale = reinterpret_cast<float*>(w + p.unscale_off);
         float* smax = unscale + a.T;
         const float* s1 = a.nmat == 2 ? a.mat[1].scales : nullptr;
-        if (a.bf16)
-            hipLaunchKernelGGL((grad_plane_kernel<false>), dim3((unsigned)(cdiv(a.T, kPlaneTok) + kMaxParts)),
-                               dim3(kPlaneThreads), 0, s, src, Op, A, unscale, a.mat[0].scales, s1,
-                               a.O * G, smax);
-        else
-            hipLaunchKernelGGL((grad_plane_kernel<true>), dim3((unsigned)cdiv(a.T, kPlaneTok)),
-                               dim3(kPlaneThreads), 0, s, src, Op, A, nullptr, nullptr, nullptr, 0, nullptr);
+        const int64_t maxparts = a.bf16 ? kMaxParts : 0;
+#define QT_PLANE(F, N)                                                                       \
+    hipLaunchKernelGGL((grad_plane_kernel<F, N>),                                            \
+                       dim3((unsigned)(cdiv(a.T, N) + maxparts)), dim3(N * 256), 0, s, src, Op, \
+                       A, unscale, a.mat[0].scales, s1, a.O * G, smax)
+        if (a.bf16) {
+            if (a.T >= 1024) QT_PLANE(false, 4);
+            else QT_PLANE(false, 1);
+        } else {
+            if (a.T >= 1024) QT_PLANE(true, 4);
+            else QT_PLANE(true, 1);
+        }
+#undef QT_PLANE
         e = hipGetLastError();
         if (e != hipSuccess) return e;
         const DxArgs d{{a.mat[0], a.mat[1]}, a.O, Op, a.I, G, a.T, a.nmat * Op, A, unscale, smax,
                        p.dx_splits, cdiv(a.T, 128 * p.dx_mt), cdiv(a.I, kTileN), a.dX,
                        reinterpret_cast<float*>(w + p.dxpart_off)};
         if (a.bf16)
-            e = p.dx_mt == 1 ? run_dx<false, 1>(d, s) : p.dx_mt == 2 ? run_dx<false, 2>(d, s)
-                                                                     : run_dx<false, 4>(d, s);
+            e = p.dx_mt == 1 ? run_dx<false, 1>(d, s) : run_dx<false, 2>(d, s);
         else
             e = p.dx_mt == 1 ? run_dx<true, 1>(d, s) : run_dx<true, 2>(d, s);
         if (e != hipSuccess) return e;
@@ -777,13 +792,15 @@ hipError_t launch_bwd(const BwdArgs& a, void* workspace, hipStream_t s) {
         e = launch_x_planes(a.X, a.bf16, true, a.T, a.I, X, s);
         if (e != hipSuccess) return e;
         const DsArgs d{{a.mat[0], a.mat[1]}, src, G, X, p.ds_splits, a.accumulate, p.ds_tb,
-                       cdiv(a.O, 16 * tile_nt(p.ds_mt)), {a.dscales[0], a.dscales[1]},
+                       cdiv(a.O, 16 * p.ds_nt), {a.dscales[0], a.dscales[1]},
                        reinterpret_cast<float*>(w + p.dspart_off)};
         if (a.bf16)
-            e = p.ds_mt == 1 ? run_ds<1, 1>(d, s) : p.ds_mt == 2 ? run_ds<1, 2>(d, s)
-                                                                 : run_ds<1, 4>(d, s);
+            e = p.ds_mt == 1   ? run_ds<1, 1, 8>(d, s)
+                : p.ds_mt == 2 ? run_ds<1, 2, 8>(d, s)
+                : p.ds_nt == 5 ? run_ds<1, 4, 5>(d, s)
+                               : run_ds<1, 4, 6>(d, s);
         else
-            e = p.ds_mt == 1 ? run_ds<3, 1>(d, s) : run_ds<3, 2>(d, s);
+            e = p.ds_mt == 1 ? run_ds<3, 1, 8>(d, s) : run_ds<3, 2, 8>(d, s);
         if (e != hipSuccess) return e;
         for (int m = 0; m < a.nmat && p.ds_tb > 1; ++m) {
             e = sum_parts(d.part + m * a.O * G, a.nmat * a.O * G, p.ds_tb, a.O * G, a.accumulate,

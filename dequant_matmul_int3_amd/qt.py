@@ -447,6 +447,8 @@ QT_ACT = {"silu": 0, "gelu": 1}
 def _on(dev, stream=None):
     """Context of a call on dev: its device is current (a launch goes to the
     current device), and what it allocates belongs to the stream given."""
+    if dev.type != "cuda":
+        raise ValueError("libqt takes device tensors only")
     stack = contextlib.ExitStack()
     if dev.index != torch.cuda.current_device():
         stack.enter_context(torch.cuda.device(dev))

@@ -407,12 +407,10 @@ qt_status qt_moe_layer(const float* X, int64_t T, int64_t D, int64_t F, const fl
  * The down projection of H is a qt_matvec / qt_matmul call.
  *   X [T x D] of type xt; H [T x F] of type xt, rounded once at the end
  *   pre  f32 [2][T][F] (g, then u; what qt_ffn_gated_bwd needs), or NULL
- * Sums are f32.  f32 inputs, and bf16 calls of up to 64 tokens, take the exact
- * codes with f32 group sums and scales: g and u within 1e-5 of
- * sum_i |w_fi X_ti|.  bf16 calls of more tokens take bf16(s v), each weight
- * rounded once: within 2^-8 of that sum.
+ * Both types take the exact codes and inputs with f32 group sums and scales:
+ * g and u within 1e-5 of sum_i |w_fi X_ti|.
  *   packed 16-byte aligned; X 16-byte aligned where xt is QT_BF16 and D a
- *   multiple of 64 (its rows are read in place), else at its elements'
+ *   multiple of 64 (small calls read its rows in place), else at its elements'
  *   alignment; 1 <= T <= 2^22; 1 <= D, F <= 2^20.
  *   workspace: qt_ffn_gated_workspace_bytes(T, D, F, xt) bytes (16-byte
  *   aligned; may be NULL when that size is 0).  Calls that may overlap in
@@ -438,9 +436,11 @@ qt_status qt_ffn_gated(const uint8_t* gate_packed, const float* gate_scales, int
  *   dX may be NULL; dgate_scales and dup_scales may both be NULL; at least
  *   one kind is wanted.  accumulate = 1 adds to the scales' gradients that
  *   are there (dX is always written).
- * bf16: dX takes dg, du and s v rounded once each to bf16, f32 sums and one
- * rounding at the end.  The scales' gradients are f32 throughout: exact codes
- * and inputs, f32 dg and du.
+ * bf16: dX takes dg, du and s v rounded to f16 (each token's gradients and all
+ * scales scaled by exact powers of two, so that values within 2^26 of the
+ * largest keep 11 bits), f32 sums and one rounding at the end; f32: products
+ * and sums in f32.  The scales' gradients are f32 throughout: exact codes and
+ * inputs, f32 dg and du.
  *   Alignment and sizes as qt_ffn_gated; workspace:
  *   qt_ffn_gated_bwd_workspace_bytes(T, D, F, xt, dX wanted, scales wanted).
  */

@@ -117,8 +117,8 @@ int main() {
     expect("x + 1", ffn(4, 65, 64, QT_BF16, 3, 3, 0, 1), QT_ERR_ALIGN, 0);
     expect("x + 4, f32", ffn(4, 64, 64, QT_F32, 3, 3, 0, 4), QT_OK, 1);
     expect("x + 2, f32", ffn(4, 64, 64, QT_F32, 3, 3, 0, 2), QT_ERR_ALIGN, 0);
-    const size_t need = qt_ffn_gated_workspace_bytes(4, 65, 64, QT_BF16);
-    expect("workspace", ffn(4, 65, 64, QT_BF16, 3, 3, 0, 0, need - 1), QT_ERR_WORKSPACE, 0);
+    const size_t need = qt_ffn_gated_workspace_bytes(20, 65, 64, QT_BF16);
+    expect("workspace", ffn(20, 65, 64, QT_BF16, 3, 3, 0, 0, need - 1), QT_ERR_WORKSPACE, 0);
     expect("no workspace needed", ffn(4, 64, 64, QT_BF16, 3, 3, 0, 0, 0), QT_OK, 1);
     expect("bwd workspace", bwd(4, 64, 64, QT_F32, true, true, 0, 0), QT_ERR_WORKSPACE, 0);
     expect("output over input",

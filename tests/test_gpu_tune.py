@@ -55,6 +55,14 @@ FFN = [
     (513, 577, 321, (3, 4), "silu", BF),
     (300, 2000, 67, (4, 4), "silu", F32),
     (1025, 256, 63, (4, 4), "silu", BF),
+    (33, 2048, 40, (3, 3), "silu", BF),    # eight waves, 48 and 64 KB of sums
+    (64, 2048, 40, (4, 3), "silu", BF),
+    (21, 2048, 24, (3, 4), "gelu", F32),
+    (4, 1536, 40, (3, 4), "silu", BF),     # 16 piece rows or less go through LDS
+    (3, 1000, 40, (4, 3), "gelu", BF),
+    (5, 1504, 24, (4, 4), "silu", F32),    # 15 of them
+    (6, 1504, 24, (3, 3), "silu", F32),    # 18: planes
+    (16, 1600, 24, (3, 4), "silu", BF),    # 16 rows, too long for LDS: in place
 ]
 
 
@@ -67,9 +75,7 @@ def test_ffn_gated(T, D, F, bits, act, dtype):
     H, fine_h = guarded((T, F), dtype)
     pre, fine_p = guarded((2, T, F), F32)
     qt.qt_ffn_gated(gate, up, x, act=act, H=H, pre=pre)
-    small = T * (1 if dtype == BF else 3) <= 64
-    wr = 0.0 if dtype == F32 or small else half_step(BF)
-    h, g, u, bh, bg, bu = ffn_ref(x, dense(gate, vg, D), dense(up, vu, D), act, dtype, wr)
+    h, g, u, bh, bg, bu = ffn_ref(x, dense(gate, vg, D), dense(up, vu, D), act, dtype)
     errs = worst(pre[0], g, bg), worst(pre[1], u, bu), worst(H, h, bh)
     say(f"  error / bound: g {errs[0]:.3f} u {errs[1]:.3f} h {errs[2]:.3f}")
     assert max(errs) <= 1.0
@@ -86,7 +92,7 @@ def test_ffn_gated_extreme_activations():
     for act in ("silu", "gelu"):
         x = rnd((T, D), 3) * 1e5
         H, pre = qt.qt_ffn_gated(gate, up, x, act=act, want_pre=True)
-        h = ffn_ref(x, dense(gate, vg, D), dense(up, vu, D), act, F32, 0.0)[0]
+        h = ffn_ref(x, dense(gate, vg, D), dense(up, vu, D), act, F32)[0]
         assert pre.abs().max() > 1e4
         assert worst(H, h, 1e-4 * h.abs() + 1e-30 + 1e-5 * h.abs().max()) <= 1.0
         dX, dsg, dsu = qt.qt_ffn_gated_bwd(gate, up, pre, torch.ones_like(H), x, act=act)
@@ -108,6 +114,8 @@ BWD = [
     (300, 320, 2000, (3, 4), "silu", BF),
     (513, 577, 321, (4, 3), "gelu", BF),
     (1025, 256, 192, (4, 4), "silu", BF),
+    (2050, 130, 90, (3, 4), "silu", BF),
+    (1030, 64, 65, (4, 3), "gelu", F32),
 ]
 
 
@@ -156,6 +164,8 @@ LIN = [
     (130, 128, 1000, 3, F32, F32),
     (513, 200, 257, 4, BF, BF),
     (600, 1024, 64, 3, BF, F32),
+    (1024, 64, 20001, 4, BF, F32),   # 251 row blocks of 80 for 209 of 96 (a step is shorter)
+    (1024, 70, 6000, 3, BF, BF),
 ]
 
 
@@ -180,6 +190,35 @@ def test_matmul_bwd(B, I, O, bits, dtype, ytype):
     acc = torch.ones_like(ds)
     qt.qt_matmul_bwd(w, dy, x, want_dx=False, dscales=acc, accumulate=True)
     assert torch.equal(acc, 1 + ds)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_wide_ranges_of_gradients_and_scales(dtype):
+    # tokens' gradients from 1e-30 to 1e20 and scales from 1e-6 to 1e4: the
+    # powers of two that bring both into f16's range are exact; rows without
+    # any gradient stay zero.  bf16: a term under 2^-26 of its token's largest
+    # gradient or of the largest scale keeps an absolute error of 2^-39 of it
+    # (2^-38 for the two together)
+    B, I, O = 40, 200, 96
+    w, v = quantized(O, I, 3, 3)
+    w[1].mul_((10.0 ** torch.linspace(-4, 5, w[1].shape[1], device=DEV))[None, :])
+    x = rnd((B, I), 1, dtype)
+    dy = rnd((B, O), 2, F32) * (10.0 ** torch.linspace(-30, 20, B, device=DEV))[:, None]
+    dy[7] = 0
+    dX, ds = qt.qt_matmul_bwd(w, dy, x)
+    W, Y = dense(w, v, I), dy.double()
+    ref = Y @ W
+    b = dx_bound([(Y, 0 * Y, W)], dtype, dtype)
+    if dtype == BF:
+        b = b + 2.0 ** -38 * O * 4 * Y.abs().amax(1, keepdim=True) * w[1].abs().max().double()
+    b = b + half_step(dtype) * (ref.abs() + b) + 2.0 ** -126
+    assert worst(dX, ref, b) <= 1.0 and (dX[7] == 0).all()
+    bound = SUM * scale_grad(Y.abs(), x.double().abs(), v.abs()) + 1e-30
+    assert worst(ds, scale_grad(Y, x.double(), v), bound) <= 1.0
+    # no scale at all
+    z = (w[0], torch.zeros_like(w[1]), 3)
+    dX, _ = qt.qt_matmul_bwd(z, dy, x)
+    assert (dX == 0).all()
 
 
 def test_masked_tokens_leave_no_trace():

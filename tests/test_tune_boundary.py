@@ -31,10 +31,13 @@ def test_tuning_validation_under_sanitizers(tmp_path):
 
 def test_workspace_sizes():
     bf, f32 = qt.QT_BF16, qt.QT_F32
-    # bf16 rows of whole groups are read in place; other inputs are copied
-    assert qt.qt_ffn_gated_workspace_bytes(1, 7168, 2048, bf) == 0
-    assert qt.qt_ffn_gated_workspace_bytes(1, 7200, 2048, bf) >= 7232 * 2
-    assert qt.qt_ffn_gated_workspace_bytes(3, 64, 64, f32) >= 3 * 3 * 64 * 2
+    # a few rows go through LDS, bf16 rows of whole groups are read in place;
+    # other inputs are copied
+    assert qt.qt_ffn_gated_workspace_bytes(1, 7200, 2048, bf) == 0
+    assert qt.qt_ffn_gated_workspace_bytes(12, 7168, 2048, bf) == 0
+    assert qt.qt_ffn_gated_workspace_bytes(12, 7200, 2048, bf) >= 12 * 7232 * 2
+    assert qt.qt_ffn_gated_workspace_bytes(8, 64, 64, f32) >= 3 * 8 * 64 * 2
+    assert qt.qt_ffn_gated_workspace_bytes(65, 64, 64, bf) >= 80 * 64 * 2
     both = qt.qt_ffn_gated_bwd_workspace_bytes(300, 200, 150, bf)
     dx = qt.qt_ffn_gated_bwd_workspace_bytes(300, 200, 150, bf, want_dscales=False)
     ds = qt.qt_ffn_gated_bwd_workspace_bytes(300, 200, 150, bf, want_dx=False)
@@ -56,9 +59,9 @@ def test_ffn_refusals():
     assert call(xt=2) == DTYPE
     assert call(T=0) == SHAPE and call(F=0) == SHAPE and call(D=(1 << 20) + 1) == SHAPE
     assert call(gb=2) == ARG and call(ub=8) == ARG and call(act=2) == ARG
-    assert call(D=65) == WORKSPACE and call(D=65, ws=H, wsb=16) == WORKSPACE
+    assert call(T=20, D=65) == WORKSPACE and call(T=20, D=65, ws=H, wsb=16) == WORKSPACE
     assert call(gp=A + 4) == ALIGN and call(X=E + 2) == ALIGN and call(pre=G_ + 2) == ALIGN
-    assert call(D=65, ws=H + 8, wsb=1 << 20) == ALIGN
+    assert call(T=20, D=65, ws=H + 8, wsb=1 << 20) == ALIGN
     assert call(Hh=E) == ALIAS and call(pre=F_) == ALIAS and call(Hh=A + 64) == ALIAS
 
 
@@ -103,3 +106,15 @@ def test_distill_refusals():
     assert fwd(lse=D) == ALIAS and fwd(dz=A + 64) == ALIAS and fwd(dz=A, ldd=65) == ALIAS
     assert b(A, 1, 4, 64, 64, B, C_, 4, 1.0, None, None, D, 64, None) == NULL
     assert b(A, 1, 4, 64, 64, B, C_, 4, 1.0, E, None, E, 64, None) == ALIAS
+
+
+def test_host_tensors_are_refused():
+    import torch
+    w = (torch.zeros(4 * 24, dtype=torch.uint8), torch.zeros(4, 1), 3)
+    x = torch.zeros(2, 64)
+    with pytest.raises(ValueError, match="device tensors"):
+        qt.qt_ffn_gated(w, w, x)
+    with pytest.raises(ValueError, match="device tensors"):
+        qt.qt_matmul_bwd(w, torch.zeros(2, 4), x)
+    with pytest.raises(ValueError, match="device tensors"):
+        qt.qt_distill_topk(x, torch.zeros(2, 1, dtype=torch.int32), torch.zeros(2, 1))

@@ -47,15 +47,14 @@ def half_step(dtype):
 SUM = 1e-5
 
 
-def ffn_ref(x, wg, wu, act, dtype, weight_rounding):
-    """h, g, u and bounds of their errors: g and u are off by SUM (plus the
-    weights' rounding) of sum |w x|; |act'| <= 1.13 for both activations."""
+def ffn_ref(x, wg, wu, act, dtype):
+    """h, g, u and bounds of their errors: g and u are off by SUM of sum |w x|;
+    |act'| <= 1.13 for both activations."""
     X = x.double()
     g, u = X @ wg.t(), X @ wu.t()
     ag, au = X.abs() @ wg.abs().t(), X.abs() @ wu.abs().t()
     a, _ = act64(g, act)
-    tol = SUM + weight_rounding
-    bg, bu = tol * ag, tol * au
+    bg, bu = SUM * ag, SUM * au
     h = a * u
     # the activation's own f32 operations: a few roundings of a and of the product
     bh = (1.13 * bg + 1e-6 * a.abs()) * (u.abs() + bu) + a.abs() * bu
@@ -71,12 +70,12 @@ def grads_ref(g, u, dh, act):
 
 
 def dx_bound(parts, dtype, out_dtype):
-    """parts: (dy, bound of dy, w) per matrix.  bf16 operands: dy and s v are
-    rounded once each."""
-    r = half_step(dtype) if dtype == torch.bfloat16 else 0.0
+    """parts: (dy, bound of dy, w) per matrix.  bf16 calls: dy is rounded once to
+    f16 and s v twice (the scale, then the product)."""
+    r = half_step(torch.float16) if dtype == torch.bfloat16 else 0.0
     b = 0
     for dy, e, w in parts:
-        b = b + (e * (1 + r) + dy.abs() * ((1 + r) ** 2 - 1 + SUM)) @ w.abs() * (1 + r)
+        b = b + (e * (1 + r) + dy.abs() * ((1 + r) ** 3 - 1 + SUM)) @ w.abs() * (1 + r)
     return b
 
 
