@@ -5,7 +5,8 @@
 //
 // f32 inputs are split exactly into three bf16 pieces (a small launch writes
 // them as planes), so that both types run on the bf16 matrix cores; bf16
-// inputs whose rows are not whole groups are copied into padded planes.
+// inputs whose rows are not whole groups are copied into padded planes, or a few
+// rows into LDS by every block.
 //
 // Small form (up to 64 rows of bf16 or pieces): the weights' stream bounds
 // it.  A block of W waves owns 16 features; a lane loads whole 24- or 32-byte
@@ -14,13 +15,19 @@
 // cores exactly: each group's products are summed in f32 and scaled by the
 // group's f32 scale, as the vector forms of the library do.
 //
-// Tile form: a block of 8 waves owns 128 MT tokens x 64 features of both
-// projections and walks the inner axis one group at a time; the weights are
-// unpacked once per block into LDS in matrix-operand order, the inputs go
-// straight from global memory into registers.  bf16 inputs take the weights
-// as bf16(s v), one rounding of each weight to the inputs' type: it saves two
-// f32 FMAs per matrix instruction, which do not hide behind the matrix cores
-// on this chip.  f32 inputs keep the exact codes and the f32 scale per group.
+// One token of 18432 x 7168 (115 MB): 34 us, 3.4 TB/s; it issues 2.8 vector
+// instructions per code, about 20 us of the vector ALUs' time.
+//
+// Tile form: a block of 8 waves owns 128 MT tokens x 8 NT features of both
+// projections and walks the inner axis one group at a time.  The inputs are
+// laid out as matrix operands by a small launch first and go straight from
+// global memory into registers; the weights are unpacked once per block into
+// LDS in operand order.  Codes and inputs are exact, each group's products are
+// scaled by the f32 scale (two FMAs per matrix instruction): weights rounded to
+// bf16(s v) would save them (1.08 against 1.35 ms at 4096 x 5120 x 2 17408) but
+// leave the pre-activations 4e-3 off, and with them the f32 gradients of the
+// scales.  That shape runs at 1080 TFLOP/s (1.5 ms with pre written), the
+// matrix cores busy 43 % of the cycles; the FMAs and the unpacking bound it.
 #include <algorithm>
 
 #include "lds_barrier.h"
@@ -39,8 +46,8 @@ typedef u32x4_t u32x4_u __attribute__((aligned(2)));
 // zero past D.  BLOCKED false: [NP][T][Dp] rows.  BLOCKED true: matrix-operand
 // order, [NP][ceil(T/16)][Dp/32] blocks of 64 lanes x 16 bytes (lane l holds
 // values 8 (l / 16) .. + 7 of token l % 16), zero past T: every operand load of
-// the tiles is then one contiguous kilobyte.  Reading rows in place instead
-// touched 16 half lines per load and measured 715 against 830 TFLOP/s.
+// the tiles is then one contiguous kilobyte (rows read in place touch 16 half lines per
+// load, at strides that share memory channels).
 template <bool BF16, bool BLOCKED>
 __global__ __launch_bounds__(256) void planes_kernel(const void* __restrict__ X, int64_t T,
                                                      int64_t D, int64_t Dp,
