@@ -577,3 +577,42 @@ def test_binding_refusals():
         qt.qt_distill_topk(z[:2], idx[:2], tl[:2], dlogits=z[1:3])
     with pytest.raises(qt.QtError):   # one row under all
         qt.qt_distill_topk(z, idx, tl, dlogits=torch.empty((1, 50), device=DEV).expand(T, 50))
+
+
+def test_offsets_past_32_bits():
+    # 70000 tokens x 40000 features (pre: 22 GB) and 20000 rows of 131072
+    # logits: the last rows, tokens and sums against references of their own
+    T, D, F = 70000, 64, 40000
+    say(f"offsets: block {T} x {F}")
+    (gate, vg), (up, vu) = quantized(F, D, 3, 1), quantized(F, D, 4, 2)
+    x = rnd((T, D), 1, BF)
+    H, pre = qt.qt_ffn_gated(gate, up, x, want_pre=True)
+    g = torch.Generator(device=DEV).manual_seed(2)
+    dh = torch.randn((T, F), generator=g, device=DEV, dtype=BF)
+    dX, dsg, dsu = qt.qt_ffn_gated_bwd(gate, up, pre, dh, x)
+    wg, wu = dense(gate, vg, D), dense(up, vu, D)
+    n = 300
+    h, gr, ur, bh, bg, bu = ffn_ref(x[-n:], wg, wu, "silu", BF)
+    assert worst(H[-n:], h, bh) <= 1 and worst(pre[0, -n:], gr, bg) <= 1
+    assert worst(pre[1, -n:], ur, bu) <= 1
+    dg, du, eg, eu = grads_ref(pre[0, -n:].double(), pre[1, -n:].double(), dh[-n:].double(), "silu")
+    ref = dg @ wg + du @ wu
+    b = dx_bound([(dg, eg, wg), (du, eu, wu)], BF, BF)
+    assert worst(dX[-n:], ref, b + half_step(BF) * (ref.abs() + b) + 1e-30) <= 1
+    o, X = 40, x.double()
+    dg, du, eg, eu = grads_ref(pre[0, :, -o:].double(), pre[1, :, -o:].double(),
+                               dh[:, -o:].double(), "silu")
+    for got, dy, e, v in ((dsg, dg, eg, vg[-o:]), (dsu, du, eu, vu[-o:])):
+        bound = scale_grad(SUM * dy.abs() + e, X.abs(), v.abs()) + 1e-30
+        assert worst(got[-o:], scale_grad(dy, X, v), bound) <= 1
+    del H, pre, dh, dX, dg, du, eg, eu
+    torch.cuda.empty_cache()
+    T, V, k = 20000, 131072, 8
+    say(f"offsets: loss {T} x {V}")
+    z = torch.zeros((T, V), device=DEV, dtype=BF)
+    z[-n:] = rnd((n, V), 3, BF)
+    idx, tl = teacher(T, V, k, 4)
+    loss, lse, dz = qt.qt_distill_topk(z, idx, tl, want_dlogits=True)
+    check_distill(z[-n:], idx[-n:], tl[-n:], 1.0, None, loss[-n:], lse[-n:], dz[-n:])
+    dz2 = qt.qt_distill_topk_bwd(z, idx, tl, lse)
+    check_distill(z[-n:], idx[-n:], tl[-n:], 1.0, None, loss[-n:], lse[-n:], dz2[-n:])
