@@ -616,3 +616,27 @@ def test_offsets_past_32_bits():
     check_distill(z[-n:], idx[-n:], tl[-n:], 1.0, None, loss[-n:], lse[-n:], dz[-n:])
     dz2 = qt.qt_distill_topk_bwd(z, idx, tl, lse)
     check_distill(z[-n:], idx[-n:], tl[-n:], 1.0, None, loss[-n:], lse[-n:], dz2[-n:])
+
+
+def test_two_calls_at_once():
+    # two streams, a workspace each (the binding's own), interleaved launches
+    D, F, T = 640, 320, 400
+    gate, up = quantized(F, D, 3, 1)[0], quantized(F, D, 4, 2)[0]
+    xs = [rnd((T, D), s, BF) for s in (1, 2)]
+    dh = rnd((T, F), 3, BF)
+    z = [rnd((5, 40000), s, F32) for s in (4, 5)]
+    idx, tl = teacher(5, 40000, 16, 6)
+
+    def step(i, stream=None):
+        h, pre = qt.qt_ffn_gated(gate, up, xs[i], want_pre=True, stream=stream)
+        return [h, *qt.qt_ffn_gated_bwd(gate, up, pre, dh, xs[i], stream=stream),
+                *qt.qt_distill_topk(z[i], idx, tl, want_dlogits=True, stream=stream)]
+
+    want = [step(0), step(1)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        got = [step(i, streams[i]) for i in (0, 1)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(p, q) for p, q in zip(a, b))
