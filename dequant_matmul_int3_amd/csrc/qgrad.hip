@@ -15,13 +15,14 @@
 //   bf16: both operands are rounded to f16, whose eight times finer step keeps
 //   the result within its own bf16 rounding (operands in bf16 left it 1.7 times
 //   as far off).  Exact powers of two bring them into f16's range and are taken
-//   back from the sums: every token's dY is scaled by (a bound of) its largest magnitude
-//   to 2^14 .. 2^15, the scales of both matrices by the largest of them to 2^11 ..
-//   2^12.  Values within 2^26 of those largest ones keep all 11 bits, smaller
-//   ones an absolute error of 2^-39 of them.  The operands come out of LDS
-//   through the transposing reads of gfx950, four rows of 16 columns at a
-//   time: a lane's eight inner elements are rows 4h .. 4h+3 and 16+4h ..
-//   16+4h+3 of a 32-row step, and the dY plane is written in that order.
+//   back from the sums: every token's dY is scaled by its largest magnitude to
+//   2^14 .. 2^15, the scales of both matrices by the largest of them to 2^11 ..
+//   2^12.  Gradients within 2^28 of their token's largest and scales within 2^25
+//   of the largest keep all 11 bits, smaller ones an absolute error of 2^-39 and
+//   2^-36 of the largest.  The operands come out of LDS through the transposing
+//   reads of gfx950, four rows of 16 columns at a time: a lane's eight inner
+//   elements are rows 4h .. 4h+3 and 16+4h .. 16+4h+3 of a 32-row step, and the
+//   dY plane is written in that order.
 //   f32: both stay f32, on the f32 matrix instructions.
 // 4096 tokens, 2 x 17408 rows of 5120: 1.55 ms (940 TFLOP/s) and 0.39 ms for
 // the plane.
@@ -170,19 +171,31 @@ __global__ __launch_bounds__(TOK * 256) void grad_plane_kernel(
         get4(0, o0);
         get4(4, o0 + (F32 ? 4 : 16));
     };
-    // The factor comes from a bound of the gradients (|act'| <= 1.13, |act(g)|
-    // <= |g| + 0.3), which costs no exponential.
+    // the gradients themselves, one matrix's after the other's
+    auto form = [&](const float (&d)[8], const float (&g)[8], const float (&u)[8],
+                    float (&v)[2][8]) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (src.nmat == 1) {
+                v[0][e] = d[e];
+                v[1][e] = 0.0f;
+            } else {
+                act_grads(g[e], u[e], d[e], src.act, v[0][e], v[1][e]);
+            }
+        }
+    };
+    // The factor comes from the largest gradient, not from a bound of it (such
+    // as |dH| (|g| + 0.3)): behind a closed gate (g = -30, say) the gradients
+    // are 2^-40 of that bound and would all become 0.
     float f = 1.0f;
     if constexpr (!F32) {
         float m = 0.0f;
         for (int64_t c = c0; c < per; c += kStep) {
-            float d[8], g[8], u[8];
+            float d[8], g[8], u[8], v[2][8];
             fetch(c, d, g, u);
+            form(d, g, u, v);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                m = fmaxf(m, src.nmat == 1 ? fabsf(d[e])
-                                           : fabsf(d[e]) * fmaxf(1.13f * fabsf(u[e]),
-                                                                 fabsf(g[e]) + 0.3f));
+            for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(fabsf(v[0][e]), fabsf(v[1][e])));
         }
         // over the lanes of the token, then the waves
 #pragma unroll
@@ -200,15 +213,7 @@ __global__ __launch_bounds__(TOK * 256) void grad_plane_kernel(
     for (int64_t c = c0; c < per; c += kStep) {
         float d[8], g[8], u[8], v[2][8];
         fetch(c, d, g, u);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (src.nmat == 1) {
-                v[0][e] = d[e];
-                v[1][e] = 0.0f;
-            } else {
-                act_grads(g[e], u[e], d[e], src.act, v[0][e], v[1][e]);
-            }
-        }
+        form(d, g, u, v);
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             if (m >= src.nmat || !live) break;

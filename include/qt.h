@@ -436,11 +436,12 @@ qt_status qt_ffn_gated(const uint8_t* gate_packed, const float* gate_scales, int
  *   dX may be NULL; dgate_scales and dup_scales may both be NULL; at least
  *   one kind is wanted.  accumulate = 1 adds to the scales' gradients that
  *   are there (dX is always written).
- * bf16: dX takes dg, du and s v rounded to f16 (each token's gradients and all
- * scales scaled by exact powers of two, so that values within 2^26 of the
- * largest keep 11 bits), f32 sums and one rounding at the end; f32: products
- * and sums in f32.  The scales' gradients are f32 throughout: exact codes and
- * inputs, f32 dg and du.
+ * bf16: dX takes dg, du and s v rounded to f16, f32 sums and one rounding at the
+ * end.  Each token's gradients and all scales are scaled by exact powers of two:
+ * gradients within 2^28 of their token's largest and scales within 2^25 of the
+ * largest keep 11 bits, smaller ones are off by at most 2^-39 and 2^-36 of it.
+ * f32: products and sums in f32.  The scales' gradients are f32 throughout:
+ * exact codes and inputs, f32 dg and du.
  *   Alignment and sizes as qt_ffn_gated; workspace:
  *   qt_ffn_gated_bwd_workspace_bytes(T, D, F, xt, dX wanted, scales wanted).
  */

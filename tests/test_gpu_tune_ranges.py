@@ -1,0 +1,60 @@
+"""The tuning calls where their inputs' ranges and levels are extreme: closed
+gates, tiny gradients, logits far from zero or at the type's lowest value,
+rows at odd addresses, the largest sizes.  Bounds count the roundings that the
+kernels make (U: half a step of f32) and know nothing of what a fault would do."""
+import math
+
+import pytest
+import torch
+
+import dequant_matmul_int3_amd as qt
+from tests.gpu_util import DEV, say
+from tests.tune_util import act64, dense, dx_bound, half_step, quantized
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+U = 2.0 ** -24
+
+
+def rnd(shape, seed, dtype=F32, std=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * std).to(dtype).to(DEV)
+
+
+# ------------------------------------------------------------ input gradient
+@pytest.mark.parametrize("act,gates", [("silu", (-5.0, -12.0, -30.0, -60.0)),
+                                       ("gelu", (-5.0, -6.0, -7.0, -9.0))])
+@pytest.mark.parametrize("T", [4, 1028])
+def test_gradients_behind_closed_gates(act, gates, T):
+    # bf16 tokens whose gradient is not zero only where the gate is closed: the
+    # largest gradients are 1e-3 down to 1e-26 there, and each token's own
+    # power of two has to follow them.
+    # The sigmoid's argument x has at most four roundings, so that the sigmoid
+    # e^x is off by (4 |x| + 4) U relative, its products and sums by a few U; for
+    # g <= -5 the two terms of act' are far from cancelling.
+    D, F = 192, 160
+    (gate, vg), (up, vu) = quantized(F, D, 3, 1), quantized(F, D, 4, 2)
+    x, dh = rnd((T, D), 3, BF), rnd((T, F), 4, BF, 0.1)
+    g = torch.tensor(gates, device=DEV).repeat(T // 4)[:, None]
+    g = g * (1 + 0.02 * rnd((T, F), 5).clamp(-2, 2))
+    g[:, F // 2:] = 3.0
+    dh[:, F // 2:] = 0
+    pre = torch.stack([g, rnd((T, F), 6)])
+    dX = qt.qt_ffn_gated_bwd(gate, up, pre, dh, x, act=act, want_dscales=False)[0]
+    G, u, H = pre[0].double(), pre[1].double(), dh.double()
+    a, da = act64(G, act)
+    dg, du = H * u * da, H * a
+    arg = G if act == "silu" else 2 * math.sqrt(2 / math.pi) * (G + 0.044715 * G ** 3)
+    e = (8 * arg.abs() + 32) * U
+    wg, wu = dense(gate, vg, D), dense(up, vu, D)
+    ref = dg @ wg + du @ wu
+    b = dx_bound([(dg, e * dg.abs(), wg), (du, e * du.abs(), wu)], BF, BF)
+    # f16's subnormals: 2^-39 of the token's largest gradient for each of 2 F terms
+    top = torch.maximum(dg.abs().amax(1), du.abs().amax(1))[:, None]
+    b = b + 2.0 ** -38 * 2 * F * 8 * top * max(float(gate[1].max()), float(up[1].max()))
+    b = b + half_step(BF) * (ref.abs() + b) + 2.0 ** -133
+    r = torch.nan_to_num((dX.double() - ref).abs() / b, nan=math.inf)
+    say(f"{act} T={T}: error / bound " +
+        " ".join(f"{v}: {float(r[n::4].max()):.3f}" for n, v in enumerate(gates)))
+    assert float(r.max()) <= 1.0
