@@ -88,6 +88,9 @@ __device__ __forceinline__ float range_factor(float m, int top) {
     return __uint_as_float((uint32_t)(127 + std::min(std::max(x, -125), 125)) << 23);
 }
 
+// x of a factor 2^x
+__device__ __forceinline__ int factor_exp(float f) { return (int)(__float_as_uint(f) >> 23) - 127; }
+
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 __device__ __forceinline__ uint32_t f16_pair(float a, float b) {
@@ -96,7 +99,7 @@ __device__ __forceinline__ uint32_t f16_pair(float a, float b) {
 
 template <bool F32, int TOK>
 __global__ __launch_bounds__(TOK * 256) void grad_plane_kernel(
-    const GradSrc src, int64_t Op, void* __restrict__ P, float* __restrict__ unscale,
+    const GradSrc src, int64_t Op, void* __restrict__ P, float* __restrict__ factor,
     const float* __restrict__ s0, const float* __restrict__ s1, int64_t nscales,
     float* __restrict__ smax) {
     constexpr int kPlaneThreads = TOK * 256, kPlaneTok = TOK;
@@ -207,7 +210,7 @@ __global__ __launch_bounds__(TOK * 256) void grad_plane_kernel(
 #pragma unroll
         for (int w = 1; w < kPlaneThreads / 64; ++w) m = fmaxf(m, wm[w][tk]);
         f = range_factor(m, 14);
-        if (tid < 4 * kPlaneTok && (tid & 3) == 0 && live) unscale[t] = 1.0f / f;
+        if (tid < 4 * kPlaneTok && (tid & 3) == 0 && live) factor[t] = f;
     }
     const int64_t row = (t >> 4) * (src.nmat * Op) * 16 + (t & 15) * 32;  // block 0, this token
     for (int64_t c = c0; c < per; c += kStep) {
@@ -236,7 +239,7 @@ struct DxArgs {
     QMat mat[2];
     int64_t O, Op, I, G, T, K;  // K = nmat Op
     const void* A;              // gradient plane
-    const float* unscale;       // [T] inverse factors of the plane's tokens (bf16)
+    const float* factor;        // [T] powers of two of the plane's tokens (bf16)
     const float* smax;          // [kMaxParts] largest scales (bf16)
     int splits;
     int64_t mblk, nblk;
@@ -435,8 +438,10 @@ __global__ __launch_bounds__(kThreads) void dx_tile_kernel(const DxArgs a) {
     for (int mt = 0; mt < MT; ++mt) {
         const int64_t t = m0 + wave * (16 * MT) + mt * 16 + l16;
         if (t >= a.T) continue;
-        float un = 1.0f;  // takes both powers of two back
-        if constexpr (!F32) un = a.unscale[t] / sf;
+        // takes both powers of two back; one exponent, since their product may
+        // be no f32 number where the result is one
+        int un = 0;
+        if constexpr (!F32) un = -factor_exp(a.factor[t]) - factor_exp(sf);
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
             const int64_t i = n * kTileN + nt * 16 + 4 * h4;
@@ -445,7 +450,7 @@ __global__ __launch_bounds__(kThreads) void dx_tile_kernel(const DxArgs a) {
             f32x4_t v = acc[mt][nt];
             if constexpr (!F32) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) v[r] *= un;
+                for (int r = 0; r < 4; ++r) v[r] = __builtin_ldexpf(v[r], un);
             }
             if (a.splits > 1 || F32) {
                 float* p = a.splits > 1 ? a.part + (int64_t)sp * a.T * a.I + o
@@ -765,14 +770,14 @@ hipError_t launch_bwd(const BwdArgs& a, void* workspace, hipStream_t s) {
     hipError_t e;
     if (want_dx) {
         void* A = w + p.grad_off;
-        float* unscale = reinterpret_cast<float*>(w + p.unscale_off);
-        float* smax = unscale + a.T;
+        float* factor = reinterpret_cast<float*>(w + p.factor_off);
+        float* smax = factor + a.T;
         const float* s1 = a.nmat == 2 ? a.mat[1].scales : nullptr;
         const int64_t maxparts = a.bf16 ? kMaxParts : 0;
 #define QT_PLANE(F, N)                                                                       \
     hipLaunchKernelGGL((grad_plane_kernel<F, N>),                                            \
                        dim3((unsigned)(cdiv(a.T, N) + maxparts)), dim3(N * 256), 0, s, src, Op, \
-                       A, unscale, a.mat[0].scales, s1, a.O * G, smax)
+                       A, factor, a.mat[0].scales, s1, a.O * G, smax)
         if (a.bf16) {
             if (a.T >= 1024) QT_PLANE(false, 4);
             else QT_PLANE(false, 1);
@@ -783,7 +788,7 @@ hipError_t launch_bwd(const BwdArgs& a, void* workspace, hipStream_t s) {
 #undef QT_PLANE
         e = hipGetLastError();
         if (e != hipSuccess) return e;
-        const DxArgs d{{a.mat[0], a.mat[1]}, a.O, Op, a.I, G, a.T, a.nmat * Op, A, unscale, smax,
+        const DxArgs d{{a.mat[0], a.mat[1]}, a.O, Op, a.I, G, a.T, a.nmat * Op, A, factor, smax,
                        p.dx_splits, cdiv(a.T, 128 * p.dx_mt), cdiv(a.I, kTileN), a.dX,
                        reinterpret_cast<float*>(w + p.dxpart_off)};
         if (a.bf16)

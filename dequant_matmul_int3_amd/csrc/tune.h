@@ -155,7 +155,7 @@ struct BwdArgs {
 struct BwdPlan {
     int dx_mt, dx_splits;
     int ds_mt, ds_nt, ds_tb, ds_splits;  // as FfnPlan; token blocks, splits of the groups
-    int64_t grad_off, unscale_off, dxpart_off, planes_off, dspart_off, bytes;
+    int64_t grad_off, factor_off, dxpart_off, planes_off, dspart_off, bytes;
 };
 inline BwdPlan bwd_plan(int64_t T, int64_t I, int64_t O, int nmat, bool bf16, bool want_dx,
                         bool want_ds) {
@@ -170,7 +170,7 @@ inline BwdPlan bwd_plan(int64_t T, int64_t I, int64_t O, int nmat, bool bf16, bo
                                    (bf16 ? 0.35 : 3.0) * p.dx_mt, 1.0 * T * I * 4);
         p.grad_off = off;
         off += sect(pad_to(T, 16) * K * (bf16 ? 2 : 4));
-        p.unscale_off = off;
+        p.factor_off = off;
         off += sect((T + 64) * 4);  // the tokens' factors and 64 partial maxima
         p.dxpart_off = off;
         off += p.dx_splits > 1 ? sect(p.dx_splits * T * I * 4) : 0;

@@ -9,7 +9,7 @@ import torch
 
 import dequant_matmul_int3_amd as qt
 from tests.gpu_util import DEV, say
-from tests.tune_util import act64, dense, dx_bound, half_step, quantized
+from tests.tune_util import act64, dense, dx_bound, half_step, quantized, worst
 
 pytestmark = pytest.mark.gpu
 
@@ -58,3 +58,22 @@ def test_gradients_behind_closed_gates(act, gates, T):
     say(f"{act} T={T}: error / bound " +
         " ".join(f"{v}: {float(r[n::4].max()):.3f}" for n, v in enumerate(gates)))
     assert float(r.max()) <= 1.0
+
+
+def test_tiny_gradients_and_scales():
+    # gradients of 2^-112 and scales of 2^-14: the powers of two that bring them
+    # into f16's range multiply to 2^150, whose inverse is no f32 number, while dX
+    # (2^-122) is a normal bf16 one
+    B, I, O = 40, 200, 1024
+    w, v = quantized(O, I, 3, 3)
+    w[1].mul_(2.0 ** -14 / float(w[1].max()))
+    x, dy = rnd((B, I), 1, BF), rnd((B, O), 2).clamp(-2, 2) * 2.0 ** -112
+    dX = qt.qt_matmul_bwd(w, dy, x, want_dscales=False)[0]
+    W, Y = dense(w, v, I), dy.double()
+    ref = Y @ W
+    b = dx_bound([(Y, 0 * Y, W)], BF, BF)
+    b = b + half_step(BF) * (ref.abs() + b) + 2.0 ** -133  # bf16's smallest step
+    assert float(ref.abs().mean()) > 2.0 ** -126
+    err = worst(dX, ref, b)
+    say(f"error / bound {err:.3f}")
+    assert err <= 1.0
