@@ -5,6 +5,8 @@
 //   p = softmax over the row's entries of tl_j / tau
 //   lse = ln sum_v exp(z_v / tau),  q_v = exp(z_v / tau - lse)
 //   loss = tau^2 sum_j p_j (ln p_j - z_{idx_j} / tau + lse)
+//        = tau (sum_j p_j (tau ln p_j + r - z_{idx_j}) + (m - r) + tau ln S)
+//     with m = max_v z_v, S = sum_v exp((z_v - m) / tau) and any r
 //   dz_v = gloss tau (q_v - sum_{j: idx_j = v} p_j)
 // A row without entries (or with every entry at -inf) has zero loss and zero
 // gradient, whatever its logits hold.
@@ -22,11 +24,16 @@
 //     and for rows past the registers: S blocks per row leave the maximum
 //     and sum of their chunk in the workspace; a second launch joins the S
 //     pairs and writes the gradient, reading its chunk again.
-// Sums, maxima and the teacher's softmax are f32; exponents are formed as
-// exp2((z - m) log2(e) / tau) from the difference to the row's maximum, so
-// their rounding is relative to the exponent and not to z.  The gradient is
-// rounded once, to the logits' type; entries at the teacher's indices are
-// formed from their own z and written after the rest of the row.
+// Sums, maxima and the teacher's softmax are f32.  Exponents are formed from
+// differences to the row's maximum (the teacher's, too), and the loss from
+// differences to r, the student's largest logit among the teacher's entries,
+// so that no term but the entropy's is negative: their rounding does not know
+// the level that all of a row's logits share.  (With z / tau and lse in place of
+// the differences the loss at tau = 1.5 was 8e-5 off at a level of 300 and 9e-4
+// at 3000; it is 1e-6 to 4e-6 off at each.)  The backward call has only lse,
+// whose own half step, 2^-24 |lse| at most, enters every probability.  The
+// gradient is rounded once, to the logits' type; entries at the teacher's
+// indices are formed from their own z and written after the rest of the row.
 #include <algorithm>
 
 #include "tune.h"
@@ -143,23 +150,25 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2, flo
 }
 
 // The teacher's entries of a row: p_j and idx_j (-1 where the entry does not
-// count) in LDS; mass: whether any entry counts.  One wave, every lane calls.
-// term(j, p_j, ln p_j) is called for every entry with p_j > 0.
+// count) in LDS, and z_j, the student's logits there, where `student` reads
+// them; the result says whether any entry counts.  One wave, every lane calls.
 struct Teacher {
     float p[kMaxK];
+    float z[kMaxK];
     int32_t idx[kMaxK];
 };
-template <typename F>
+template <typename Z, typename F>
 __device__ __forceinline__ bool teacher_softmax(Teacher& th, const int32_t* __restrict__ idx,
                                                 const float* __restrict__ tl, int k, int64_t V,
-                                                float itau, int lane, F term) {
+                                                float itau, int lane, Z student, F term) {
     float m = neg_inf(), bad = 0.0f;
     for (int j = lane; j < k; j += 64) {
         const int32_t id = idx[j];
         const bool ok = id >= 0 && id < V;
-        const float x = ok ? tl[j] * itau : neg_inf();
+        const float x = ok ? tl[j] : neg_inf();
         th.idx[j] = ok ? id : -1;
         th.p[j] = x;
+        student(j, ok ? id : -1);
         m = fmaxf(m, x);
         bad += x != x ? 1.0f : 0.0f;
     }
@@ -168,16 +177,49 @@ __device__ __forceinline__ bool teacher_softmax(Teacher& th, const int32_t* __re
     const bool mass = m > neg_inf() || wave_sum(bad) > 0.0f;
     const float f = finite_max(m);
     float s = 0.0f;
-    for (int j = lane; j < k; j += 64) s += expf(th.p[j] - f);
+    for (int j = lane; j < k; j += 64) s += expf((th.p[j] - f) * itau);
     s = wave_sum(s);
     const float ls = logf(s), is = 1.0f / s;
     for (int j = lane; j < k; j += 64) {
-        const float d = th.p[j] - f;
+        const float d = (th.p[j] - f) * itau;
         const float p = mass ? expf(d) * is : 0.0f;
         if (th.idx[j] >= 0 && p != 0.0f) term(j, p, d - ls);  // NaN included
         th.p[j] = p;
     }
     return mass;
+}
+
+// The teacher's side of the loss: a = sum_j p_j (tau ln p_j + r - z_j) over the
+// entries with p_j > 0 and r, their largest finite z_j (0: none).
+struct TeacherLoss {
+    float a, r;
+    bool mass;
+};
+template <bool BF16>
+__device__ __forceinline__ TeacherLoss teacher_loss(Teacher& th, const int32_t* __restrict__ idx,
+                                                    const float* __restrict__ tl, int k, int64_t V,
+                                                    float tau, float itau, int lane,
+                                                    const char* row) {
+    float ent = 0.0f, r = neg_inf();
+    TeacherLoss t;
+    t.mass = teacher_softmax(
+        th, idx, tl, k, V, itau, lane,
+        [&](int j, int32_t id) { th.z[j] = id >= 0 ? Vec<BF16>::load1(row, id) : 0.0f; },
+        [&](int j, float p, float lp) {
+            ent += p * lp;
+            r = fmaxf(r, th.z[j]);
+        });
+    t.r = finite_max(wave_max(r));
+    float d = 0.0f;
+    for (int j = lane; j < k; j += 64)
+        if (th.p[j] != 0.0f) d += th.p[j] * (t.r - th.z[j]);
+    t.a = wave_sum(tau * ent + d);
+    return t;
+}
+// m, s: the row's maximum and sum.  A row with a NaN, a +inf or nothing but -inf
+// gives NaN, mass on a logit of -inf gives +inf.
+__device__ __forceinline__ float loss_value(float a, float r, float m, float s, float tau) {
+    return tau * (a + (m - r) + tau * logf(s));
 }
 
 // ---------------------------------------------------------------- row form
@@ -189,7 +231,6 @@ __global__ __launch_bounds__(THREADS) void distill_row_kernel(
     typedef Vec<BF16> X;
     constexpr int W = THREADS / 64;
     __shared__ Teacher th;
-    __shared__ float zj[kMaxK];
     __shared__ float wm[W], wsum[W];
     __shared__ int has;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -203,17 +244,10 @@ __global__ __launch_bounds__(THREADS) void distill_row_kernel(
 
     // the last wave also takes the teacher's entries and the student's
     // logits at them (before anything is written: dlogits may be logits)
-    float a = 0.0f;
+    TeacherLoss tls{0.0f, 0.0f, false};
     if (wave == W - 1) {
-        const bool mass = teacher_softmax(
-            th, idx + t * k, tl + t * k, k, V, itau, lane, [&](int j, float p, float lp) {
-                const float z = X::load1(row, th.idx[j]);
-                a += p * (lp - z * itau);
-            });
-        a = wave_sum(a);
-        for (int j = lane; j < k; j += 64)
-            zj[j] = th.idx[j] >= 0 ? X::load1(row, th.idx[j]) : 0.0f;
-        if (lane == 0) has = mass;
+        tls = teacher_loss<BF16>(th, idx + t * k, tl + t * k, k, V, tau, itau, lane, row);
+        if (lane == 0) has = tls.mass;
     }
 
     // The row stays as loaded between the passes: without this the compiler
@@ -248,9 +282,8 @@ __global__ __launch_bounds__(THREADS) void distill_row_kernel(
     for (int w = 1; w < W; ++w) join(m, s, wm[w], wsum[w], c);
     const bool mass = has != 0;
     if (tid == THREADS - 64) {  // first lane of the last wave
-        const float l = m * itau + logf(s);
-        lse[t] = l;
-        loss[t] = mass ? tau * tau * (a + l) : 0.0f;
+        lse[t] = m * itau + logf(s);
+        loss[t] = mass ? loss_value(tls.a, tls.r, m, s, tau) : 0.0f;
     }
     if (!dlogits) return;
 
@@ -284,7 +317,7 @@ __global__ __launch_bounds__(THREADS) void distill_row_kernel(
                     first = first && i >= j;
                     p += th.p[i];
                 }
-            if (first) X::store1(drow, id, (exp2_((zj[j] - fm) * c) * is - p) * g);
+            if (first) X::store1(drow, id, (exp2_((th.z[j] - fm) * c) * is - p) * g);
         }
 }
 
@@ -293,7 +326,7 @@ constexpr int kSplitThreads = 256;
 
 struct SplitWs {
     float* part;  // [T][S][2]: maximum and sum of each chunk
-    float* row;   // [T][2]: sum_j p_j (ln p_j - z_j / tau), and whether there is mass
+    float* row;   // [T][3]: a and r of TeacherLoss, and whether there is mass
 };
 
 __device__ __host__ inline int64_t split_chunk(int64_t V, int S, int E) {
@@ -319,15 +352,12 @@ __global__ __launch_bounds__(kSplitThreads) void distill_stats_kernel(
     const int64_t v1 = std::min<int64_t>(v0 + chunk / X::E, (V + X::E - 1) / X::E);
 
     if (sp == 0 && wave == W - 1) {
-        float a = 0.0f;
-        const bool mass = teacher_softmax(
-            th, idx + t * k, tl + t * k, k, V, itau, lane, [&](int j, float p, float lp) {
-                a += p * (lp - X::load1(row, th.idx[j]) * itau);
-            });
-        a = wave_sum(a);
+        const TeacherLoss tls =
+            teacher_loss<BF16>(th, idx + t * k, tl + t * k, k, V, tau, itau, lane, row);
         if (lane == 0) {
-            ws.row[2 * t] = a;
-            ws.row[2 * t + 1] = mass ? 1.0f : 0.0f;
+            ws.row[3 * t] = tls.a;
+            ws.row[3 * t + 1] = tls.r;
+            ws.row[3 * t + 2] = tls.mass ? 1.0f : 0.0f;
         }
     }
     // four vectors at a time: their loads are in flight together
@@ -380,7 +410,6 @@ __global__ __launch_bounds__(kSplitThreads) void distill_grad_kernel(
     void* dlogits, int64_t ldd) {
     typedef Vec<BF16> X;
     __shared__ Teacher th;
-    __shared__ float zj[kMaxK];
     __shared__ int has;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t t = blockIdx.x / nblk;
@@ -399,9 +428,9 @@ __global__ __launch_bounds__(kSplitThreads) void distill_grad_kernel(
         fm = finite_max(m);
         is = 1.0f / s;
         if (sp == 0 && tid == 0) {
-            const float lv = m * itau + logf(s);
-            lse[t] = lv;
-            loss[t] = ws.row[2 * t + 1] != 0.0f ? tau * tau * (ws.row[2 * t] + lv) : 0.0f;
+            lse[t] = m * itau + logf(s);
+            const float* r = ws.row + 3 * t;
+            loss[t] = r[2] != 0.0f ? loss_value(r[0], r[1], m, s, tau) : 0.0f;
         }
     } else {
         l = lse[t];
@@ -415,7 +444,7 @@ __global__ __launch_bounds__(kSplitThreads) void distill_grad_kernel(
     };
     if (wave == 0) {
         const bool mass = teacher_softmax(th, idx + t * k, tl + t * k, k, V, itau, lane,
-                                          [](int, float, float) {});
+                                          [](int, int32_t) {}, [](int, float, float) {});
         if (lane == 0) has = mass;
     }
     __syncthreads();
@@ -427,7 +456,7 @@ __global__ __launch_bounds__(kSplitThreads) void distill_grad_kernel(
     const float g = (gloss ? gloss[t] : 1.0f) * tau;
     for (int j = tid; j < k; j += kSplitThreads) {
         const int32_t id = th.idx[j];
-        zj[j] = id >= e0 && id < e1 ? X::load1(row, id) : 0.0f;
+        th.z[j] = id >= e0 && id < e1 ? X::load1(row, id) : 0.0f;
     }
     __syncthreads();  // the logits at the teacher's indices are read: dlogits may be logits
     char* drow = static_cast<char*>(dlogits) + t * ldd * X::kBytes;
@@ -462,7 +491,7 @@ __global__ __launch_bounds__(kSplitThreads) void distill_grad_kernel(
                     first = first && i >= j;
                     p += th.p[i];
                 }
-            if (first) X::store1(drow, id, (prob(zj[j]) - p) * g);
+            if (first) X::store1(drow, id, (prob(th.z[j]) - p) * g);
         }
 }
 

@@ -219,7 +219,7 @@ inline int distill_bwd_splits(int64_t T, int64_t V, bool bf16) {
 }
 inline int64_t distill_workspace(int64_t T, int64_t V, bool bf16) {
     const int S = distill_splits(T, V, bf16);
-    return S == 0 ? 0 : T * (2 * S + 2) * 4;
+    return S == 0 ? 0 : T * (2 * S + 3) * 4;
 }
 hipError_t launch_distill(const DistillArgs& a, float* loss, float* lse, void* dlogits,
                           int64_t ldd, void* workspace, hipStream_t s);

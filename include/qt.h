@@ -492,7 +492,11 @@ qt_status qt_matmul_bwd(const uint8_t* packed, const float* scales, int32_t bits
  * qt_distill_topk writes loss and lse, and dlogits unless it is NULL.
  * workspace: qt_distill_topk_workspace_bytes(T, V, lt) bytes (16-byte
  * aligned; may be NULL when that size is 0).
- * qt_distill_topk_bwd writes dlogits alone, from the lse of the former call.
+ * Rounding (f32): loss and the gradient that qt_distill_topk writes are formed
+ * from differences of logits, so that their error does not grow with the level
+ * that a row's logits (or the teacher's) share.
+ * qt_distill_topk_bwd writes dlogits alone, from the lse of the former call, whose
+ * own half step (2^-24 |lse| at most) enters every probability.
  *   1 <= T <= 2^22; 1 <= V < 2^31.
  */
 size_t qt_distill_topk_workspace_bytes(int64_t T, int64_t V, qt_dtype lt);

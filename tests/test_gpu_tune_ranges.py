@@ -9,7 +9,7 @@ import torch
 
 import dequant_matmul_int3_amd as qt
 from tests.gpu_util import DEV, say
-from tests.tune_util import act64, dense, dx_bound, half_step, quantized, worst
+from tests.tune_util import act64, dense, distill_ref, dx_bound, half_step, quantized, worst
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +77,82 @@ def test_tiny_gradients_and_scales():
     err = worst(dX, ref, b)
     say(f"error / bound {err:.3f}")
     assert err <= 1.0
+
+
+# --------------------------------------------------------------- distillation
+def level_bounds(z, idx, tl, tau, gloss=None):
+    """The 64-bit results and bounds that depend on differences of logits only.
+    Relative to U: the row's sum is off by its longest chain of additions (160:
+    16 vectors of 8, and the joins; + 40) and by eight roundings of the exponents, whose
+    magnitude (m - z_v) / tau counts with its weight q_v; p_j by the same of the
+    teacher's exponents and its k / 64 additions per lane.  An error of p_j
+    counts with the terms that it multiplies in the loss."""
+    T, V = z.shape
+    loss, lse, dz, q, P, g = distill_ref(z, idx, tl, tau, gloss)
+    z = z.double()
+    m = z.amax(1, keepdim=True)
+    live = (idx >= 0) & (idx < V)
+    t = tl.double().masked_fill(~live, -math.inf)
+    d = (t - t.amax(1, keepdim=True)) / tau
+    p = torch.softmax(d, 1)
+    on = p > 0
+
+    def only(x):
+        return torch.where(on, x, torch.zeros_like(p))
+
+    zj = z.gather(1, torch.where(live, idx, torch.zeros_like(idx)).long())
+    r = torch.where(on, zj, torch.full_like(zj, -math.inf)).amax(1, keepdim=True)
+    span = torch.where(q > 0, (m - z) / tau, torch.zeros_like(q))
+    es = U * (min(V, 160) + 40 + 8 * (q * span).sum(1))
+    dj = only(d.abs())
+    ep = only(U * (8 * dj + 8 * (p * dj).sum(1, keepdim=True) + 2 * (2 * -(-tl.shape[1] // 64) + 16)))
+    term = only(p.clamp(min=1e-300).log().abs() + (r - zj) / tau)
+    term = term + (m - r) / tau + (lse - m[:, 0] / tau).abs()[:, None] + 1
+    el = tau * tau * ((p * only((ep + 8 * U) * term)).sum(1) + es)
+    top = ep.amax(1, keepdim=True)
+    ez = g.abs() * (q * (es[:, None] + 8 * U * (span + 1)) + P * (top + 4 * U))
+    return loss, lse, dz, el, ez, g.abs() * q
+
+
+def rounded(ref, b, dtype):
+    return b + half_step(dtype) * (ref.abs() + b) + 1e-37
+
+
+FORMS = [(6, 300), (6, 9000), (6, 140000), (140, 9000)]  # row, split, long split, wide row form
+
+
+@pytest.mark.parametrize("T,V", FORMS)
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("level", [0.0, 300.0, -300.0, 3000.0])
+def test_loss_does_not_know_the_logits_level(T, V, dtype, level):
+    # softmax and loss do not change when all of a row's logits are shifted, and
+    # neither may their error; the teacher's have another level
+    k, tau = 32, 1.5
+    z = (rnd((T, V), V, F32, 2.0) + level).to(dtype)
+    idx = torch.randint(0, V, (T, k), generator=torch.Generator().manual_seed(1))
+    idx = idx.to(torch.int32).to(DEV)
+    tl = z.gather(1, idx.long()).float() + 0.05 * rnd((T, k), 9) - 2 * level
+    gl = torch.rand(T, device=DEV)
+    loss, lse, dz = qt.qt_distill_topk(z, idx, tl, tau=tau, gloss=gl, want_dlogits=True)
+    rl, rs, rz, el, ez, gq = level_bounds(z, idx, tl, tau, gl)
+    # the gradient alone knows lse only, with its rounding
+    dz2 = qt.qt_distill_topk_bwd(z, idx, tl, lse, gl, tau=tau)
+    ez2 = ez + gq * (4 * U * (1 + rs.abs()))[:, None]
+    errs = (worst(loss, rl, el), worst(dz, rz, rounded(rz, ez, dtype)),
+            worst(dz2, rz, rounded(rz, ez2, dtype)))
+    say(f"T={T} V={V} {dtype} level {level}: error / bound " + " ".join("%.3f" % e for e in errs) +
+        f"; loss off by {float((loss.double() - rl).abs().max()):.1e}")
+    assert max(errs) <= 1.0
+
+
+@pytest.mark.parametrize("T,V", FORMS)
+@pytest.mark.parametrize("tau", [0.25, 0.5])
+def test_loss_of_a_lowest_logit_at_low_temperature(T, V, tau):
+    # z / tau passes the largest f32 number there, the loss does not
+    z = rnd((T, V), V, F32, 2.0)
+    z[:, 5] = torch.finfo(F32).min
+    idx = torch.arange(5, 13, dtype=torch.int32).repeat(T, 1).to(DEV)
+    tl = rnd((T, 8), 9)
+    loss = qt.qt_distill_topk(z, idx, tl, tau=tau)[0]
+    rl, _, _, el, _, _ = level_bounds(z, idx, tl, tau)
+    assert torch.isfinite(loss).all() and worst(loss, rl, el) <= 1.0
