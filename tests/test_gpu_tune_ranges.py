@@ -79,6 +79,32 @@ def test_tiny_gradients_and_scales():
     assert err <= 1.0
 
 
+@pytest.mark.parametrize("ytype", [BF, F32, "block"])
+def test_input_gradient_adds_little_to_its_rounding(ytype):
+    # in norm: a rounding to f16 is off by at most 2^-11 / sqrt(3) in the mean
+    # square, relative to the value; three of them per term (dY, the scale, its
+    # product with the code), of terms of either sign, add (2^-11)^2 at most to
+    # the square of what the one rounding of dX itself leaves.  (bf16 operands
+    # would add eight times that, which bounds of single values do not see.)
+    B, I, O = 256, 512, 1024
+    w, v = quantized(O, I, 4, 3)
+    x, dy = rnd((B, I), 1, BF), rnd((B, O), 2, BF if ytype == "block" else ytype, 0.1)
+    if ytype == "block":
+        up, vu = quantized(O, I, 3, 4)
+        pre = rnd((2, B, O), 5)
+        dX = qt.qt_ffn_gated_bwd(w, up, pre, dy, x, want_dscales=False)[0]
+        a, da = act64(pre[0].double(), "silu")
+        ref = (dy.double() * pre[1].double() * da) @ dense(w, v, I)
+        ref = ref + (dy.double() * a) @ dense(up, vu, I)
+    else:
+        dX = qt.qt_matmul_bwd(w, dy, x, want_dscales=False)[0]
+        ref = dy.double() @ dense(w, v, I)
+    err = float((dX.double() - ref).norm() / ref.norm())
+    own = float((ref.to(BF).double() - ref).norm() / ref.norm())
+    say(f"dY {ytype}: {err:.4e} off in norm, its own rounding {own:.4e}")
+    assert err ** 2 <= own ** 2 + half_step(torch.float16) ** 2
+
+
 # --------------------------------------------------------------- distillation
 def level_bounds(z, idx, tl, tau, gloss=None):
     """The 64-bit results and bounds that depend on differences of logits only.
