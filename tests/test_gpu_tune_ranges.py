@@ -182,3 +182,25 @@ def test_loss_of_a_lowest_logit_at_low_temperature(T, V, tau):
     loss = qt.qt_distill_topk(z, idx, tl, tau=tau)[0]
     rl, _, _, el, _, _ = level_bounds(z, idx, tl, tau)
     assert torch.isfinite(loss).all() and worst(loss, rl, el) <= 1.0
+
+
+@pytest.mark.parametrize("T,V", FORMS)
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_logits_masked_with_the_lowest_value(T, V, dtype):
+    # half of every row masked with the type's lowest value; bounds of what is
+    # left alone, and proof that they would see a wrong loss or gradient
+    k, tau = 24, 2.0
+    z = rnd((T, V), V, dtype, 2.0)
+    z[:, ::2] = torch.finfo(dtype).min
+    idx = (2 * torch.arange(k, dtype=torch.int32) + 1).repeat(T, 1).to(DEV)
+    tl = rnd((T, k), 4, F32, 3.0)
+    loss, lse, dz = qt.qt_distill_topk(z, idx, tl, tau=tau, want_dlogits=True)
+    dz2 = qt.qt_distill_topk_bwd(z, idx, tl, lse, tau=tau)
+    rl, rs, rz, el, ez, gq = level_bounds(z, idx, tl, tau)
+    ez2 = ez + gq * (4 * U * (1 + rs.abs()))[:, None]
+    errs = (worst(loss, rl, el), worst(lse, rs, el / tau ** 2 + 4 * U * (1 + rs.abs())),
+            worst(dz, rz, rounded(rz, ez, dtype)), worst(dz2, rz, rounded(rz, ez2, dtype)))
+    say(f"T={T} V={V} {dtype}: error / bound " + " ".join("%.3f" % e for e in errs))
+    assert max(errs) <= 1.0
+    assert (dz[:, ::2] == 0).all() and (dz2[:, ::2] == 0).all()
+    assert worst(loss * 1.01, rl, el) > 1 and worst(dz * 1.02, rz, rounded(rz, ez, dtype)) > 1
