@@ -225,7 +225,7 @@ __device__ __forceinline__ float loss_value(float a, float r, float m, float s, 
 // ---------------------------------------------------------------- row form
 template <bool BF16, int THREADS, int NV>
 __global__ __launch_bounds__(THREADS) void distill_row_kernel(
-    const void* logits, int64_t V, int64_t ld, const int32_t* __restrict__ idx,
+    const void* logits, int64_t T, int64_t V, int64_t ld, const int32_t* __restrict__ idx,
     const float* __restrict__ tl, int k, float tau, float* __restrict__ loss,
     float* __restrict__ lse, const float* __restrict__ gloss, void* dlogits, int64_t ldd) {
     typedef Vec<BF16> X;
@@ -234,7 +234,8 @@ __global__ __launch_bounds__(THREADS) void distill_row_kernel(
     __shared__ float wm[W], wsum[W];
     __shared__ int has;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int64_t t = blockIdx.x;
+    const int64_t t = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    if (t >= T) return;
     const char* row = static_cast<const char*>(logits) + t * ld * X::kBytes;
     const float itau = 1.0f / tau, c = itau * kLog2e;
 
@@ -498,8 +499,9 @@ __global__ __launch_bounds__(kSplitThreads) void distill_grad_kernel(
 template <bool BF16, int THREADS, int NV>
 void run_row(const DistillArgs& a, float* loss, float* lse, void* dlogits, int64_t ldd,
              hipStream_t s) {
-    hipLaunchKernelGGL((distill_row_kernel<BF16, THREADS, NV>), dim3((unsigned)a.T),
-                       dim3(THREADS), 0, s, a.logits, a.V, a.ld, a.idx, a.tl, a.k, a.tau, loss,
+    const GridRows g = grid_rows(a.T, THREADS);
+    hipLaunchKernelGGL((distill_row_kernel<BF16, THREADS, NV>), dim3(g.x, g.y),
+                       dim3(THREADS), 0, s, a.logits, a.T, a.V, a.ld, a.idx, a.tl, a.k, a.tau, loss,
                        lse, a.gloss, dlogits, ldd);
 }
 

@@ -52,7 +52,8 @@ template <bool BF16, bool BLOCKED>
 __global__ __launch_bounds__(256) void planes_kernel(const void* __restrict__ X, int64_t T,
                                                      int64_t D, int64_t Dp,
                                                      uint16_t* __restrict__ P) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t i =
+        ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
     const int64_t Tp = BLOCKED ? (T + 15) / 16 * 16 : T;
     if (i >= Tp * (Dp / 8)) return;
     int64_t t, d0;
@@ -377,7 +378,7 @@ hipError_t small_bits(const SmallArgs& a, bool bf16, bool staged, hipStream_t s)
 }
 
 // ---------------------------------------------------------------- tile form
-constexpr int kThreads = 512;
+constexpr int kThreads = kTileThreads;
 
 struct TileArgs {
     QMat gate, up;
@@ -629,7 +630,6 @@ __global__ __launch_bounds__(256) void ffn_join_kernel(const float* __restrict__
 template <int GB, int UB, int NP, int MT, int NT>
 hipError_t run_tile(const TileArgs& a, hipStream_t s) {
     const int64_t nb = a.mblk * a.nblk * a.splits;
-    if (nb > 0x7FFFFFFF) return hipErrorInvalidValue;
     hipLaunchKernelGGL((ffn_tile_kernel<GB, UB, NP, MT, NT>), dim3((unsigned)nb),
                        dim3(kThreads), 0, s, a);
     return hipGetLastError();
@@ -646,9 +646,8 @@ hipError_t tile_bits(const TileArgs& a, hipStream_t s) {
 hipError_t launch_x_planes(const void* X, bool bf16, bool blocked, int64_t T, int64_t D,
                            uint16_t* planes, hipStream_t s) {
     const int64_t Dp = pad_to(D, kGroup);
-    const int64_t nb = cdiv((blocked ? pad_to(T, 16) : T) * (Dp / 8), 256);
-    if (nb > 0x7FFFFFFF) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)nb), block(256);
+    const GridRows g = grid_rows(x_planes_blocks(T, D, blocked), 256);
+    const dim3 grid(g.x, g.y), block(256);
 #define QT_PLANES(B, K) \
     hipLaunchKernelGGL((planes_kernel<B, K>), grid, block, 0, s, X, T, D, Dp, planes)
     if (bf16) {
@@ -664,7 +663,8 @@ hipError_t launch_x_planes(const void* X, bool bf16, bool blocked, int64_t T, in
 
 hipError_t launch_ffn_gated(const FfnArgs& a, void* workspace, hipStream_t s) {
     const FfnPlan p = ffn_plan(a.T, a.D, a.F, a.bf16);
-    const int64_t G = cdiv(a.D, kGroup), Dp = G * kGroup;
+    if (!ffn_fits(p, a.T, a.F)) return hipErrorInvalidValue;
+    const int64_t G = cdiv(a.D, kGroup);
     const int np = ffn_pieces(a.bf16);
     const uint16_t* A = static_cast<const uint16_t*>(a.X);
     char* w = static_cast<char*>(workspace);
@@ -695,7 +695,6 @@ hipError_t launch_ffn_gated(const FfnArgs& a, void* workspace, hipStream_t s) {
         e = p.mt == 1 ? tile_bits<3, 1, 8>(ta, s) : tile_bits<3, 2, 8>(ta, s);
     if (e != hipSuccess || p.splits == 1) return e;
     const int64_t n = a.T * a.F, nb = cdiv(n, 1024);
-    if (nb > 0x7FFFFFFF) return hipErrorInvalidValue;
     if (a.bf16)
         hipLaunchKernelGGL((ffn_join_kernel<true>), dim3((unsigned)nb), dim3(256), 0, s, ta.part,
                            p.splits, n, a.act, a.H, a.pre);

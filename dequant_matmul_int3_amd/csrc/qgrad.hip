@@ -44,7 +44,7 @@
 namespace qt {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = kTileThreads;
 constexpr int kNT = kTileN / 16;
 
 typedef f32x4_t f32x4_u __attribute__((aligned(4)));
@@ -725,7 +725,6 @@ __global__ __launch_bounds__(kThreads) void ds_tile_kernel(const DsArgs a, const
 template <bool F32, int MT>
 hipError_t run_dx(const DxArgs& a, hipStream_t s) {
     const int64_t nb = a.mblk * a.nblk * a.splits;
-    if (nb > 0x7FFFFFFF) return hipErrorInvalidValue;
     hipLaunchKernelGGL((dx_tile_kernel<F32, MT>), dim3((unsigned)nb), dim3(kThreads), 0, s, a);
     return hipGetLastError();
 }
@@ -733,7 +732,6 @@ hipError_t run_dx(const DxArgs& a, hipStream_t s) {
 template <int NP, int MT, int NT>
 hipError_t run_ds(const DsArgs& a, hipStream_t s) {
     const int64_t nb = a.oblk * a.tblk * a.splits;
-    if (nb > 0x7FFFFFFF) return hipErrorInvalidValue;
     for (int m = 0; m < a.src.nmat; ++m) {
         if (a.mat[m].bits == 3)
             hipLaunchKernelGGL((ds_tile_kernel<3, NP, MT, NT>), dim3((unsigned)nb),
@@ -749,7 +747,6 @@ hipError_t run_ds(const DsArgs& a, hipStream_t s) {
 hipError_t sum_parts(const float* part, int64_t stride, int splits, int64_t n, int accumulate,
                      bool bf16, void* out, hipStream_t s) {
     const int64_t nb = cdiv(n, 1024);
-    if (nb > 0x7FFFFFFF) return hipErrorInvalidValue;
     if (bf16)
         hipLaunchKernelGGL((sum_parts_kernel<true>), dim3((unsigned)nb), dim3(256), 0, s, part,
                            stride, splits, n, accumulate, out);
@@ -764,6 +761,7 @@ hipError_t sum_parts(const float* part, int64_t stride, int splits, int64_t n, i
 hipError_t launch_bwd(const BwdArgs& a, void* workspace, hipStream_t s) {
     const bool want_dx = a.dX != nullptr, want_ds = a.dscales[0] != nullptr;
     const BwdPlan p = bwd_plan(a.T, a.I, a.O, a.nmat, a.bf16, want_dx, want_ds);
+    if (!bwd_fits(p, a.T, a.I, a.O, want_dx, want_ds)) return hipErrorInvalidValue;
     char* w = static_cast<char*>(workspace);
     const int64_t G = cdiv(a.I, kGroup), Op = pad_to(a.O, 4 * kTileK);
     const GradSrc src{a.nmat, a.act, a.dy_bf16, a.dY, a.pre, a.T, a.O};

@@ -22,6 +22,19 @@ inline int64_t pad_to(int64_t a, int64_t b) { return cdiv(a, b) * b; }
 // Workspace sections start at multiples of 256 bytes.
 inline int64_t sect(int64_t bytes) { return pad_to(bytes, 256); }
 
+// A launch has fewer than 2^32 threads along a dimension.  Kernels that a call of
+// documented size may give more blocks than that take them in rows of equal
+// length (their last row may be a few blocks too long); the others are checked
+// before anything is enqueued.
+inline bool launch_fits(int64_t blocks, int64_t threads) { return blocks * threads < (1LL << 32); }
+struct GridRows {
+    uint32_t x, y;
+};
+inline GridRows grid_rows(int64_t blocks, int64_t threads) {
+    const int64_t rows = cdiv(blocks, ((1LL << 32) - 1) / threads);
+    return {(uint32_t)cdiv(blocks, rows), (uint32_t)rows};
+}
+
 // A packed matrix and its bits (3 or 4).
 struct QMat {
     const uint8_t* packed;
@@ -44,6 +57,12 @@ inline int64_t x_planes_bytes(int64_t T, int64_t D, bool bf16, bool blocked) {
     return sect(ffn_pieces(bf16) * (blocked ? pad_to(T, 16) : T) * pad_to(D, kGroup) * 2);
 }
 
+// Blocks of the launch that writes them: 256 threads, eight values each.
+inline int64_t x_planes_blocks(int64_t T, int64_t D, bool blocked) {
+    return cdiv((blocked ? pad_to(T, 16) : T) * (pad_to(D, kGroup) / 8), 256);
+}
+
+constexpr int kTileThreads = 512;  // of every block tile
 constexpr int kTileN = 128;  // input columns of a block tile of the input gradient
 constexpr int kTileK = 64;   // inner elements of a step
 // 16-token tiles per wave of the 8-wave block tile: 1, 2 or 4
@@ -119,6 +138,16 @@ inline FfnPlan ffn_plan(int64_t T, int64_t D, int64_t F, bool bf16) {
     return p;
 }
 
+inline int64_t ffn_tile_blocks(const FfnPlan& p, int64_t T, int64_t F) {
+    return cdiv(T, 128 * p.mt) * cdiv(F, 8 * p.nt) * p.splits;
+}
+// Launches that join partial sums: four values a thread.
+inline bool join_fits(int64_t n) { return launch_fits(cdiv(n, 1024), 256); }
+inline bool ffn_fits(const FfnPlan& p, int64_t T, int64_t F) {
+    return p.small || (launch_fits(ffn_tile_blocks(p, T, F), kTileThreads) &&
+                       (p.splits == 1 || join_fits(T * F)));
+}
+
 struct FfnArgs {
     QMat gate, up;
     int64_t F, D;
@@ -191,6 +220,20 @@ inline BwdPlan bwd_plan(int64_t T, int64_t I, int64_t O, int nmat, bool bf16, bo
     }
     p.bytes = off;
     return p;
+}
+inline int64_t dx_tile_blocks(const BwdPlan& p, int64_t T, int64_t I) {
+    return cdiv(T, 128 * p.dx_mt) * cdiv(I, kTileN) * p.dx_splits;
+}
+inline int64_t ds_tile_blocks(const BwdPlan& p, int64_t O) {
+    return cdiv(O, 16 * p.ds_nt) * p.ds_tb * p.ds_splits;
+}
+inline bool bwd_fits(const BwdPlan& p, int64_t T, int64_t I, int64_t O, bool want_dx,
+                     bool want_ds) {
+    if (want_dx && !(launch_fits(dx_tile_blocks(p, T, I), kTileThreads) &&
+                     (p.dx_splits == 1 || join_fits(T * I))))
+        return false;
+    return !want_ds || (launch_fits(ds_tile_blocks(p, O), kTileThreads) &&
+                        (p.ds_tb == 1 || join_fits(O * cdiv(I, kGroup))));
 }
 hipError_t launch_bwd(const BwdArgs& a, void* workspace, hipStream_t s);
 

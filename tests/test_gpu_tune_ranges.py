@@ -9,7 +9,8 @@ import torch
 
 import dequant_matmul_int3_amd as qt
 from tests.gpu_util import DEV, say
-from tests.tune_util import act64, dense, distill_ref, dx_bound, half_step, quantized, worst
+from tests.tune_util import (act64, dense, distill_ref, dx_bound, ffn_ref, half_step, quantized,
+                             worst)
 
 pytestmark = pytest.mark.gpu
 
@@ -204,3 +205,60 @@ def test_logits_masked_with_the_lowest_value(T, V, dtype):
     assert max(errs) <= 1.0
     assert (dz[:, ::2] == 0).all() and (dz2[:, ::2] == 0).all()
     assert worst(loss * 1.01, rl, el) > 1 and worst(dz * 1.02, rz, rounded(rz, ez, dtype)) > 1
+
+
+# -------------------------------------------------------------- largest sizes
+def room(gib):
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < gib * 2 ** 30:
+        pytest.skip(f"needs {gib} GiB of free device memory")
+
+
+def test_most_tokens_through_the_input_planes():
+    # 2^22 tokens of 8256: the planes' launch has more than 2^32 threads (69 GB
+    # of inputs and as much of planes)
+    room(140)
+    T, D, F, n = 1 << 22, 8256, 16, 300
+    say(f"block {T} x {D}")
+    (gate, vg), (up, vu) = quantized(F, D, 3, 1), quantized(F, D, 4, 2)
+    x = torch.zeros((T, D), dtype=BF, device=DEV)
+    at = [0, T // 2 - n // 2, T - n]
+    for i, t in enumerate(at):
+        x[t:t + n] = rnd((n, D), i, BF)
+    h = qt.qt_ffn_gated(gate, up, x)
+    for t in at:
+        ref, _, _, b, _, _ = ffn_ref(x[t:t + n], dense(gate, vg, D), dense(up, vu, D), "silu", BF)
+        assert worst(h[t:t + n], ref, b) <= 1.0
+        h[t:t + n] = 0
+    assert not h.any()
+    del x, h
+    torch.cuda.empty_cache()
+
+
+def test_most_rows_of_logits():
+    # 2^22 rows that take 1024 threads each: 2^32 threads (137 GB of logits, whose
+    # gradient replaces them)
+    room(140)
+    T, V, n = 1 << 22, 16392, 300
+    say(f"loss {T} x {V}")
+    z = torch.zeros((T, V), dtype=BF, device=DEV)
+    idx = torch.full((T, 2), -1, dtype=torch.int32, device=DEV)
+    tl = torch.zeros((T, 2), device=DEV)
+    at = [0, T // 2 - n // 2, T - n]
+    want = []
+    for i, t in enumerate(at):
+        z[t:t + n] = rnd((n, V), i, BF, 2.0)
+        idx[t:t + n] = torch.randint(0, V, (n, 2), device=DEV, dtype=torch.int32)
+        tl[t:t + n] = rnd((n, 2), i + 9)
+        want.append(level_bounds(z[t:t + n], idx[t:t + n], tl[t:t + n], 1.0))
+    loss, lse, _ = qt.qt_distill_topk(z, idx, tl, dlogits=z)
+    for t, (rl, rs, rz, el, ez, _) in zip(at, want):
+        assert worst(loss[t:t + n], rl, el) <= 1.0
+        assert worst(z[t:t + n], rz, rounded(rz, ez, BF)) <= 1.0
+        assert worst(lse[t:t + n], rs, el + 4 * U * (1 + rs.abs())) <= 1.0
+        loss[t:t + n], lse[t:t + n], z[t:t + n] = 0, math.log(V), 0
+    # rows without entries: no loss, no gradient, the lse of equal logits
+    assert not loss.any() and float((lse - math.log(V)).abs().max()) <= 200 * U
+    assert float(z.view(torch.int32).amax()) == 0 == float(z.view(torch.int32).amin())
+    del z, want
+    torch.cuda.empty_cache()
