@@ -37,9 +37,11 @@ qt_status workspace_ok(const void* workspace, size_t ws_bytes, size_t need) {
     return aligned(workspace, 16) ? QT_OK : QT_ERR_ALIGN;
 }
 
-// bf16 rows of whole groups are read in place, with 16-byte loads.
-bool rows_aligned(const void* X, qt_dtype xt, int64_t D) {
-    return aligned(X, xt == QT_BF16 && D % kGroup == 0 ? 16 : (uintptr_t)esize(xt));
+// A few bf16 rows of whole groups may be read in place, with 16-byte loads;
+// everything else copies X first, from its elements' alignment.
+uintptr_t x_alignment(qt_dtype xt, int64_t T, int64_t D) {
+    const bool in_place = xt == QT_BF16 && D % kGroup == 0 && qt::ffn_small(T, true);
+    return in_place ? 16 : (uintptr_t)esize(xt);
 }
 
 }  // namespace
@@ -64,7 +66,7 @@ qt_status qt_ffn_gated(const uint8_t* gate_packed, const float* gate_scales, int
     const qt_status st = workspace_ok(workspace, ws_bytes, need);
     if (st != QT_OK) return st;
     if (!aligned(gate_packed, 16) || !aligned(up_packed, 16) || !aligned(gate_scales, 4) ||
-        !aligned(up_scales, 4) || !rows_aligned(X, xt, D) ||
+        !aligned(up_scales, 4) || !aligned(X, x_alignment(xt, T, D)) ||
         !aligned(H, (uintptr_t)esize(xt)) || !aligned(pre, 4))
         return QT_ERR_ALIGN;
     const int64_t G = qt_groups(D), e = esize(xt);
@@ -106,7 +108,7 @@ qt_status qt_ffn_gated_bwd(const uint8_t* gate_packed, const float* gate_scales,
     if (!aligned(gate_packed, 16) || !aligned(up_packed, 16) || !aligned(gate_scales, 4) ||
         !aligned(up_scales, 4) || !aligned(pre, 4) || !aligned(dH, ea) || !aligned(dX, ea) ||
         !aligned(dgate_scales, 4) || !aligned(dup_scales, 4) ||
-        (want_ds && !rows_aligned(X, xt, D)))
+        (want_ds && !aligned(X, ea)))
         return QT_ERR_ALIGN;
     const int64_t G = qt_groups(D), e = esize(xt);
     const Buf out[4] = {{dX, T * D * e}, {dgate_scales, F * G * 4}, {dup_scales, F * G * 4},
@@ -141,7 +143,7 @@ qt_status qt_matmul_bwd(const uint8_t* packed, const float* scales, int32_t bits
     if (st != QT_OK) return st;
     if (!aligned(packed, 16) || !aligned(scales, 4) || !aligned(dY, (uintptr_t)esize(yt)) ||
         !aligned(dX, (uintptr_t)esize(xt)) || !aligned(dscales, 4) ||
-        (dscales && !rows_aligned(X, xt, I)))
+        (dscales && !aligned(X, (uintptr_t)esize(xt))))
         return QT_ERR_ALIGN;
     const int64_t G = qt_groups(I);
     const Buf out[3] = {{dX, B * I * esize(xt)}, {dscales, O * G * 4}, {workspace, (int64_t)need}};

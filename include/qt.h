@@ -409,9 +409,9 @@ qt_status qt_moe_layer(const float* X, int64_t T, int64_t D, int64_t F, const fl
  *   pre  f32 [2][T][F] (g, then u; what qt_ffn_gated_bwd needs), or NULL
  * Both types take the exact codes and inputs with f32 group sums and scales:
  * g and u within 1e-5 of sum_i |w_fi X_ti|.
- *   packed 16-byte aligned; X 16-byte aligned where xt is QT_BF16 and D a
- *   multiple of 64 (small calls read its rows in place), else at its elements'
- *   alignment; 1 <= T <= 2^22; 1 <= D, F <= 2^20.
+ *   packed 16-byte aligned; X 16-byte aligned where xt is QT_BF16, D a multiple
+ *   of 64 and T <= 64 (such calls may read its rows in place), else at its
+ *   elements' alignment; 1 <= T <= 2^22; 1 <= D, F <= 2^20.
  *   workspace: qt_ffn_gated_workspace_bytes(T, D, F, xt) bytes (16-byte
  *   aligned; may be NULL when that size is 0).  Calls that may overlap in
  *   time need a workspace each (also: graphs captured over one workspace must
@@ -442,7 +442,8 @@ qt_status qt_ffn_gated(const uint8_t* gate_packed, const float* gate_scales, int
  * largest keep 11 bits, smaller ones are off by at most 2^-39 and 2^-36 of it.
  * f32: products and sums in f32.  The scales' gradients are f32 throughout:
  * exact codes and inputs, f32 dg and du.
- *   Alignment and sizes as qt_ffn_gated; workspace:
+ *   packed 16-byte aligned, all else at its elements' alignment; sizes as
+ *   qt_ffn_gated; workspace:
  *   qt_ffn_gated_bwd_workspace_bytes(T, D, F, xt, dX wanted, scales wanted).
  */
 size_t qt_ffn_gated_bwd_workspace_bytes(int64_t T, int64_t D, int64_t F, qt_dtype xt,
