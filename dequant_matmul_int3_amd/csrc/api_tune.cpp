@@ -165,7 +165,7 @@ qt_status distill_ok(const void* logits, qt_dtype lt, int64_t T, int64_t V, int6
     if (T < 1 || T > qt::kTuneMaxTokens || V < 1 || V >= qt::kDistillMaxV || ldl < V ||
         ldl >= qt::kDistillMaxV || (dlogits && (ldd < V || ldd >= qt::kDistillMaxV)))
         return QT_ERR_SHAPE;
-    if (k < 1 || k > qt::kDistillMaxK || !(tau > 0.0f) || !(tau < __builtin_inff()))
+    if (k < 1 || k > qt::kDistillMaxK || !(tau >= qt::kDistillMinTau && tau <= qt::kDistillMaxTau))
         return QT_ERR_ARG;
     const uintptr_t e = (uintptr_t)esize(lt);
     if (!aligned(logits, e) || !aligned(dlogits, e) || !aligned(idx, 4) || !aligned(tlogits, 4) ||

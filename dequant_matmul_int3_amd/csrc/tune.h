@@ -15,6 +15,8 @@ constexpr int kCUs = 256;                  // compute units of an MI355X
 constexpr int64_t kTuneMaxDim = 1 << 20;   // D, F, O, I of these calls
 constexpr int64_t kTuneMaxTokens = 1 << 22;
 constexpr int kDistillMaxK = 1024;
+// 1 / tau, log2(e) / tau and tau times a sum of logarithms are all f32 numbers
+constexpr float kDistillMinTau = 0x1p-100f, kDistillMaxTau = 0x1p100f;
 constexpr int64_t kDistillMaxV = 1LL << 31;  // row strides, too
 
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }

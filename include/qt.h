@@ -488,8 +488,8 @@ qt_status qt_matmul_bwd(const uint8_t* packed, const float* scales, int32_t bits
  *   logits [T x V] of type lt with rows ldl >= V elements apart; dlogits
  *   likewise with ldd; columns past V are neither read nor written.  dlogits
  *   may be logits itself (same stride): the gradient then replaces them.
- *   idx [T x k] int32, tlogits [T x k] f32; 1 <= k <= 1024; tau > 0 finite;
- *   loss, lse [T] f32.
+ *   idx [T x k] int32, tlogits [T x k] f32; 1 <= k <= 1024;
+ *   2^-100 <= tau <= 2^100; loss, lse [T] f32.
  * qt_distill_topk writes loss and lse, and dlogits unless it is NULL.
  * workspace: qt_distill_topk_workspace_bytes(T, V, lt) bytes (16-byte
  * aligned; may be NULL when that size is 0).

@@ -1,5 +1,5 @@
-// Drives the validation layer of the tuning calls through alignments that it
-// accepts and refuses, over the stubs of tune_stubs.cpp.
+// Drives the validation layer of the tuning calls through alignments and
+// temperatures that it accepts and refuses, over the stubs of tune_stubs.cpp.
 #include <cstdint>
 #include <cstdio>
 #include <initializer_list>
@@ -39,8 +39,23 @@ static int lin(int64_t B, int64_t I, qt_dtype xt, uintptr_t xo) {
                          at<char>(3) + xo, xt, B, at<char>(4), at<float>(5), 0, at<char>(6),
                          qt_matmul_bwd_workspace_bytes(B, I, 64, xt, 1, 1), nullptr);
 }
+static int loss(float tau, bool bwd) {
+    if (bwd)
+        return qt_distill_topk_bwd(at<char>(0), QT_BF16, 4, 64, 64, at<int32_t>(1), at<float>(2), 3,
+                                   tau, at<float>(4), nullptr, at<char>(3), 64, nullptr);
+    return qt_distill_topk(at<char>(0), QT_F32, 4, 64, 64, at<int32_t>(1), at<float>(2), 3, tau,
+                           at<float>(4), at<float>(5), nullptr, at<char>(3), 64, nullptr, 0, nullptr);
+}
 
 int main() {
+    // temperatures whose inverse (times log2 e) is no f32 number, or whose product
+    // with a logarithm is none, would give NaN
+    for (bool bwd : {false, true}) {
+        for (float tau : {0x1p-149f, 1e-39f, 2e-39f, 0x1.fffffep-101f, 0x1.000002p100f, 0x1p127f, -1.0f,
+                          0.0f, __builtin_inff(), __builtin_nanf("")})
+            expect("tau", loss(tau, bwd), QT_ERR_ARG);
+        for (float tau : {0x1p-100f, 1e-4f, 1.0f, 100.0f, 0x1p100f}) expect("tau", loss(tau, bwd), QT_OK);
+    }
     // only forward calls that may read rows of whole groups in place want 16 bytes
     for (int T : {1, 4, 64}) {
         expect("small", ffn(T, 128, QT_BF16, 8), QT_ERR_ALIGN);

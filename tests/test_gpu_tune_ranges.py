@@ -207,6 +207,24 @@ def test_logits_masked_with_the_lowest_value(T, V, dtype):
     assert worst(loss * 1.01, rl, el) > 1 and worst(dz * 1.02, rz, rounded(rz, ez, dtype)) > 1
 
 
+@pytest.mark.parametrize("T,V", FORMS)
+@pytest.mark.parametrize("tau", [2.0 ** -100, 1e-4, 100.0, 2.0 ** 60, 2.0 ** 100])
+def test_temperatures(T, V, tau):
+    z = rnd((T, V), V, F32, 2.0)
+    idx = torch.randint(0, V, (T, 9), generator=torch.Generator().manual_seed(2))
+    idx = idx.to(torch.int32).to(DEV)
+    tl = rnd((T, 9), 9)
+    loss, lse, dz = qt.qt_distill_topk(z, idx, tl, tau=tau, want_dlogits=True)
+    rl, rs, rz, el, ez, _ = level_bounds(z, idx, tl, tau)
+    if tau == 2.0 ** 100:  # tau^2 times any loss here passes the largest f32
+        assert torch.isinf(loss).all() and (loss > 0).all()
+    else:
+        assert worst(loss, rl, el + 1e-37) <= 1.0
+    assert worst(dz, rz, rounded(rz, ez, F32)) <= 1.0
+    assert worst(lse, rs, 8 * U * (1 + rs.abs()) + 200 * U) <= 1.0
+    say(f"tau {tau} V={V}: loss {float(loss[0]):.4g}")
+
+
 # ------------------------------------------------------------------ alignment
 @pytest.mark.parametrize("T", [4, 64, 65, 300])
 def test_rows_at_an_odd_element(T):
