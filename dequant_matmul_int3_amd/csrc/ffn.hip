@@ -565,6 +565,7 @@ __global__ __launch_bounds__(kThreads) void ffn_tile_kernel(const TileArgs a) {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 tl[(4 * h4 + r) * kRow + nt * 16 + l16] = acc[mt][nt][r];
+        lds_wave_sync();
 #pragma unroll
         for (int i = 0; i < NT / 2; ++i) {
             const int k = i * 64 + lane, tt = k / (2 * NT), qd = k % (2 * NT);
@@ -591,6 +592,7 @@ __global__ __launch_bounds__(kThreads) void ffn_tile_kernel(const TileArgs a) {
                 else store4(static_cast<float*>(a.H) + o, h, left);
             }
         }
+        lds_wave_sync();  // the next 16 tokens take their place
     }
 }
 
