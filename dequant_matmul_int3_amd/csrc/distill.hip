@@ -37,6 +37,7 @@
 #include <algorithm>
 
 #include "tune.h"
+#include "wave_reduce.h"
 
 namespace qt {
 namespace {
@@ -123,18 +124,6 @@ struct Vec {
         }
     }
 };
-
-// Reductions over a wave, every lane gets the result (fixed order).
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
-    return v;
-}
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
-    return v;
-}
 
 // fmaxf drops a NaN; the sum over the row brings it back, since
 // exp2(NaN - m) is NaN.  m = -inf (nothing but -inf seen so far) is replaced

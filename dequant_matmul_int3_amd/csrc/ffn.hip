@@ -148,8 +148,8 @@ __global__ __launch_bounds__(1024) void ffn_small_kernel(const SmallArgs a) {
         for (int mt = 0; mt < MT; ++mt) acc[x][mt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
     struct Chunk {
-        RowGroup<GB, false> g;
-        RowGroup<UB, false> u;
+        RowGroup<GB> g;
+        RowGroup<UB> u;
         float sg, su;
     };
     // four groups of the lane's row, one per lane row; past the row a valid

@@ -40,6 +40,7 @@
 #include "lds_barrier.h"
 #include "tune.h"
 #include "unpack.h"
+#include "wave_reduce.h"
 
 namespace qt {
 namespace {
@@ -75,11 +76,6 @@ __device__ __forceinline__ float load_dy(const GradSrc& s, int64_t at) {
 // blocks leave the largest magnitude of their part of the scales (bf16 calls).
 constexpr int kMaxParts = 64;
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
-    return v;
-}
 // 2^(top - floor(log2 m)), and 1 for m = 0; the exponent is kept where the
 // factor and its inverse are normal numbers.
 __device__ __forceinline__ float range_factor(float m, int top) {

@@ -22,20 +22,6 @@ struct Quarter {
     uint32_t a, b;
 };
 
-// Quarter q of group `grp` (24 or 32 bytes, 4-byte aligned).
-__device__ __forceinline__ Quarter load_quarter(const uint8_t* __restrict__ grp, int q, int bits) {
-    Quarter r;
-    if (bits == 3) {
-        r.a = *reinterpret_cast<const uint32_t*>(grp + 4 * q);
-        r.b = *reinterpret_cast<const uint32_t*>(grp + 16 + 4 * (q >> 1));
-    } else {
-        const u32x2_t w = *reinterpret_cast<const u32x2_t*>(grp + 8 * q);
-        r.a = w.x;
-        r.b = w.y;
-    }
-    return r;
-}
-
 // int3: u = v + 4 of the quarter's codes, one per byte: word 0 holds codes
 // 0 1 4 5, word 1 codes 2 3 6 7, word 2 codes 8 9 12 13, word 3 codes
 // 10 11 14 15.  hsel picks the quarter's two high-plane bytes (0x0C010C00 for
@@ -229,25 +215,18 @@ __device__ __forceinline__ void transpose_rows(uint32_t (&v)[4]) {
     v[3] = d[1];
 }
 
-template <bool STREAM, typename T>
-__device__ __forceinline__ T load_stream(const T* p) {
-    if constexpr (STREAM) return __builtin_nontemporal_load(p);
-    else return *p;
-}
-
 // One lane's whole group of a row.  Where the four lane rows of a wave hold
 // four consecutive groups of the same 16 matrix rows, quarters() exchanges
 // them: lane row h gets quarter h of all four groups.
-// STREAM: the weights are read once per call (non-temporal loads).
-template <int BITS, bool STREAM>
+template <int BITS>
 struct RowGroup;
-template <bool STREAM>
-struct RowGroup<3, STREAM> {
+template <>
+struct RowGroup<3> {
     u32x2_t w[3];
     __device__ __forceinline__ void load(const uint8_t* __restrict__ p) {
 #pragma unroll
         for (int i = 0; i < 3; ++i)
-            w[i] = load_stream<STREAM>(reinterpret_cast<const u32x2_t*>(p) + i);
+            w[i] = reinterpret_cast<const u32x2_t*>(p)[i];
     }
     __device__ __forceinline__ void quarters(Quarter (&q)[4]) const {
         uint32_t a[4] = {w[0].x, w[0].y, w[1].x, w[1].y};
@@ -258,13 +237,13 @@ struct RowGroup<3, STREAM> {
         for (int j = 0; j < 4; ++j) q[j] = Quarter{a[j], b[j]};
     }
 };
-template <bool STREAM>
-struct RowGroup<4, STREAM> {
+template <>
+struct RowGroup<4> {
     u32x4_t w[2];
     __device__ __forceinline__ void load(const uint8_t* __restrict__ p) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            w[i] = load_stream<STREAM>(reinterpret_cast<const u32x4_t*>(p) + i);
+            w[i] = reinterpret_cast<const u32x4_t*>(p)[i];
     }
     __device__ __forceinline__ void quarters(Quarter (&q)[4]) const {
         uint32_t a[4] = {w[0].x, w[0].z, w[1].x, w[1].z};
@@ -289,7 +268,7 @@ struct RowFeed {
     const float* s;
     int G, h;
     bool second, four;  // this lane's matrix; whether its groups are int4
-    RowGroup<B1, false> r;  // B1 == B2
+    RowGroup<B1> r;  // B1 == B2
     u32x2_t w[4];           // else: both formats' groups in 8-byte pieces
     float rs;
     Quarter q[4];
