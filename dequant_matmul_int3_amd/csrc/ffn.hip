@@ -26,7 +26,7 @@
 // scaled by the f32 scale (two FMAs per matrix instruction): weights rounded to
 // bf16(s v) would save them (1.08 against 1.35 ms at 4096 x 5120 x 2 17408) but
 // leave the pre-activations 4e-3 off, and with them the f32 gradients of the
-// scales.  That shape runs at 1080 TFLOP/s (1.5 ms with pre written), the
+// scales.  That shape takes 1.41 ms (1030 TFLOP/s), 1.49 with pre written, the
 // matrix cores busy 43 % of the cycles; the FMAs and the unpacking bound it.
 #include <algorithm>
 

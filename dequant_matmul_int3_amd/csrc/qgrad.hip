@@ -8,13 +8,13 @@
 //
 // Input gradient.  A matrix product with the weights' rows as its inner axis:
 // a block of 8 waves owns 128 MT tokens x 128 inputs (MT 1 or 2: with 4 the
-// registers had no room for the weights' loads four steps ahead, 1.76 against
-// 1.54 ms) and walks the rows of both matrices 64 at a time.  dY is first written as one padded plane in
-// operand blocks; the weights are unpacked once per block into LDS row by row
-// and read back as matrix operands.
+// registers have no room for the weights' loads four steps ahead, 1.65 against
+// 1.50 ms) and walks the rows of both matrices 64 at a time.  dY is first
+// written as one padded plane in operand blocks; the weights are unpacked once
+// per block into LDS row by row and read back as matrix operands.
 //   bf16: both operands are rounded to f16, whose eight times finer step keeps
-//   the result within its own bf16 rounding (operands in bf16 left it 1.7 times
-//   as far off).  Exact powers of two bring them into f16's range and are taken
+//   the result within its own bf16 rounding (1.69e-3 off in norm, of which the
+//   rounding alone makes 1.66e-3; operands in bf16 left it 1.7 times as far off).  Exact powers of two bring them into f16's range and are taken
 //   back from the sums: every token's dY is scaled by its largest magnitude to
 //   2^14 .. 2^15, the scales of both matrices by the largest of them to 2^11 ..
 //   2^12.  Gradients within 2^28 of their token's largest and scales within 2^25
@@ -24,8 +24,8 @@
 //   elements are rows 4h .. 4h+3 and 16+4h .. 16+4h+3 of a 32-row step, and the
 //   dY plane is written in that order.
 //   f32: both stay f32, on the f32 matrix instructions.
-// 4096 tokens, 2 x 17408 rows of 5120: 1.55 ms (940 TFLOP/s) and 0.39 ms for
-// the plane.
+// 4096 tokens, 2 x 17408 rows of 5120: 1.92 ms, of which the plane takes 0.38
+// and the tiles about 1.5 (1.62 under a kernel trace).
 //
 // Scale gradient.  The forward product once more, group by group: the exact
 // codes times the inputs (three exact bf16 pieces of an f32 input) give each
@@ -33,8 +33,9 @@
 // summed over the tokens.  dY is held in registers for the whole walk over the
 // groups.  Nothing is rounded below f32, and the weights' gradient never
 // exists.  Token blocks leave partial sums that a last launch adds in order.
-// The same shape: 0.83 ms per matrix (880 TFLOP/s), bound as the forward tile
-// by the FMAs and the unpacking beside the matrix instructions.
+// The same shape: 1.71 ms for both matrices (860 TFLOP/s; each 0.87 ms under a
+// kernel trace), bound as the forward tile by the FMAs and the unpacking beside
+// the matrix instructions.
 #include <algorithm>
 
 #include "lds_barrier.h"

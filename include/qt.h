@@ -462,6 +462,8 @@ qt_status qt_ffn_gated_bwd(const uint8_t* gate_packed, const float* gate_scales,
  *   dY [B x O] of type yt, X [B x I] of type xt (any pair of types)
  * dX, dscales (not both), X without dscales may be NULL; roundings,
  * accumulate, alignment and sizes (B, I, O as T, D, F) as qt_ffn_gated_bwd.
+ * xt chooses the input gradient's arithmetic: with QT_BF16 an f32 dY is rounded
+ * to f16 for it, too; with QT_F32 nothing is rounded below f32.
  */
 size_t qt_matmul_bwd_workspace_bytes(int64_t B, int64_t I, int64_t O, qt_dtype xt,
                                      int32_t want_dx, int32_t want_dscales);
