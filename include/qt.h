@@ -408,7 +408,8 @@ qt_status qt_moe_layer(const float* X, int64_t T, int64_t D, int64_t F, const fl
  *   X [T x D] of type xt; H [T x F] of type xt, rounded once at the end
  *   pre  f32 [2][T][F] (g, then u; what qt_ffn_gated_bwd needs), or NULL
  * Both types take the exact codes and inputs with f32 group sums and scales:
- * g and u within 1e-5 of sum_i |w_fi X_ti|.
+ * g and u within 1e-5 of sum_i |w_fi X_ti| for D <= 8192, in proportion to D
+ * above (up to ceil(D/64) f32 additions in a row).
  *   packed 16-byte aligned; X 16-byte aligned where xt is QT_BF16, D a multiple
  *   of 64 and T <= 64 (such calls may read its rows in place), else at its
  *   elements' alignment; 1 <= T <= 2^22; 1 <= D, F <= 2^20.

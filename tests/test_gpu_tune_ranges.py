@@ -9,8 +9,8 @@ import torch
 
 import dequant_matmul_int3_amd as qt
 from tests.gpu_util import DEV, say
-from tests.tune_util import (act64, dense, distill_ref, dx_bound, ffn_ref, half_step, quantized,
-                             worst)
+from tests.tune_util import (SUM, act64, dense, distill_ref, dx_bound, ffn_ref, half_step,
+                             quantized, worst)
 
 pytestmark = pytest.mark.gpu
 
@@ -249,6 +249,24 @@ def test_rows_at_an_odd_element(T):
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     want, got = qt.qt_matmul_bwd(gate, dh, x), qt.qt_matmul_bwd(gate, off(dh), off(x), dX=off(x))
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ------------------------------------------------- ends of the documented sizes
+@pytest.mark.parametrize("D", [7168, 8192, 1 << 17, 1 << 20])
+@pytest.mark.parametrize("T,dtype", [(1, BF), (65, BF), (600, BF), (70, F32)])
+def test_sums_of_equal_terms(T, dtype, D):
+    # equal terms make every addition of a long sum round the same way: 2^-24 of
+    # the sum for each of its groups at most, which is 1e-5 for 8192 inputs
+    F = 24
+    c = torch.ones((F, D), dtype=torch.int8, device=DEV)
+    s = torch.linspace(0.01, 0.02, F, device=DEV)[:, None].expand(F, D // 64).contiguous()
+    w = (qt.qt_pack_i3(c), s, 3)
+    x = torch.full((T, D), 1.171875, dtype=dtype, device=DEV)
+    _, pre = qt.qt_ffn_gated(w, w, x, want_pre=True)
+    ref = (s[:, 0].double() * D * 1.171875).expand(T, F)
+    err = float(((pre.double() - ref) / ref).abs().max())
+    say(f"T={T} D={D} {dtype}: {err:.1e}")
+    assert err <= SUM * max(1.0, D / 8192)
 
 
 # -------------------------------------------------------------- largest sizes
