@@ -9,8 +9,8 @@ import torch
 
 import dequant_matmul_int3_amd as qt
 from tests.gpu_util import DEV, say
-from tests.tune_util import (SUM, act64, dense, distill_ref, dx_bound, ffn_ref, half_step,
-                             quantized, worst)
+from tests.tune_util import (SUM, act64, dense, distill_ref, dx_bound, ffn_ref, grads_ref,
+                             half_step, quantized, scale_grad, worst)
 
 pytestmark = pytest.mark.gpu
 
@@ -252,6 +252,22 @@ def test_rows_at_an_odd_element(T):
 
 
 # ------------------------------------------------- ends of the documented sizes
+def matrix(O, I, bits, seed):
+    """A matrix of random codes and scales, drawn on the device, and its codes."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    half = 4 if bits == 3 else 8
+    c = torch.randint(-half, half, (O, I), generator=g, device=DEV, dtype=torch.int8)
+    s = torch.rand((O, -(-I // 64)), generator=g, device=DEV) * 0.02 + 0.001
+    p = (qt.qt_pack_i3 if bits == 3 else qt.qt_pack_i4)(c)
+    v = torch.nn.functional.pad(c.double(), (0, s.shape[1] * 64 - I)).view(O, -1, 64)
+    return (p, s, bits), v
+
+
+def drawn(shape, seed, dtype):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return torch.randn(shape, device=DEV, generator=g).to(dtype)
+
+
 @pytest.mark.parametrize("D", [7168, 8192, 1 << 17, 1 << 20])
 @pytest.mark.parametrize("T,dtype", [(1, BF), (65, BF), (600, BF), (70, F32)])
 def test_sums_of_equal_terms(T, dtype, D):
@@ -323,4 +339,93 @@ def test_most_rows_of_logits():
     assert not loss.any() and float((lse - math.log(V)).abs().max()) <= 200 * U
     assert float(z.view(torch.int32).amax()) == 0 == float(z.view(torch.int32).amin())
     del z, want
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("T,D,F,bits,dtype", [
+    (1, 1 << 20, 33, (3, 4), BF),
+    (1, 1 << 20, 33, (4, 3), F32),
+    (70, 1 << 20, 20, (3, 3), BF),
+    (30, 1 << 20, 20, (4, 4), F32),
+    (3, 100, 1 << 20, (4, 3), BF),
+    (70, 64, 1 << 20, (3, 4), F32),
+    (1 << 22, 65, 40, (3, 3), BF),
+    ((1 << 21) + 1, 70, 24, (4, 4), F32),
+])
+def test_longest_axes(T, D, F, bits, dtype):
+    # random signs keep the long sums' errors far under SUM of their terms
+    room(40)
+    say(f"block {T} x {D} x {F} {dtype}")
+    (gate, vg), (up, vu) = matrix(F, D, bits[0], 1), matrix(F, D, bits[1], 2)
+    x, dh = drawn((T, D), 3, dtype), drawn((T, F), 4, dtype)
+    h, pre = qt.qt_ffn_gated(gate, up, x, want_pre=True)
+    dx, dsg, dsu = qt.qt_ffn_gated_bwd(gate, up, pre, dh, x)
+    wg, wu = dense(gate, vg, D), dense(up, vu, D)
+    t = slice(max(0, T - 5000), T)
+    rh, g, u, bh, bg, bu = ffn_ref(x[t], wg, wu, "silu", dtype)
+    errs = [worst(pre[0, t], g, bg), worst(pre[1, t], u, bu), worst(h[t], rh, bh)]
+    dg, du, eg, eu = grads_ref(pre[0, t].double(), pre[1, t].double(), dh[t].double(), "silu")
+    ref = dg @ wg + du @ wu
+    b = dx_bound([(dg, eg, wg), (du, eu, wu)], dtype, dtype)
+    errs.append(worst(dx[t], ref, b + half_step(dtype) * (ref.abs() + b) + 1e-30))
+    o = slice(max(0, F - 5000), F)
+    dg, du, eg, eu = grads_ref(pre[0, :, o].double(), pre[1, :, o].double(), dh[:, o].double(), "silu")
+    X = x.double()
+    for got, dy, e, v in ((dsg, dg, eg, vg[o]), (dsu, du, eu, vu[o])):
+        bound = scale_grad(SUM * dy.abs() + e, X.abs(), v.abs()) + 1e-30
+        errs.append(worst(got[o], scale_grad(dy, X, v), bound))
+    say("  error / bound: " + " ".join("%.3f" % e for e in errs))
+    assert max(errs) <= 1.0
+
+
+def test_one_matrix_and_one_tensor_twice():
+    w, _ = matrix(128, 128, 3, 1)
+    x = rnd((200, 128), 1, BF)
+    h, pre = qt.qt_ffn_gated(w, w, x, want_pre=True)
+    assert torch.equal(pre[0], pre[1])
+    got, want = qt.qt_ffn_gated_bwd(w, w, pre, x, x), qt.qt_ffn_gated_bwd(w, w, pre, x.clone(), x)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("T,V", [(3, 1), (200, 3), (2, 9000), (130, 9000)])
+def test_most_entries_on_few_indices(T, V):
+    k = 1024
+    z = rnd((T, V), 5, F32, 2.0)
+    idx = torch.randint(0, min(V, 3), (T, k), generator=torch.Generator().manual_seed(1))
+    idx, tl = idx.to(torch.int32).to(DEV), rnd((T, k), 6)
+    loss, lse, dz = qt.qt_distill_topk(z, idx, tl, want_dlogits=True)
+    rl, rs, rz, el, ez, gq = level_bounds(z, idx, tl, 1.0)
+    # an index's p is a sum of up to 1024 in a row, at most 1 in all
+    assert worst(loss, rl, el) <= 1.0 and worst(dz, rz, rounded(rz, ez + k * U, F32)) <= 1.0
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_widest_rows(dtype):
+    # 2^31 - 1 logits, all 0 but the last thousand; f32 sums of 2^31 terms: each
+    # thread adds 32768 of them, 32 at a time (1024 additions in a row), then
+    # the 256 chunks are joined
+    room(40)
+    T, V, n = 2, (1 << 31) - 1, 1000
+    say(f"loss {T} x {V} {dtype}")
+    z = torch.zeros((T, V), dtype=dtype, device=DEV)
+    z[1, -n:] = rnd((n,), 3, dtype, 3.0) + 20
+    idx = torch.tensor([[0, V - 1, V - 2], [V - 1, 5, V - 3]], dtype=torch.int32, device=DEV)
+    tl = rnd((2, 3), 4)
+    loss, lse, _ = qt.qt_distill_topk(z, idx, tl)
+    rest = torch.tensor([math.log(V), math.log(V - n)], dtype=torch.float64, device=DEV)
+    tail = torch.logsumexp(torch.cat([z[1, -n:].double(), rest[1:]]), 0)
+    rs = torch.stack([rest[0], tail])
+    p = torch.softmax(tl.double(), 1)
+    zi = torch.stack([z[r][idx[r].long()] for r in range(T)]).double()
+    rl = (p * (p.log() - zi + rs[:, None])).sum(1)
+    e = (1024 + 256 + 64) * U + 8 * U * 32
+    assert worst(lse, rs, torch.full_like(rs, e)) <= 1.0
+    assert worst(loss, rl, torch.full_like(rl, 2 * e)) <= 1.0
+    rz = torch.exp(zi - rs[:, None]) - p
+    middle = torch.exp(-rs)
+    qt.qt_distill_topk_bwd(z, idx, tl, lse, dlogits=z)
+    got = torch.stack([z[r][idx[r].long()] for r in range(T)])
+    assert worst(got, rz, rounded(rz, e + 16 * U, dtype)) <= 1.0
+    assert worst(z[:, V // 2], middle, rounded(middle, middle * (2 * e + 64 * U), dtype)) <= 1.0
+    del z
     torch.cuda.empty_cache()
