@@ -429,3 +429,62 @@ def test_widest_rows(dtype):
     assert worst(z[:, V // 2], middle, rounded(middle, middle * (2 * e + 64 * U), dtype)) <= 1.0
     del z
     torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------------ workspaces
+@pytest.mark.parametrize("T,dtype", [(1, F32), (20, BF), (70, BF), (70, F32), (700, BF)])
+def test_what_a_workspace_held_does_not_matter(T, dtype):
+    # of exactly the size asked for, full of NaN, and reused by the next call
+    D, F, V = 700, 520, 9001
+    (gate, _), (up, _) = matrix(F, D, 3, 1), matrix(F, D, 4, 2)
+    x, dh, z = rnd((T, D), 1, dtype), rnd((T, F), 2, dtype), rnd((T, V), 3, dtype)
+    idx = torch.randint(0, V, (T, 9), generator=torch.Generator().manual_seed(4))
+    idx, tl = idx.to(torch.int32).to(DEV), rnd((T, 9), 5)
+    xt = qt.QT_BF16 if dtype == BF else qt.QT_F32
+    sizes = [qt.qt_ffn_gated_workspace_bytes(T, D, F, xt),
+             qt.qt_ffn_gated_bwd_workspace_bytes(T, D, F, xt),
+             qt.qt_matmul_bwd_workspace_bytes(T, D, F, xt),
+             qt.qt_distill_topk_workspace_bytes(T, V, xt)]
+    buf = torch.full((max(sizes) + 256,), 0xFF, dtype=torch.uint8, device=DEV)
+
+    def run(ws):
+        h, pre = qt.qt_ffn_gated(gate, up, x, want_pre=True, workspace=ws(0))
+        return [h, pre, *qt.qt_ffn_gated_bwd(gate, up, pre, dh, x, workspace=ws(1)),
+                *qt.qt_matmul_bwd(gate, dh, x, workspace=ws(2)),
+                *qt.qt_distill_topk(z, idx, tl, want_dlogits=True, workspace=ws(3))]
+
+    want = run(lambda n: None)
+    for _ in range(2):
+        got = run(lambda n: buf[:max(sizes[n], 16)])
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert (buf[max(sizes):] == 0xFF).all(), "wrote past the workspace"
+
+
+def test_gradient_in_place_in_a_graph():
+    for T, V, dtype in ((4, 300, F32), (3, 40000, BF), (140, 9000, BF)):
+        z, out = rnd((T, V), 1, dtype), torch.empty((T, V), dtype=dtype, device=DEV)
+        idx = torch.randint(0, V, (T, 9), generator=torch.Generator().manual_seed(4))
+        idx, tl = idx.to(torch.int32).to(DEV), rnd((T, 9), 5)
+
+        def run():
+            loss, lse, _ = qt.qt_distill_topk(out, idx, tl, dlogits=out)
+            return loss, lse
+
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            out.copy_(z)
+            run()
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            captured = run()
+        for r in range(3):
+            z.copy_(rnd((T, V), 10 + r, dtype))
+            want = qt.qt_distill_topk(z, idx, tl, want_dlogits=True)
+            out.copy_(z)
+            g.replay()
+            torch.cuda.synchronize()
+            for a, b in zip((*captured, out), want):
+                assert torch.equal(a, b), f"T={T} V={V}: replay {r} differs"
