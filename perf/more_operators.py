@@ -252,18 +252,27 @@ def _unrows(b, bits):
     return b - (1 << (bits - 1))
 
 
+def _blocks(codes, bits):
+    """A view of a page's bytes as blocks of eight tokens, [pages, H, block, pair of tokens, token
+    of the pair, group, 4 values of the group, byte]."""
+    n, H, P, w = codes.shape
+    shape = (n, H, P // 8, w * 8 // (bits * GROUP), 16, 4)
+    if bits == 8:
+        return codes.view(*shape, 2, 4).permute(0, 1, 2, 5, 6, 3, 4, 7)
+    return codes.view(*shape, 2, 2).permute(0, 1, 2, 5, 7, 3, 4, 6)  # a pair's bytes alternate
+
+
 def _octets(c, bits):
-    """Codes [pages, H, P, 64 G] -> a page's bytes, as [.., P, 8 bits G]: blocks of eight tokens,
-    in them group, 4 values of the group, token."""
+    """Codes [pages, H, P, 64 G] -> the pages' bytes [pages, H, P, 8 bits G] in blocks."""
     n, H, P, w = c.shape
-    b = _rows(c.view(n, H, P // 8, 8, w // GROUP, 16, 4), bits)
-    return b.permute(0, 1, 2, 4, 5, 3, 6).reshape(n, H, P, w * bits // 8)
+    codes = torch.empty((n, H, P, w * bits // 8), dtype=torch.uint8, device=c.device)
+    _blocks(codes, bits).copy_(_rows(c.view(n, H, P // 8, 4, 2, w // GROUP, 16, 4), bits))
+    return codes
 
 
 def _unoctets(b, bits):
-    n, H, P, w = b.shape
-    b = b.view(n, H, P // 8, w * 8 // (bits * GROUP), 16, 8, bits // 2).permute(0, 1, 2, 5, 3, 4, 6)
-    return _unrows(b.reshape(n, H, P, w), bits)
+    n, H, P, _ = b.shape
+    return _unrows(_blocks(b, bits).reshape(n, H, P, -1), bits)
 
 
 def _plain_write(st):
@@ -277,9 +286,8 @@ def _plain_write(st):
         scales[at, :, t] = s
         b = _rows(c, bits)
         if octets:
-            n, H, _, w = codes.shape
-            view = codes.view(n, H, P // 8, w * 8 // (bits * GROUP), 16, 8, bits // 2)
-            view[at, :, t // 8, :, :, t % 8] = b.view(b.shape[0], H, -1, 16, bits // 2)
+            _blocks(codes, bits)[at, :, t // 8, t // 2 % 4, t % 2] = b.view(
+                *b.shape[:2], -1, 16, bits // 2)
         else:
             codes[at, :, t] = b
 
@@ -470,8 +478,10 @@ def _held64(part, octets, page, t, d):
     j = torch.arange(d, device=codes.device)
     if octets:
         # the byte of value j of token t, counted from the page's first
-        block = (t // 8)[..., None] * (G * 16 * 8 * W)
-        byte = block + ((j // 64) * 16 + j % 64 // 4) * 8 * W + (t % 8)[..., None] * W + j % 4 * bits // 8
+        t = t[..., None]
+        byte = (t // 8 * G * 16 + j // 64 * 16 + j % 64 // 4) * 8 * W
+        byte = byte + (t % 8 * 4 + j % 4 if bits == 8 else t % 8 // 2 * 4 + j % 4 // 2 * 2 + t % 2)
+        t = t[..., 0]
     else:
         byte = t[..., None] * w + j * bits // 8
     b = codes.view(n, H, P * w)[page[..., None, None], torch.arange(H, device=codes.device)[:, None],
