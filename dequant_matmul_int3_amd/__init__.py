@@ -13,7 +13,9 @@ from .qt import (QtError, QT_BF16, QT_F32, lib, qt_groups, qt_hessian_diag,
                  qt_gptq_proxy_workspace_bytes, qt_moe_layer, qt_moe_layer_workspace_bytes,
                  qt_ffn_gated, qt_ffn_gated_bwd, qt_ffn_gated_workspace_bytes,
                  qt_ffn_gated_bwd_workspace_bytes, qt_matmul_bwd, qt_matmul_bwd_workspace_bytes,
-                 qt_distill_topk, qt_distill_topk_bwd, qt_distill_topk_workspace_bytes)
+                 qt_distill_topk, qt_distill_topk_bwd, qt_distill_topk_workspace_bytes,
+                 qt_kv_bytes, qt_kv_cache, qt_kv_write, qt_kv_read, qt_attn_decode,
+                 qt_attn_decode_workspace_bytes)
 
 __all__ = ["QtError", "QT_BF16", "QT_F32", "lib", "qt_groups", "qt_hessian_diag",
            "qt_hessian_diag_noalloc", "qt_hessian_scratch_bytes", "qt_hessian_workspace_bytes", "qt_matmul_i3", "qt_matmul_i4", "qt_matvec_i3",
@@ -25,4 +27,6 @@ __all__ = ["QtError", "QT_BF16", "QT_F32", "lib", "qt_groups", "qt_hessian_diag"
            "qt_gptq_proxy_workspace_bytes", "qt_moe_layer", "qt_moe_layer_workspace_bytes",
            "qt_ffn_gated", "qt_ffn_gated_bwd", "qt_ffn_gated_workspace_bytes",
            "qt_ffn_gated_bwd_workspace_bytes", "qt_matmul_bwd", "qt_matmul_bwd_workspace_bytes",
-           "qt_distill_topk", "qt_distill_topk_bwd", "qt_distill_topk_workspace_bytes"]
+           "qt_distill_topk", "qt_distill_topk_bwd", "qt_distill_topk_workspace_bytes",
+           "qt_kv_bytes", "qt_kv_cache", "qt_kv_write", "qt_kv_read", "qt_attn_decode",
+           "qt_attn_decode_workspace_bytes"]

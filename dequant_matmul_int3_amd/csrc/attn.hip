@@ -1,0 +1,102 @@
+// Attention over the quantized cache (attn.h): bf16 queries, and the join of
+// the chunks' parts.
+#include "attn.h"
+
+namespace qt {
+namespace {
+
+// One block per (sequence, query head): the chunks' maxima, sums and value
+// sums, 4 values a thread, the chunks dealt to 256 / (W / 4) threads each and
+// joined in LDS, always in the same order.
+template <int G, bool F32>
+__global__ __launch_bounds__(256) void attn_join_kernel(const AttnKernelArgs x) {
+    constexpr int W = G * kGroup, COLS = W / 4, ROWS = 256 / COLS;
+    const AttnArgs& a = x.a;
+    const int64_t row = blockIdx.x;
+    const int b = (int)(row / a.q_heads);
+    const int64_t reach = a.table_pages * a.c.page;
+    const int n = (int)min<int64_t>(max(a.lens[b], 0), reach);
+    const int lo = a.window > 0 && a.window < n ? (int)(n - a.window) : 0;
+    const int first = lo & ~(kAttnTile - 1);
+    // the first chunk is there even when empty
+    const int parts = max(1, (int)(((int64_t)n - first + x.chunk - 1) / x.chunk));
+    const float* part = x.part + row * x.splits * (W + 2);
+    const int tid = threadIdx.x, col = tid % COLS, who = tid / COLS;
+
+    __shared__ float wmax[4];
+    float mx = -INFINITY;
+    for (int i = tid; i < parts; i += 256) mx = fmaxf(mx, part[(int64_t)i * (W + 2) + W]);
+    mx = wave_max(mx);
+    if ((tid & 63) == 0) wmax[tid >> 6] = mx;
+    __syncthreads();
+    mx = fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3]));
+    const float base = mx == -INFINITY ? 0.0f : mx;
+
+    __shared__ float red[ROWS][W + 1];
+    float v[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.0f;
+    if (who < ROWS) {
+#pragma unroll 4
+        for (int i = who; i < parts; i += ROWS) {
+            const float* p = part + (int64_t)i * (W + 2);
+            const float e = __builtin_amdgcn_exp2f(p[W] - base);
+            sum += e * p[W + 1];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = __builtin_fmaf(e, p[4 * col + k], v[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) red[who][4 * col + k] = v[k];
+        if (col == 0) red[who][W] = sum;
+    }
+    __syncthreads();
+    if (tid >= W) return;
+    float y = 0.0f;
+    sum = 0.0f;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        y += red[r][tid];
+        sum += red[r][W];
+    }
+    const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+    if (tid < a.c.dim) {
+        if constexpr (F32)
+            static_cast<float*>(a.out)[row * a.c.dim + tid] = y * inv;
+        else
+            static_cast<__bf16*>(a.out)[row * a.c.dim + tid] = (__bf16)(y * inv);
+    }
+    if (tid == 0 && a.lse) a.lse[row] = (mx + __log2f(sum)) * 0.6931471805599453f;
+}
+
+template <bool F32>
+hipError_t join(const AttnKernelArgs& k, hipStream_t s) {
+    const unsigned grid = (unsigned)((int64_t)k.a.B * k.a.q_heads);
+    switch (k.a.c.groups) {
+        case 1: attn_join_kernel<1, F32><<<grid, 256, 0, s>>>(k); break;
+        case 2: attn_join_kernel<2, F32><<<grid, 256, 0, s>>>(k); break;
+        case 3: attn_join_kernel<3, F32><<<grid, 256, 0, s>>>(k); break;
+        default: attn_join_kernel<4, F32><<<grid, 256, 0, s>>>(k); break;
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attn_bf16(const AttnKernelArgs& k, hipStream_t s) {
+    return attn_bits<false>(k, s);
+}
+
+hipError_t launch_attn_decode(const AttnArgs& a, void* workspace, hipStream_t s) {
+    const AttnPlan p = attn_plan(a.B, a.c.heads, a.q_heads, a.c.dim, a.table_pages, a.c.page,
+                                 a.window);
+    AttnKernelArgs k{a, p.chunk, p.splits, (a.q_heads / a.c.heads + 15) / 16, 0, 0,
+                     static_cast<float*>(workspace)};
+    // x / page = (x * mul >> 32) >> sh for x < 2^31: mul = ceil(2^(32 + sh) / page)
+    // with 2^sh < page <= 2^(sh + 1), so that mul < 2^32 and the error x / 2^(32 + sh) is
+    // below 1 / page
+    while ((int64_t(2) << k.page_sh) < a.c.page) ++k.page_sh;
+    k.page_mul = (uint32_t)(((uint64_t(1) << (32 + k.page_sh)) + a.c.page - 1) / a.c.page);
+    hipError_t e = a.bf16 ? launch_attn_bf16(k, s) : launch_attn_f32(k, s);
+    if (e != hipSuccess || p.splits == 1) return e;
+    return a.bf16 ? join<false>(k, s) : join<true>(k, s);
+}
+
+}  // namespace qt

@@ -1,0 +1,90 @@
+// Internal interface between the C-ABI layer of the serving calls
+// (api_serve.cpp) and their kernels, and the host rules that choose forms and
+// size workspaces.  Arguments here are already validated.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "qt_internal.h"
+
+namespace qt {
+
+constexpr int64_t kServeMaxTokens = int64_t(1) << 22;
+constexpr int64_t kKvMaxSlots = (int64_t(1) << 31) - 1;  // pages * page
+constexpr int64_t kKvMaxPage = 65536;
+constexpr int64_t kKvMaxHeads = 1024;
+constexpr int64_t kKvMaxDim = 256;
+constexpr int64_t kAttnMaxBatch = 65535;
+constexpr int64_t kAttnMaxGroupHeads = 256;  // query heads per key-value head
+
+// A paged cache: codes [pages][heads][page][groups * 8 bits] and scales
+// [pages][heads][page][groups] of the keys and of the values.
+struct KvCache {
+    uint8_t* kc;
+    float* ks;
+    int kbits;
+    uint8_t* vc;
+    float* vs;
+    int vbits;
+    int64_t pages;
+    int page, heads, dim, groups;
+};
+
+struct KvRows {  // of one call: [T x heads x dim], rows ld elements apart
+    const void* K;
+    int64_t ldk;
+    const void* V;
+    int64_t ldv;
+    bool bf16;
+};
+hipError_t launch_kv_write(const KvCache& c, const KvRows& r, const int32_t* slots, int64_t T,
+                           hipStream_t s);
+hipError_t launch_kv_read(const KvCache& c, const int32_t* slots, int64_t R, void* K, void* V,
+                          bool bf16, hipStream_t s);
+
+struct AttnArgs {
+    KvCache c;
+    const void* Q;  // [B x q_heads x dim], rows ldq elements apart
+    int64_t ldq;
+    bool bf16;
+    int B, q_heads;
+    const int32_t* table;  // [B x table_pages]
+    int64_t table_pages;
+    const int32_t* lens;   // [B]
+    int64_t window;        // 0: everything
+    float scale;
+    void* out;             // [B x q_heads x dim]
+    float* lse;            // [B x q_heads] or null
+};
+
+// How the positions are cut: chunks of `chunk` positions, `splits` of them at
+// most; more than one leaves partial results in the workspace.
+struct AttnPlan {
+    int chunk, splits;
+    int64_t bytes;
+};
+inline AttnPlan attn_plan(int64_t B, int64_t heads, int64_t q_heads, int64_t dim,
+                          int64_t table_pages, int64_t page, int64_t window) {
+    constexpr int64_t kStep = 128;      // four waves of 32 positions
+    constexpr int64_t kBlocks = 1024;   // four blocks for every CU
+    int64_t span = table_pages * page;
+    // a window may start inside a tile of 32
+    if (window) span = std::min(span, window + 31);
+    const int64_t tiles = (q_heads / heads + 15) / 16;
+    const int64_t rows = B * heads * tiles;
+    const int64_t want = std::max<int64_t>(1, (kBlocks + rows - 1) / rows);
+    int64_t chunk = (span + want - 1) / want;
+    chunk = (chunk + kStep - 1) / kStep * kStep;
+    chunk = std::min<int64_t>(std::max<int64_t>(chunk, 2 * kStep), 4096);
+    AttnPlan p;
+    p.chunk = (int)chunk;
+    p.splits = (int)std::max<int64_t>(1, (span + chunk - 1) / chunk);
+    const int64_t G = (dim + kGroup - 1) / kGroup;
+    p.bytes = p.splits == 1 ? 0 : B * q_heads * p.splits * (G * kGroup + 2) * 4;
+    return p;
+}
+hipError_t launch_attn_decode(const AttnArgs& a, void* workspace, hipStream_t s);
+
+}  // namespace qt

@@ -91,6 +91,20 @@ _SIGS = {
     "qt_distill_topk_bwd": (C.c_int, [C.c_void_p, C.c_int, C.c_int64, C.c_int64, C.c_int64,
                                       C.c_void_p, C.c_void_p, C.c_int32, C.c_float, C.c_void_p,
                                       C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p]),
+    "qt_kv_bytes": (C.c_int64, [C.c_int64] * 4 + [C.c_int32]),
+    "qt_kv_write": (C.c_int, [C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int, C.c_int64,
+                              C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32, C.c_void_p,
+                              C.c_void_p, C.c_int32, C.c_int64, C.c_int64, C.c_int64, C.c_int64,
+                              C.c_void_p]),
+    "qt_kv_read": (C.c_int, [C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_int32, C.c_void_p,
+                             C.c_void_p, C.c_int32, C.c_int64, C.c_int64, C.c_int64, C.c_int64,
+                             C.c_void_p, C.c_void_p, C.c_int, C.c_void_p]),
+    "qt_attn_decode_workspace_bytes": (C.c_size_t, [C.c_int64] * 7),
+    "qt_attn_decode": (C.c_int, [C.c_void_p, C.c_int64, C.c_int, C.c_int64, C.c_int64, C.c_void_p,
+                                 C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p, C.c_int32,
+                                 C.c_int64, C.c_int64, C.c_int64, C.c_int64, C.c_void_p,
+                                 C.c_int64, C.c_void_p, C.c_int64, C.c_float, C.c_void_p,
+                                 C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
     "qt_quantize_g64_i4": (C.c_int, [C.c_void_p, C.c_int64, C.c_int64, C.c_void_p, C.c_int32,
                                      C.c_float, C.c_float, C.c_void_p, C.c_void_p, C.c_void_p,
                                      C.c_void_p]),
@@ -686,3 +700,149 @@ def qt_distill_topk_bwd(logits, idx, tlogits, lse, gloss=None, tau: float = 1.0,
                                          tau, _ptr(lse), _ptr(gloss), _ptr(dlogits), ldd,
                                          _stream(stream, dev)), "qt_distill_topk_bwd")
     return dlogits
+
+
+# ------------------------------------- quantized key-value cache and attention
+def qt_kv_bytes(n_pages: int, page: int, heads: int, dim: int, bits: int) -> int:
+    return int(lib().qt_kv_bytes(n_pages, page, heads, dim, bits))
+
+
+def qt_kv_cache(n_pages: int, page: int, heads: int, dim: int, k_bits: int = 8, v_bits: int = 8,
+                device="cuda"):
+    """An empty cache -> (k, v), each (codes [n_pages, heads, page, bytes] uint8,
+    scales [n_pages, heads, page, G] f32, bits): zeros, which no call requires."""
+    parts = []
+    for bits in (k_bits, v_bits):
+        n = qt_kv_bytes(n_pages, page, heads, dim, bits)
+        if n == 0:
+            raise ValueError("no such cache: page a multiple of 16, dim up to 256, bits 4 or 8")
+        codes = torch.zeros((n_pages, heads, page, n // (n_pages * heads * page)),
+                            dtype=torch.uint8, device=device)
+        scales = torch.zeros((n_pages, heads, page, -(-dim // 64)), dtype=torch.float32,
+                             device=device)
+        parts.append((codes, scales, bits))
+    return parts[0], parts[1]
+
+
+def _kv(k, v, dim):
+    """(n_pages, page, heads) of a cache for heads of dim values, checked."""
+    if not 1 <= dim <= 256:
+        raise ValueError("dim must be 1 to 256")
+    for (codes, scales, bits), what in ((k, "k"), (v, "v")):
+        if bits not in (4, 8):
+            raise ValueError(f"{what}: bits must be 4 or 8")
+        if scales.dim() != 4 or scales.dtype != torch.float32 or scales.shape[3] != -(-dim // 64):
+            raise ValueError(f"{what}: scales must be float32 [n_pages, heads, page, ceil({dim}/64)]")
+        if codes.dtype != torch.uint8 or codes.numel() != scales.numel() * 8 * bits:
+            raise ValueError(f"{what}: codes do not match the scales' shape and {bits} bits")
+    if k[1].shape != v[1].shape:
+        raise ValueError("k and v must have the same pages, heads and page size")
+    n_pages, heads, page, _ = k[1].shape
+    return n_pages, page, heads
+
+
+def _kv_args(k, v, n_pages, page, heads, dim):
+    return (_ptr(k[0]), _ptr(k[1]), k[2], _ptr(v[0]), _ptr(v[1]), v[2], n_pages, page, heads, dim)
+
+
+def _tokens(t, what):
+    """Distance in elements between the tokens of a [T, heads, dim] tensor whose
+    tokens are contiguous (a slice of a projection's rows, say)."""
+    if t.dim() != 3:
+        raise ValueError(f"{what} must be [T, heads, dim]")
+    T, H, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d):
+        raise ValueError(f"{what} must have contiguous tokens")
+    return t.stride(0) if T > 1 else H * d
+
+
+def _same(dev, *ts):
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise ValueError("all tensors must be on the same device")
+
+
+def qt_kv_write(K, V, slots, k, v, stream=None):
+    """Quantizes K, V [T, heads, dim] (f32 or bf16, tokens of any stride) into
+    the slots [T] int32 of the cache k, v = (codes, scales, bits); slot p*page + i
+    is token i of page p, slots outside the cache are left out."""
+    ldk, ldv = _tokens(K, "K"), _tokens(V, "V")
+    if K.shape != V.shape or K.dtype != V.dtype:
+        raise ValueError("K and V must have the same shape and type")
+    xt = _xtype(K, "K")
+    T, H, d = K.shape
+    n_pages, page, heads = _kv(k, v, d)
+    if heads != H:
+        raise ValueError("K and the cache must have the same heads")
+    _is(slots, (T,), torch.int32, "slots")
+    with _on(K.device, stream):
+        dev = _dev(slots, k[0], k[1], v[0], v[1])
+        _same(dev, K, V)
+        _check(lib().qt_kv_write(_ptr(K), ldk, _ptr(V), ldv, xt, T, _ptr(slots),
+                                 *_kv_args(k, v, n_pages, page, heads, d), _stream(stream, dev)),
+               "qt_kv_write")
+
+
+def qt_kv_read(slots, k, v, dim: int, dtype=torch.bfloat16, K=None, V=None, stream=None):
+    """-> (K, V) [R, heads, dim] of the slots [R] int32 of the cache, in dtype
+    (f32 or bf16); slots outside the cache give zeros."""
+    n_pages, page, heads = _kv(k, v, dim)
+    if slots.dim() != 1:
+        raise ValueError("slots must be [R]")
+    R = slots.shape[0]
+    _is(slots, (R,), torch.int32, "slots")
+    with _on(slots.device, stream):
+        if K is None:
+            K = torch.empty((R, heads, dim), dtype=dtype, device=slots.device)
+        if V is None:
+            V = torch.empty((R, heads, dim), dtype=K.dtype, device=slots.device)
+        xt = _xtype(K, "K")
+        _is(K, (R, heads, dim), K.dtype, "K")
+        _is(V, (R, heads, dim), K.dtype, "V")
+        dev = _dev(slots, k[0], k[1], v[0], v[1], K, V)
+        _check(lib().qt_kv_read(_ptr(slots), R, *_kv_args(k, v, n_pages, page, heads, dim),
+                                _ptr(K), _ptr(V), xt, _stream(stream, dev)), "qt_kv_read")
+    return K, V
+
+
+def qt_attn_decode_workspace_bytes(B: int, q_heads: int, heads: int, dim: int, table_pages: int,
+                                   page: int, window: int = 0) -> int:
+    return int(lib().qt_attn_decode_workspace_bytes(B, q_heads, heads, dim, table_pages, page,
+                                                    window))
+
+
+def qt_attn_decode(Q, k, v, page_table, lens, scale=None, window: int = 0, out=None, lse=None,
+                   want_lse: bool = False, workspace=None, stream=None):
+    """out [B, q_heads, dim] = softmax(scale Q K^T) V over the first lens[b]
+    positions (the last `window` of them, 0: all) of each sequence's pages
+    page_table [B, table_pages] of the cache k, v.  Q [B, q_heads, dim] f32 or
+    bf16, sequences of any stride; scale None: 1 / sqrt(dim).  With want_lse or
+    a given lse [B, q_heads] f32 (ln of the softmax's sum) -> (out, lse)."""
+    ldq = _tokens(Q, "Q")
+    xt = _xtype(Q, "Q")
+    B, q_heads, d = Q.shape
+    n_pages, page, heads = _kv(k, v, d)
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must be [B, table_pages]")
+    pages = page_table.shape[1]
+    _is(page_table, (B, pages), torch.int32, "page_table")
+    _is(lens, (B,), torch.int32, "lens")
+    if scale is None:
+        scale = d ** -0.5
+    with _on(Q.device, stream):
+        if out is None:
+            out = torch.empty((B, q_heads, d), dtype=Q.dtype, device=Q.device)
+        if lse is None and want_lse:
+            lse = torch.empty((B, q_heads), dtype=torch.float32, device=Q.device)
+        _is(out, (B, q_heads, d), Q.dtype, "out")
+        _is(lse, (B, q_heads), torch.float32, "lse")
+        need = qt_attn_decode_workspace_bytes(B, q_heads, heads, d, pages, page, window)
+        workspace, wsb = _scratch(need, Q.device, workspace)
+        dev = _dev(page_table, lens, k[0], k[1], v[0], v[1], out, lse, workspace)
+        _same(dev, Q)
+        _check(lib().qt_attn_decode(_ptr(Q), ldq, xt, B, q_heads,
+                                    *_kv_args(k, v, n_pages, page, heads, d), _ptr(page_table),
+                                    pages, _ptr(lens), window, scale, _ptr(out), _ptr(lse),
+                                    _ptr(workspace), wsb, _stream(stream, dev)),
+               "qt_attn_decode")
+    return out if lse is None else (out, lse)

@@ -513,6 +513,85 @@ qt_status qt_distill_topk_bwd(const void* logits, qt_dtype lt, int64_t T, int64_
                               const float* lse, const float* gloss, void* dlogits, int64_t ldd,
                               void* stream);
 
+/*
+ * Quantized key-value cache: the keys and values of every token that a network
+ * has seen, at 4 or 8 bits in groups of 64 values of a head, in pages that a
+ * table deals to the sequences.  A cache is
+ *   k_codes  [n_pages][heads][page][G * 8 k_bits] bytes, v_codes likewise,
+ *   k_scales [n_pages][heads][page][G] f32, v_scales likewise; G = ceil(dim/64);
+ *   page: tokens of a page, a multiple of 16 up to 65536; slot s is token
+ *   s % page of page s / page;
+ *   1 <= dim <= 256; heads <= 1024; bits 4 or 8, each its own;
+ *   n_pages * page < 2^31.  Codes 16-byte aligned, scales 16-byte aligned.
+ * A group x_j of a token and head (values past dim are 0) is held as s v_j:
+ *   m = the value of largest magnitude (the first of equals), h = 8 or 128,
+ *   s = -m / h, v_j = clamp(nearest integer to x_j / s, ties to even, -h, h - 1),
+ *   0 where s = 0: bit-exact functions of the inputs, with x_j / s unrounded.
+ *   A group with a NaN or an infinity has the scale NaN and reads back as NaN.
+ * Key codes: a token's groups one after the other, in the int4-g64 layout above
+ * or as bytes v + 128.  Value codes: blocks of 8 tokens; in a block group after
+ * group; in a group 16 columns of values 4c .. 4c+3; in a column, value 4c+i of
+ * token t is byte 4t + i (8 bits, v + 128), or nibble i % 2 (low first) of byte
+ * 4 (t/2) + 2 (i/2) + t % 2 (4 bits, v + 8).
+ */
+
+/* Host: bytes of k_codes or v_codes; 0 for sizes or bits that no cache has. */
+int64_t qt_kv_bytes(int64_t n_pages, int64_t page, int64_t heads, int64_t dim, int32_t bits);
+
+/*
+ * Write T tokens: K, V [T x heads x dim] of type xt, tokens ldk and ldv >=
+ * heads*dim elements apart (slices of a projection's rows); slots [T] int32.  A
+ * token whose slot is negative or not below n_pages*page is left out; of two
+ * tokens of one call with one slot the codes and scales may mix.  Everything
+ * else in the cache stays as it is.  1 <= T <= 2^22.
+ */
+qt_status qt_kv_write(const void* K, int64_t ldk, const void* V, int64_t ldv, qt_dtype xt,
+                      int64_t T, const int32_t* slots, uint8_t* k_codes, float* k_scales,
+                      int32_t k_bits, uint8_t* v_codes, float* v_scales, int32_t v_bits,
+                      int64_t n_pages, int64_t page, int64_t heads, int64_t dim, void* stream);
+
+/*
+ * Read R slots back: K, V [R x heads x dim] contiguous, of type xt, s v rounded
+ * once; either may be NULL.  slots [R] int32, in any order, repeated or not; a
+ * negative one, or one not below n_pages*page, gives zeros.  1 <= R <= 2^22.
+ */
+qt_status qt_kv_read(const int32_t* slots, int64_t R, const uint8_t* k_codes,
+                     const float* k_scales, int32_t k_bits, const uint8_t* v_codes,
+                     const float* v_scales, int32_t v_bits, int64_t n_pages, int64_t page,
+                     int64_t heads, int64_t dim, void* K, void* V, qt_dtype xt, void* stream);
+
+/*
+ * Attention of one new token per sequence over the cache:
+ *   positions i of sequence b with max(0, n - window) <= i < n, n = lens[b]
+ *   (window 0: all i < n); position i is token i % page of page
+ *   page_table[b][i / page]; query head q reads head q / (q_heads/heads);
+ *   S_i = scale * sum_j q_j k_ij, p = softmax over the positions,
+ *   out = sum_i p_i v_i, lse = ln sum_i e^S_i
+ * with k and v as the cache holds them (qt_kv_write of the new token comes
+ * first, on the same stream).  No position: out 0, lse -inf.  A length past the
+ * table counts as its end, a negative one as 0; positions of a page outside [0, n_pages)
+ * do not count.  Cache memory of other positions may hold anything.
+ *   Q [B x q_heads x dim] of type xt, sequences ldq >= q_heads*dim elements
+ *   apart; page_table [B x table_pages] int32, lens [B] int32;
+ *   out [B x q_heads x dim] of type xt; lse [B x q_heads] f32 or NULL
+ *   q_heads a multiple of heads, up to 256 per head; B <= 65535; scale finite;
+ *   table_pages * page < 2^31
+ * Rounding: exact codes, scales in f32; bf16 calls take p s as two bf16 pieces
+ * (2^-17), f32 calls exactly; f32 sums and softmax, one rounding at the end.
+ *   workspace: qt_attn_decode_workspace_bytes(...) bytes (16-byte aligned; may
+ *   be NULL when that size is 0): long contexts are cut into chunks that are
+ *   joined by a second launch.  Chunks depend on the sizes only, not on lens.
+ */
+size_t qt_attn_decode_workspace_bytes(int64_t B, int64_t q_heads, int64_t heads, int64_t dim,
+                                      int64_t table_pages, int64_t page, int64_t window);
+qt_status qt_attn_decode(const void* Q, int64_t ldq, qt_dtype xt, int64_t B, int64_t q_heads,
+                         const uint8_t* k_codes, const float* k_scales, int32_t k_bits,
+                         const uint8_t* v_codes, const float* v_scales, int32_t v_bits,
+                         int64_t n_pages, int64_t page, int64_t heads, int64_t dim,
+                         const int32_t* page_table, int64_t table_pages, const int32_t* lens,
+                         int64_t window, float scale, void* out, float* lse, void* workspace,
+                         size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,129 @@
+"""The C ABI of the cache and attention calls on the CPU: sizes and refusals
+through the built library (nothing may reach the GPU here)."""
+import pytest
+import torch
+
+import dequant_matmul_int3_amd as qt
+
+A, B, C_, D = 0x7F0000000000, 0x7F1000000000, 0x7F2000000000, 0x7F3000000000
+E, F_, G_, H = 0x7F4000000000, 0x7F5000000000, 0x7F6000000000, 0x7F7000000000
+I_, J = 0x7E0000000000, 0x7E1000000000
+NULL, SHAPE, ALIGN, DTYPE, ARG, ALIAS, WORKSPACE = 1, 2, 3, 4, 5, 6, 8
+
+
+def test_cache_sizes():
+    assert qt.qt_kv_bytes(3, 16, 2, 128, 8) == 3 * 16 * 2 * 128
+    assert qt.qt_kv_bytes(3, 16, 2, 128, 4) == 3 * 16 * 2 * 64
+    assert qt.qt_kv_bytes(1, 48, 1, 65, 4) == 48 * 64
+    for bad in ((0, 16, 1, 64, 8), (1, 8, 1, 64, 8), (1, 24, 1, 64, 8), (1, 16, 0, 64, 8),
+                (1, 16, 1, 0, 8), (1, 16, 1, 257, 8), (1, 16, 1, 64, 3), (1 << 27, 16, 1, 64, 8),
+                (1, 65552, 1, 64, 8), (1, 16, 1025, 64, 8)):
+        assert qt.qt_kv_bytes(*bad) == 0, bad
+
+
+def test_workspace_sizes():
+    w = qt.qt_attn_decode_workspace_bytes
+    assert w(1, 32, 8, 128, 16, 16) == 0                    # one chunk
+    assert w(1, 32, 8, 128, 64, 64) > 0                     # a long context is cut
+    assert w(256, 32, 8, 128, 64, 64) == 0                  # a batch fills the card uncut
+    assert w(1, 32, 8, 128, 4096, 64, window=100) == 0      # a window bounds the span
+    assert w(1, 8, 8, 64, 1 << 20, 16) == 8 * 4096 * 66 * 4  # chunks of 4096 at most
+    for bad in ((0, 8, 8, 64, 1, 16), (1, 8, 3, 64, 1, 16), (1, 8, 8, 64, 0, 16),
+                (1, 8, 8, 64, 1, 17), (65536, 8, 8, 64, 1, 16), (1, 257, 1, 64, 1, 16),
+                (1, 8, 8, 64, 1 << 27, 16), (1, 8, 8, 64, 1, 16, -1)):
+        assert w(*bad) == 0, bad
+
+
+def test_write_refusals():
+    f = qt.lib().qt_kv_write
+
+    def call(K=A, ldk=128, V=B, ldv=128, xt=1, T=4, slots=C_, kc=D, ks=E, kb=8, vc=F_, vs=G_, vb=4,
+             n=4, page=16, heads=2, dim=64):
+        return f(K, ldk, V, ldv, xt, T, slots, kc, ks, kb, vc, vs, vb, n, page, heads, dim, None)
+
+    for p in ("K", "V", "slots", "kc", "ks", "vc", "vs"):
+        assert call(**{p: None}) == NULL
+    assert call(xt=2) == DTYPE
+    assert call(T=0) == SHAPE and call(T=(1 << 22) + 1) == SHAPE and call(ldk=127) == SHAPE
+    assert call(ldv=1 << 40) == SHAPE and call(page=8) == SHAPE and call(page=20) == SHAPE
+    assert call(heads=0) == SHAPE and call(dim=257, ldk=514, ldv=514) == SHAPE and call(n=0) == SHAPE
+    assert call(n=1 << 27) == SHAPE and call(n=-3) == SHAPE and call(n=1 << 62) == SHAPE
+    assert call(kb=3) == ARG and call(vb=16) == ARG
+    assert call(K=A + 1) == ALIGN and call(kc=D + 8) == ALIGN and call(vs=G_ + 4) == ALIGN
+    assert call(slots=C_ + 2) == ALIGN
+    assert call(K=D + 64) == ALIAS and call(vc=D) == ALIAS and call(slots=E) == ALIAS
+
+
+def test_read_refusals():
+    f = qt.lib().qt_kv_read
+
+    def call(slots=C_, R=4, kc=D, ks=E, kb=8, vc=F_, vs=G_, vb=4, n=4, page=16, heads=2, dim=64,
+             K=A, V=B, xt=0):
+        return f(slots, R, kc, ks, kb, vc, vs, vb, n, page, heads, dim, K, V, xt, None)
+
+    assert call(slots=None) == NULL and call(K=None, V=None) == NULL and call(kc=None) == NULL
+    assert call(xt=-1) == DTYPE and call(R=0) == SHAPE and call(dim=0) == SHAPE
+    assert call(kb=5) == ARG and call(K=A + 2) == ALIGN and call(ks=E + 4) == ALIGN
+    assert call(K=D) == ALIAS and call(V=A + 16) == ALIAS and call(V=C_) == ALIAS
+
+
+def test_attention_refusals():
+    f = qt.lib().qt_attn_decode
+
+    def call(Q=A, ldq=512, xt=1, Bn=2, hq=8, kc=D, ks=E, kb=8, vc=F_, vs=G_, vb=4, n=4, page=16,
+             heads=2, dim=64, table=B, pages=2, lens=C_, window=0, scale=0.125, out=H, lse=I_,
+             ws=None, wsb=0):
+        return f(Q, ldq, xt, Bn, hq, kc, ks, kb, vc, vs, vb, n, page, heads, dim, table, pages, lens,
+                 window, scale, out, lse, ws, wsb, None)
+
+    for p in ("Q", "kc", "ks", "vc", "vs", "table", "lens", "out"):
+        assert call(**{p: None}) == NULL
+    assert call(xt=7) == DTYPE
+    assert call(Bn=0) == SHAPE and call(Bn=65536) == SHAPE and call(hq=7) == SHAPE
+    assert call(hq=2 * 257, ldq=1 << 20) == SHAPE and call(ldq=511) == SHAPE
+    assert call(pages=0) == SHAPE and call(pages=1 << 27) == SHAPE and call(window=-1) == SHAPE
+    assert call(page=17) == SHAPE and call(dim=300) == SHAPE
+    assert call(kb=2) == ARG and call(vb=0) == ARG
+    assert call(scale=float("nan")) == ARG and call(scale=float("inf")) == ARG
+    assert call(pages=64) == WORKSPACE and call(pages=64, ws=J, wsb=64) == WORKSPACE
+    assert call(pages=64, ws=J + 4, wsb=1 << 24) == ALIGN
+    assert call(out=H + 1) == ALIGN and call(lse=I_ + 2) == ALIGN and call(lens=C_ + 1) == ALIGN
+    assert call(out=A) == ALIAS and call(lse=H) == ALIAS and call(out=D + 16) == ALIAS
+    assert call(lse=B) == ALIAS and call(pages=64, ws=A, wsb=1 << 24) == ALIAS
+
+
+def test_binding_refusals():
+    """Refused before any device is touched."""
+    k, v = qt.qt_kv_cache(2, 16, 2, 80, 4, 8, device="cpu")
+    assert k[0].shape == (2, 2, 16, 64) and v[0].shape == (2, 2, 16, 128)
+    assert k[1].shape == (2, 2, 16, 2) and k[2] == 4 and v[2] == 8
+    with pytest.raises(ValueError, match="no such cache"):
+        qt.qt_kv_cache(2, 10, 2, 80, device="cpu")
+    x, slots = torch.zeros(3, 2, 80), torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="device tensors"):
+        qt.qt_kv_write(x, x, slots, k, v)
+    with pytest.raises(ValueError, match="device tensors"):
+        qt.qt_kv_read(slots, k, v, 80)
+    with pytest.raises(ValueError, match="contiguous tokens"):
+        qt.qt_kv_write(torch.zeros(3, 2, 160)[..., ::2], x, slots, k, v)
+    with pytest.raises(ValueError, match="contiguous tokens"):
+        qt.qt_kv_write(torch.zeros(2, 3, 80).transpose(0, 1), x, slots, k, v)
+    with pytest.raises(ValueError, match="same shape"):
+        qt.qt_kv_write(x, x.bfloat16(), slots, k, v)
+    with pytest.raises(ValueError, match="same heads"):
+        qt.qt_kv_write(x[:, :1], x[:, :1], slots, k, v)
+    with pytest.raises(ValueError, match="scales must be"):
+        qt.qt_kv_write(torch.zeros(3, 2, 130), torch.zeros(3, 2, 130), slots, k, v)
+    with pytest.raises(ValueError, match="slots must be"):
+        qt.qt_kv_write(x, x, slots.long(), k, v)
+    with pytest.raises(ValueError, match="codes do not match"):
+        qt.qt_kv_read(slots, (k[0], k[1], 8), v, 80)
+    q, table, lens = torch.zeros(3, 4, 80), torch.zeros(3, 2, dtype=torch.int32), slots
+    with pytest.raises(ValueError, match="page_table must be"):
+        qt.qt_attn_decode(q, k, v, table[:2], lens)
+    with pytest.raises(ValueError, match="lens must be"):
+        qt.qt_attn_decode(q, k, v, table, lens.long())
+    with pytest.raises(ValueError, match="float32 or bfloat16"):
+        qt.qt_attn_decode(q.half(), k, v, table, lens)
+    with pytest.raises(ValueError, match="device tensors"):
+        qt.qt_attn_decode(q, k, v, table, lens)
