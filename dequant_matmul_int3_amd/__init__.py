@@ -15,7 +15,7 @@ from .qt import (QtError, QT_BF16, QT_F32, lib, qt_groups, qt_hessian_diag,
                  qt_ffn_gated_bwd_workspace_bytes, qt_matmul_bwd, qt_matmul_bwd_workspace_bytes,
                  qt_distill_topk, qt_distill_topk_bwd, qt_distill_topk_workspace_bytes,
                  qt_kv_bytes, qt_kv_cache, qt_kv_write, qt_kv_read, qt_attn_decode,
-                 qt_attn_decode_workspace_bytes)
+                 qt_attn_decode_workspace_bytes, qt_moe_decode, qt_moe_decode_workspace_bytes)
 
 __all__ = ["QtError", "QT_BF16", "QT_F32", "lib", "qt_groups", "qt_hessian_diag",
            "qt_hessian_diag_noalloc", "qt_hessian_scratch_bytes", "qt_hessian_workspace_bytes", "qt_matmul_i3", "qt_matmul_i4", "qt_matvec_i3",
@@ -29,4 +29,4 @@ __all__ = ["QtError", "QT_BF16", "QT_F32", "lib", "qt_groups", "qt_hessian_diag"
            "qt_ffn_gated_bwd_workspace_bytes", "qt_matmul_bwd", "qt_matmul_bwd_workspace_bytes",
            "qt_distill_topk", "qt_distill_topk_bwd", "qt_distill_topk_workspace_bytes",
            "qt_kv_bytes", "qt_kv_cache", "qt_kv_write", "qt_kv_read", "qt_attn_decode",
-           "qt_attn_decode_workspace_bytes"]
+           "qt_attn_decode_workspace_bytes", "qt_moe_decode", "qt_moe_decode_workspace_bytes"]

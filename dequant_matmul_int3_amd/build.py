@@ -23,7 +23,8 @@ ARCH = "gfx950"
 SOURCES = ["api.cpp", "quantize.hip", "gemv.hip", "grouped.hip", "gemm.hip", "hessian.hip",
            "syrk.hip", "factor.hip", "gptq.hip", "moe.hip",
            "api_tune.cpp", "ffn.hip", "qgrad.hip", "distill.hip",
-           "api_serve.cpp", "kvcache.hip", "attn.hip", "attn_f32.hip"]
+           "api_serve.cpp", "kvcache.hip", "attn.hip", "attn_f32.hip",
+           "moe_few.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -1,5 +1,5 @@
-// C-ABI layer of the serving calls (the quantized key-value cache and the
-// attention that reads it): host-side argument validation, then the launches
+// C-ABI layer of the serving calls (the quantized key-value cache, the
+// attention that reads it and the expert layer for a few tokens): host-side argument validation, then the launches
 // on the caller's stream.  See qt.h for the contract of every entry point.
 #include <cmath>
 
@@ -177,6 +177,62 @@ qt_status qt_attn_decode(const void* Q, int64_t ldq, qt_dtype xt, int64_t B, int
                          Q, ldq, xt == QT_BF16, (int)B, (int)q_heads, page_table, table_pages,
                          lens, window, scale, out, lse};
     return launched(qt::launch_attn_decode(a, workspace, as_stream(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+bool few_sizes_ok(int64_t T, int32_t k, int32_t E, int64_t D, int64_t F) {
+    return T >= 1 && T <= qt::kFewMaxTokens && D >= 1 && D <= qt::kFewMaxDim && F >= 1 &&
+           F <= qt::kFewMaxDim && E >= 1 && E <= qt::kFewMaxExperts && k >= 1 &&
+           k <= qt::kFewMaxTopK && k <= E;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t qt_moe_decode_workspace_bytes(int64_t T, int32_t k, int32_t E, int64_t D, int64_t F,
+                                     qt_dtype xt) {
+    if (!few_sizes_ok(T, k, E, D, F) || !dtype_ok(xt)) return 0;
+    return (size_t)qt::few_plan(T, k, F, xt == QT_BF16).bytes;
+}
+
+qt_status qt_moe_decode(const void* X, qt_dtype xt, int64_t T, int64_t D, int64_t F,
+                        const float* logits, int32_t E, int32_t k, qt_act act,
+                        const uint8_t* gate_packed, const float* gate_scales, int32_t gate_bits,
+                        const uint8_t* up_packed, const float* up_scales, int32_t up_bits,
+                        const uint8_t* down_packed, const float* down_scales, int32_t down_bits,
+                        void* out, void* workspace, size_t ws_bytes, void* stream) {
+    if (!X || !logits || !gate_packed || !gate_scales || !up_packed || !up_scales ||
+        !down_packed || !down_scales || !out)
+        return QT_ERR_NULL;
+    if (!dtype_ok(xt)) return QT_ERR_DTYPE;
+    if (!few_sizes_ok(T, k, E, D, F)) return QT_ERR_SHAPE;
+    auto bits_ok = [](int32_t b) { return b == 3 || b == 4; };
+    if (!bits_ok(gate_bits) || !bits_ok(up_bits) || !bits_ok(down_bits) ||
+        (act != QT_ACT_SILU && act != QT_ACT_GELU))
+        return QT_ERR_ARG;
+    const size_t need = qt_moe_decode_workspace_bytes(T, k, E, D, F, xt);
+    if (!workspace || ws_bytes < need) return QT_ERR_WORKSPACE;
+    const uintptr_t e = (uintptr_t)esize(xt);
+    if (!aligned(gate_packed, 16) || !aligned(up_packed, 16) || !aligned(down_packed, 16) ||
+        !aligned(gate_scales, 4) || !aligned(up_scales, 4) || !aligned(down_scales, 4) ||
+        !aligned(X, e) || !aligned(out, e) || !aligned(logits, 4) || !aligned(workspace, 16))
+        return QT_ERR_ALIGN;
+    auto gb = [](int32_t b) -> int64_t { return b == 3 ? kGroupBytes : kGroupBytesI4; };
+    const int64_t up_groups = E * F * groups(D), down_groups = E * D * groups(F);
+    const Buf o[2] = {{out, T * D * esize(xt)}, {workspace, (int64_t)need}};
+    const Buf in[8] = {{X, T * D * esize(xt)}, {logits, T * E * 4},
+                       {gate_packed, up_groups * gb(gate_bits)}, {gate_scales, up_groups * 4},
+                       {up_packed, up_groups * gb(up_bits)}, {up_scales, up_groups * 4},
+                       {down_packed, down_groups * gb(down_bits)}, {down_scales, down_groups * 4}};
+    if (any_overlap(o, in)) return QT_ERR_ALIAS;
+    const qt::FewArgs a{X, xt == QT_BF16, (int)T, E, k, (int)act, D, F, logits,
+                        {gate_packed, gate_scales, gate_bits}, {up_packed, up_scales, up_bits},
+                        {down_packed, down_scales, down_bits}, out};
+    return launched(qt::launch_moe_few(a, workspace, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -87,4 +87,48 @@ inline AttnPlan attn_plan(int64_t B, int64_t heads, int64_t q_heads, int64_t dim
 }
 hipError_t launch_attn_decode(const AttnArgs& a, void* workspace, hipStream_t s);
 
+// ------------------------------------------- expert layer for a few tokens
+constexpr int kFewMaxTokens = 16;
+constexpr int kFewMaxTopK = 32;
+constexpr int kFewMaxExperts = 512;
+constexpr int64_t kFewMaxDim = int64_t(1) << 20;
+
+struct FewMat {
+    const uint8_t* packed;  // [E][rows x groups] packed groups
+    const float* scales;
+    int bits;
+};
+struct FewArgs {
+    const void* X;  // [T x D]
+    bool bf16;
+    int T, E, k, act;
+    int64_t D, F;
+    const float* logits;  // [T x E]
+    FewMat gate, up, down;
+    void* out;  // [T x D]
+};
+
+// Workspace: the routing of the call (FewTables), then the activations of the
+// pairs as bf16 pieces [pieces][pairs][groups of F x 64].
+constexpr int64_t few_align(int64_t b) { return (b + 15) / 16 * 16; }
+struct FewPlan {
+    int64_t pairs, fp;        // pairs at most, F padded to whole groups
+    int pieces;               // of an activation: two (bf16 calls) or three
+    int64_t weight, planes;   // offsets of the parts in bytes; the counts are first
+    int64_t bytes;
+};
+inline FewPlan few_plan(int64_t T, int64_t k, int64_t F, bool bf16) {
+    FewPlan p;
+    p.pairs = T * k;
+    p.fp = (F + kGroup - 1) / kGroup * kGroup;
+    p.pieces = bf16 ? 2 : 3;
+    // active experts: their number (16 bytes), then each one's expert and
+    // first pair; then for each the tokens' weights and pairs
+    p.weight = 16 + few_align(p.pairs * 8);
+    p.planes = p.weight + few_align(p.pairs * T * 8);
+    p.bytes = p.planes + p.pieces * p.pairs * p.fp * 2;
+    return p;
+}
+hipError_t launch_moe_few(const FewArgs& a, void* workspace, hipStream_t s);
+
 }  // namespace qt

@@ -105,6 +105,12 @@ _SIGS = {
                                  C.c_int64, C.c_int64, C.c_int64, C.c_int64, C.c_void_p,
                                  C.c_int64, C.c_void_p, C.c_int64, C.c_float, C.c_void_p,
                                  C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "qt_moe_decode_workspace_bytes": (C.c_size_t, [C.c_int64, C.c_int32, C.c_int32, C.c_int64,
+                                                   C.c_int64, C.c_int]),
+    "qt_moe_decode": (C.c_int, [C.c_void_p, C.c_int, C.c_int64, C.c_int64, C.c_int64, C.c_void_p,
+                                C.c_int32, C.c_int32, C.c_int, C.c_void_p, C.c_void_p, C.c_int32,
+                                C.c_void_p, C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p,
+                                C.c_int32, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
     "qt_quantize_g64_i4": (C.c_int, [C.c_void_p, C.c_int64, C.c_int64, C.c_void_p, C.c_int32,
                                      C.c_float, C.c_float, C.c_void_p, C.c_void_p, C.c_void_p,
                                      C.c_void_p]),
@@ -846,3 +852,49 @@ def qt_attn_decode(Q, k, v, page_table, lens, scale=None, window: int = 0, out=N
                                     _ptr(workspace), wsb, _stream(stream, dev)),
                "qt_attn_decode")
     return out if lse is None else (out, lse)
+
+
+# ------------------------------------------------ expert layer, a few tokens
+def qt_moe_decode_workspace_bytes(T: int, k: int, E: int, D: int, F: int, xt: int) -> int:
+    return int(lib().qt_moe_decode_workspace_bytes(T, k, E, D, F, xt))
+
+
+def _expert_weight(w, E, rows, cols, what):
+    packed, scales, bits = w
+    if bits not in (3, 4):
+        raise ValueError(f"{what}: bits must be 3 or 4")
+    G = -(-cols // 64)
+    _is(scales, (E, rows, G), torch.float32, f"{what}: scales")
+    if packed.dtype != torch.uint8 or packed.numel() != E * rows * G * (24 if bits == 3 else 32):
+        raise ValueError(f"{what}: packed bytes do not match the scales' shape and {bits} bits")
+
+
+def qt_moe_decode(X, logits, k: int, gate, up, down, act: str = "silu", out=None, workspace=None,
+                  stream=None):
+    """The expert layer for X [T, D] f32 or bf16, T <= 16, logits [T, E] f32;
+    gate / up / down = (packed [E, bytes], scales [E, O, G], bits) with gate,
+    up [F x D] and down [D x F] per expert -> out [T, D] of X's type."""
+    if act not in QT_ACT:
+        raise ValueError(f"act must be one of {sorted(QT_ACT)}")
+    if X.dim() != 2 or logits.dim() != 2 or gate[1].dim() != 3:
+        raise ValueError("X must be [T, D], logits [T, E], scales [E, O, G]")
+    T, D = X.shape
+    E, F = logits.shape[1], gate[1].shape[1]
+    xt = _xtype(X, "X")
+    _is(logits, (T, E), torch.float32, "logits")
+    _expert_weight(gate, E, F, D, "gate")
+    _expert_weight(up, E, F, D, "up")
+    _expert_weight(down, E, D, F, "down")
+    with _on(X.device, stream):
+        if out is None:
+            out = torch.empty((T, D), dtype=X.dtype, device=X.device)
+        _is(out, (T, D), X.dtype, "out")
+        workspace, wsb = _scratch(qt_moe_decode_workspace_bytes(T, k, E, D, F, xt), X.device,
+                                  workspace)
+        dev = _dev(X, logits, gate[0], gate[1], up[0], up[1], down[0], down[1], out, workspace)
+        _check(lib().qt_moe_decode(_ptr(X), xt, T, D, F, _ptr(logits), E, k, QT_ACT[act],
+                                   _ptr(gate[0]), _ptr(gate[1]), gate[2], _ptr(up[0]),
+                                   _ptr(up[1]), up[2], _ptr(down[0]), _ptr(down[1]), down[2],
+                                   _ptr(out), _ptr(workspace), wsb, _stream(stream, dev)),
+               "qt_moe_decode")
+    return out

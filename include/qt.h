@@ -592,6 +592,30 @@ qt_status qt_attn_decode(const void* Q, int64_t ldq, qt_dtype xt, int64_t B, int
                          int64_t window, float scale, void* out, float* lse, void* workspace,
                          size_t ws_bytes, void* stream);
 
+/*
+ * qt_moe_layer for a few tokens, in two launches: routing, gate, up and the
+ * activation; then the down projection and the sum over a token's experts.
+ * Experts, routing, weights and formulas as qt_moe_layer (equal logits: the
+ * lower expert first), with either activation of qt_ffn_gated, but
+ *   1 <= T <= 16; any D and F up to 2^20; X [T x D] and out [T x D] of type
+ *   xt (logits f32), at their elements' alignment; the sum over a token's
+ *   experts runs in ascending order of the experts.
+ * Logits of -inf have the weight 0 as long as the token has another one.
+ * Roundings: exact codes and inputs, f32 group sums and scales; bf16 calls take
+ * the activation as two bf16 pieces (2^-17), f32 calls exactly; one rounding
+ * at the end.
+ *   packed 16-byte aligned; workspace: qt_moe_decode_workspace_bytes(...)
+ *   bytes (16-byte aligned).
+ */
+size_t qt_moe_decode_workspace_bytes(int64_t T, int32_t k, int32_t E, int64_t D, int64_t F,
+                                     qt_dtype xt);
+qt_status qt_moe_decode(const void* X, qt_dtype xt, int64_t T, int64_t D, int64_t F,
+                        const float* logits, int32_t E, int32_t k, qt_act act,
+                        const uint8_t* gate_packed, const float* gate_scales, int32_t gate_bits,
+                        const uint8_t* up_packed, const float* up_scales, int32_t up_bits,
+                        const uint8_t* down_packed, const float* down_scales, int32_t down_bits,
+                        void* out, void* workspace, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,4 +1,4 @@
-"""The C ABI of the cache and attention calls on the CPU: sizes and refusals
+"""The C ABI of the cache, attention and few-token expert calls on the CPU: sizes and refusals
 through the built library (nothing may reach the GPU here)."""
 import pytest
 import torch
@@ -127,3 +127,45 @@ def test_binding_refusals():
         qt.qt_attn_decode(q.half(), k, v, table, lens)
     with pytest.raises(ValueError, match="device tensors"):
         qt.qt_attn_decode(q, k, v, table, lens)
+
+
+def test_expert_layer_refusals():
+    f, w = qt.lib().qt_moe_decode, qt.qt_moe_decode_workspace_bytes
+    assert w(1, 8, 128, 7168, 2048, qt.QT_BF16) >= 2 * 8 * 2048 * 2
+    assert w(16, 8, 128, 7168, 2049, qt.QT_F32) >= 3 * 128 * 2112 * 2
+    for bad in ((0, 1, 1, 64, 64, 0), (17, 1, 1, 64, 64, 0), (1, 2, 1, 64, 64, 0),
+                (1, 33, 64, 64, 64, 0), (1, 1, 513, 64, 64, 0), (1, 1, 1, 0, 64, 0),
+                (1, 1, 1, 64, (1 << 20) + 1, 0), (1, 1, 1, 64, 64, 2)):
+        assert w(*bad) == 0, bad
+    K = 1 << 20
+
+    def call(X=A, xt=1, T=2, Dm=128, F=64, lg=B, En=4, k=2, act=0, gp=C_, gs=D, gb=3, up=E, us=F_,
+             ub=4, dp=G_, ds=H, db=3, out=I_, ws=J, wsb=K):
+        return f(X, xt, T, Dm, F, lg, En, k, act, gp, gs, gb, up, us, ub, dp, ds, db, out, ws, wsb,
+                 None)
+
+    for p in ("X", "lg", "gp", "gs", "up", "us", "dp", "ds", "out"):
+        assert call(**{p: None}) == NULL
+    assert call(xt=3) == DTYPE
+    assert call(T=17) == SHAPE and call(k=5) == SHAPE and call(k=0) == SHAPE
+    assert call(En=513) == SHAPE and call(F=0) == SHAPE and call(Dm=-1) == SHAPE
+    assert call(gb=5) == ARG and call(db=8) == ARG and call(act=2) == ARG
+    assert call(ws=None) == WORKSPACE and call(wsb=64) == WORKSPACE
+    assert call(gp=C_ + 8) == ALIGN and call(X=A + 1) == ALIGN and call(ws=J + 8) == ALIGN
+    assert call(out=A) == ALIAS and call(out=C_ + 64) == ALIAS and call(ws=I_) == ALIAS
+
+
+def test_expert_layer_binding_refusals():
+    x, lg = torch.zeros(2, 100), torch.zeros(2, 4)
+    w = (torch.zeros(4, 70 * 2 * 24, dtype=torch.uint8), torch.zeros(4, 70, 2), 3)
+    dn = (torch.zeros(4, 100 * 2 * 32, dtype=torch.uint8), torch.zeros(4, 100, 2), 4)
+    with pytest.raises(ValueError, match="device tensors"):
+        qt.qt_moe_decode(x, lg, 2, w, w, dn)
+    with pytest.raises(ValueError, match="act must be"):
+        qt.qt_moe_decode(x, lg, 2, w, w, dn, act="relu")
+    with pytest.raises(ValueError, match="down: scales"):
+        qt.qt_moe_decode(x, lg, 2, w, w, w)
+    with pytest.raises(ValueError, match="gate: packed"):
+        qt.qt_moe_decode(x, lg, 2, (w[0], w[1], 4), w, dn)
+    with pytest.raises(ValueError, match="logits"):
+        qt.qt_moe_decode(x, lg.double(), 2, w, w, dn)
