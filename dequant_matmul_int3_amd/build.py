@@ -35,10 +35,12 @@ FLAGS = [
 # The grouped matrix-core kernels scale every MFMA result on the vector ALUs:
 # ask the backend to keep MFMA results in VGPRs rather than AGPRs (saves one
 # copy per result).  The f64 tile products of the GPTQ factor fit two waves
-# per SIMD only in that form.
+# per SIMD only in that form, the attention over a cache of 128 values a head too.
 EXTRA = {"grouped.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          "moe.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-         "factor.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+         "factor.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+         "attn.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+         "attn_f32.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def _compile(src, verbose):

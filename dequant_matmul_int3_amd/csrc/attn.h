@@ -28,6 +28,7 @@
 // initial value, in the values' at the end).  f32 calls convert to v itself
 // (over a long flat softmax the offset costs more than f32's accuracy).
 #pragma once
+#include "lds_barrier.h"
 #include "serve.h"
 #include "unpack.h"
 #include "wave_reduce.h"
@@ -167,13 +168,20 @@ __device__ __forceinline__ f32x4_t mma(const u32x4_t& a, const u32x4_t& b, const
                                                    __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
 }
 
-// What a tile of 32 positions is read into.
+// What a tile of 32 positions is read into: codes as the operands want them,
+// the tile's 32 G scales one after the other over the lanes.
 template <int KB, int VB, int G>
 struct AttnTile {
     u32x4_t k[2][KB == 8 ? G : (G + 1) / 2];  // int4: two groups a word of four
     u32x4_t v[VB == 8 ? 2 * G : G];
-    f32x4_t sk[2 * G], sv[2 * G];  // [token 8 g ..][group], flat
-    bool ok0, ok1;                 // the pages of positions 0-15 and 16-31 exist
+    float sk[(G + 1) / 2], sv[(G + 1) / 2];
+};
+
+// Where a tile lies: the (page, head) and place of its halves of 16 positions.
+struct AttnPlace {
+    int64_t ph[2];
+    int at[2];
+    bool ok[2];  // the page exists
 };
 
 template <int KB, int VB, int G, bool F32>
@@ -184,7 +192,8 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_decode_kernel(const Attn
     using KC = Code<KB, F32>;
     using VC = Code<VB, F32>;
     const AttnArgs& a = x.a;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int l16 = lane & 15, g = lane >> 4;
     const int kvh = blockIdx.y / x.tiles, qt = blockIdx.y % x.tiles, b = blockIdx.z;
     const int per = a.q_heads / a.c.heads;
@@ -236,60 +245,60 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_decode_kernel(const Attn
         }
     }
 
-    // ---- a tile's loads
+    // ---- a tile's place (scalar) and its loads
     const int64_t prow = (int64_t)a.c.page * G;  // scales of a (page, head)
     const int32_t* table = a.table + (int64_t)b * a.table_pages;
     const int ka = 8 * (l16 >> 2) + (l16 & 3);  // this lane's key row of half 0
-    auto load = [&](int t0, AttnTile<KB, VB, G>& t) {
-        // the pages of both halves (the same but at a page's end)
-        uint32_t pi[2], po[2];
-        int64_t ph[2];
-        bool ok[2];
+    auto find = [&](int t0) {
+        AttnPlace w;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const uint32_t pos = min((uint32_t)t0 + 16u * h, (uint32_t)reach - 16u);
-            pi[h] = (uint32_t)(((uint64_t)pos * x.page_mul) >> 32) >> x.page_sh;
-            po[h] = pos - pi[h] * (uint32_t)a.c.page;
-            const int32_t id = table[pi[h]];
-            ok[h] = id >= 0 && id < a.c.pages;
-            ph[h] = (int64_t)(ok[h] ? id : 0) * a.c.heads + kvh;
+            const uint32_t pi = (uint32_t)(((uint64_t)pos * x.page_mul) >> 32) >> x.page_sh;
+            w.at[h] = (int)(pos - pi * (uint32_t)a.c.page);
+            const int32_t id = table[pi];
+            w.ok[h] = id >= 0 && id < a.c.pages;
+            w.ph[h] = (int64_t)(w.ok[h] ? id : 0) * a.c.heads + kvh;
         }
-        t.ok0 = ok[0];
-        t.ok1 = ok[1];
-        // token `i` of the tile: its (page, head) and its place there
-        auto base = [&](int i) { return i < 16 ? ph[0] * prow : ph[1] * prow; };
-        auto place = [&](int i) { return i < 16 ? (int)po[0] + i : (int)po[1] + i - 16; };
-        const int64_t kb = base(ka) * 8 * KB;
+        return w;
+    };
+    auto load = [&](const AttnPlace& w, AttnTile<KB, VB, G>& t) {
+        // rows of the (page, head) from which token i of the tile is row i
+        const int64_t b0 = w.ph[0] * prow + (int64_t)w.at[0] * G;
+        const int64_t b1 = w.ph[1] * prow + (int64_t)(w.at[1] - 16) * G;
+        const uint8_t* kp = a.c.kc + (l16 < 8 ? b0 : b1) * (8 * KB) + ka * KROW +
+                            (KB == 8 ? 16 : 8) * g;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint8_t* p = a.c.kc + kb + (int64_t)place(ka + 4 * h) * KROW;
 #pragma unroll
             for (int gr = 0; gr < G; ++gr) {
+                const uint8_t* p = kp + 4 * h * KROW + 8 * KB * gr;
                 if constexpr (KB == 8) {
-                    t.k[h][gr] = *reinterpret_cast<const u32x4_t*>(p + 64 * gr + 16 * g);
+                    t.k[h][gr] = *reinterpret_cast<const u32x4_t*>(p);
                 } else {
-                    const u32x2_t w = *reinterpret_cast<const u32x2_t*>(p + 32 * gr + 8 * g);
-                    t.k[h][gr >> 1][2 * (gr & 1)] = w.x;
-                    t.k[h][gr >> 1][2 * (gr & 1) + 1] = w.y;
+                    const u32x2_t z = *reinterpret_cast<const u32x2_t*>(p);
+                    t.k[h][gr >> 1][2 * (gr & 1)] = z.x;
+                    t.k[h][gr >> 1][2 * (gr & 1) + 1] = z.y;
                 }
             }
         }
-        const int64_t sb = base(8 * g) + (int64_t)place(8 * g) * G;
 #pragma unroll
-        for (int i = 0; i < 2 * G; ++i) {
-            t.sk[i] = reinterpret_cast<const f32x4_t*>(a.c.ks + sb)[i];
-            t.sv[i] = reinterpret_cast<const f32x4_t*>(a.c.vs + sb)[i];
+        for (int i = 0; i < (G + 1) / 2; ++i) {
+            const int f = min(lane + 64 * i, 32 * G - 1);
+            const int64_t at = (f < 16 * G ? b0 : b1) + f;
+            t.sk[i] = a.c.ks[at];
+            t.sv[i] = a.c.vs[at];
         }
-        const uint8_t* v = a.c.vc + base(8 * g) * 8 * VB +
-                           ((int64_t)(place(8 * g) >> 3) * G * 16 + l16) * (4 * VB);
+        // blocks of eight tokens; a block's 64 G values are its columns' 16 G words
+        const uint8_t* vp = a.c.vc + (g < 2 ? b0 : b1) * (8 * VB) + (8 * g * G * 16 / 8 + l16) * (4 * VB);
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) {
-            const u32x4_t* w = reinterpret_cast<const u32x4_t*>(v + gr * 16 * (4 * VB));
+            const u32x4_t* p = reinterpret_cast<const u32x4_t*>(vp + gr * 16 * (4 * VB));
             if constexpr (VB == 8) {
-                t.v[2 * gr] = w[0];
-                t.v[2 * gr + 1] = w[1];
+                t.v[2 * gr] = p[0];
+                t.v[2 * gr + 1] = p[1];
             } else {
-                t.v[gr] = w[0];
+                t.v[gr] = p[0];
             }
         }
     };
@@ -304,7 +313,23 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_decode_kernel(const Attn
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[gr][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
-    auto step = [&](int t0, AttnTile<KB, VB, G>& t) {
+    __shared__ __attribute__((aligned(16))) float sl[kAttnWaves][2][32 * G];
+    auto step = [&](int t0, const AttnPlace& w, const AttnTile<KB, VB, G>& t) {
+        // the scales of this lane's tokens 8 g + j, [j][group] flat
+        f32x4_t sk[2 * G], sv[2 * G];
+        lds_wave_sync();  // the last tile's are read
+#pragma unroll
+        for (int i = 0; i < (G + 1) / 2; ++i)
+            if (32 * G >= 64 * (i + 1) || lane < 32) {
+                sl[wave][0][lane + 64 * i] = t.sk[i];
+                sl[wave][1][lane + 64 * i] = t.sv[i];
+            }
+        lds_wave_sync();
+#pragma unroll
+        for (int i = 0; i < 2 * G; ++i) {
+            sk[i] = *reinterpret_cast<const f32x4_t*>(&sl[wave][0][8 * G * g + 4 * i]);
+            sv[i] = *reinterpret_cast<const f32x4_t*>(&sl[wave][1][8 * G * g + 4 * i]);
+        }
         float s[8];  // token 8 g + j
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -330,16 +355,16 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_decode_kernel(const Attn
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int at = (4 * h + j) * G;
-                float v = t.sk[at >> 2][at & 3] * r[0][j];
+                float v = sk[at >> 2][at & 3] * r[0][j];
 #pragma unroll
                 for (int gr = 1; gr < G; ++gr)
-                    v = __builtin_fmaf(t.sk[(at + gr) >> 2][(at + gr) & 3], r[gr][j], v);
+                    v = __builtin_fmaf(sk[(at + gr) >> 2][(at + gr) & 3], r[gr][j], v);
                 s[4 * h + j] = v * sc;
             }
         }
-        if (t0 < lo || t0 + kAttnTile > n || !t.ok0 || !t.ok1) {
+        if (t0 < lo || t0 + kAttnTile > n || !w.ok[0] || !w.ok[1]) {
             // what is not there counts as nothing, whatever the memory holds
-            const bool ok = g < 2 ? t.ok0 : t.ok1;
+            const bool ok = g < 2 ? w.ok[0] : w.ok[1];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int pos = t0 + 8 * g + j;
@@ -348,7 +373,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_decode_kernel(const Attn
 #pragma unroll
                 for (int gr = 0; gr < G; ++gr) {
                     const int at = j * G + gr;
-                    t.sv[at >> 2][at & 3] = in ? t.sv[at >> 2][at & 3] : 0.0f;
+                    sv[at >> 2][at & 3] = in ? sv[at >> 2][at & 3] : 0.0f;
                 }
             }
         }
@@ -383,8 +408,8 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_decode_kernel(const Attn
             u32x4_t ap[PP];
 #pragma unroll
             for (int j = 0; j < 8; j += 2) {
-                float w0 = p[j] * t.sv[(j * G + gr) >> 2][(j * G + gr) & 3];
-                float w1 = p[j + 1] * t.sv[((j + 1) * G + gr) >> 2][((j + 1) * G + gr) & 3];
+                float w0 = p[j] * sv[(j * G + gr) >> 2][(j * G + gr) & 3];
+                float w1 = p[j + 1] * sv[((j + 1) * G + gr) >> 2][((j + 1) * G + gr) & 3];
                 if constexpr (VC::kOffset) voff[gr] += w0 + w1;
 #pragma unroll
                 for (int k = 0; k < PP; ++k) {
@@ -410,21 +435,33 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_decode_kernel(const Attn
     };
 
     {
-        // this wave's tiles, the next one's loads in flight meanwhile; tiles
-        // past the end read the last one
-        AttnTile<KB, VB, G> ta, tb;
+        // this wave's tiles, the next two in flight meanwhile; past the last
+        // one its loads repeat (a loop without branches around its loads)
         constexpr int kHop = kAttnWaves * kAttnTile;
         const int first = t_begin + wave * kAttnTile;
         if (first < t_end) {
-            load(first, ta);
-            for (int t0 = first;; t0 += 2 * kHop) {
-                const bool more = t0 + kHop < t_end;
-                if (more) load(t0 + kHop, tb);
-                step(t0, ta);
-                if (!more) break;
-                if (t0 + 2 * kHop < t_end) load(t0 + 2 * kHop, ta);
-                step(t0 + kHop, tb);
-                if (t0 + 2 * kHop >= t_end) break;
+            const int last = first + (t_end - 1 - first) / kHop * kHop;
+            AttnTile<KB, VB, G> ta, tb, tc;
+            AttnPlace pa = find(first), pb = find(min(first + kHop, last)), pc, pn;
+            load(pa, ta);
+            load(pb, tb);
+            pc = find(min(first + 2 * kHop, last));
+            for (int t0 = first;; t0 += 3 * kHop) {
+                load(pc, tc);
+                pn = find(min(t0 + 3 * kHop, last));
+                step(t0, pa, ta);
+                if (t0 == last) break;
+                pa = pn;
+                load(pa, ta);
+                pn = find(min(t0 + 4 * kHop, last));
+                step(t0 + kHop, pb, tb);
+                if (t0 + kHop == last) break;
+                pb = pn;
+                load(pb, tb);
+                pn = find(min(t0 + 5 * kHop, last));
+                step(t0 + 2 * kHop, pc, tc);
+                if (t0 + 2 * kHop == last) break;
+                pc = pn;
             }
         }
     }

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes as C
+import functools
 import os
 
 import torch
@@ -709,6 +710,35 @@ def qt_distill_topk_bwd(logits, idx, tlogits, lse, gloss=None, tau: float = 1.0,
 
 
 # ------------------------------------- quantized key-value cache and attention
+# These calls are short (a few microseconds of the GPU's time for one token), so
+# their binding takes the shortest way: plain integers for pointers, torch's raw
+# stream, sizes that depend on shapes alone computed once per shape.
+def _current(device, stream):
+    """Whether a call on device needs no context (see _on): its device is
+    current and the stream is torch's."""
+    if device.type != "cuda":
+        raise ValueError("libqt takes device tensors only")
+    return stream is None and device.index == torch.cuda.current_device()
+
+
+def _raw_stream(device):
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _there(index, *ts):
+    """Every tensor given is contiguous and on the device of this index."""
+    for t in ts:
+        if t.get_device() != index:
+            raise ValueError("all tensors must be on the same device" if t.is_cuda
+                             else "libqt takes device tensors only")
+        if not t.is_contiguous():
+            raise ValueError("libqt takes contiguous tensors only")
+
+
+def _adr(t):
+    return None if t is None else t.data_ptr()
+
+
 def qt_kv_bytes(n_pages: int, page: int, heads: int, dim: int, bits: int) -> int:
     return int(lib().qt_kv_bytes(n_pages, page, heads, dim, bits))
 
@@ -730,42 +760,39 @@ def qt_kv_cache(n_pages: int, page: int, heads: int, dim: int, k_bits: int = 8, 
     return parts[0], parts[1]
 
 
+def _kv_part(part, dim, what):
+    codes, scales, bits = part
+    if bits != 4 and bits != 8:
+        raise ValueError(f"{what}: bits must be 4 or 8")
+    shape = scales.shape
+    if len(shape) != 4 or scales.dtype != torch.float32 or shape[3] != -(-dim // 64):
+        raise ValueError(f"{what}: scales must be float32 [n_pages, heads, page, ceil({dim}/64)]")
+    if codes.dtype != torch.uint8 or codes.numel() != scales.numel() * 8 * bits:
+        raise ValueError(f"{what}: codes do not match the scales' shape and {bits} bits")
+    return shape
+
+
 def _kv(k, v, dim):
-    """(n_pages, page, heads) of a cache for heads of dim values, checked."""
+    """(n_pages, heads, page) of a cache for heads of dim values, checked."""
     if not 1 <= dim <= 256:
         raise ValueError("dim must be 1 to 256")
-    for (codes, scales, bits), what in ((k, "k"), (v, "v")):
-        if bits not in (4, 8):
-            raise ValueError(f"{what}: bits must be 4 or 8")
-        if scales.dim() != 4 or scales.dtype != torch.float32 or scales.shape[3] != -(-dim // 64):
-            raise ValueError(f"{what}: scales must be float32 [n_pages, heads, page, ceil({dim}/64)]")
-        if codes.dtype != torch.uint8 or codes.numel() != scales.numel() * 8 * bits:
-            raise ValueError(f"{what}: codes do not match the scales' shape and {bits} bits")
-    if k[1].shape != v[1].shape:
+    shape = _kv_part(k, dim, "k")
+    if shape != _kv_part(v, dim, "v"):
         raise ValueError("k and v must have the same pages, heads and page size")
-    n_pages, heads, page, _ = k[1].shape
-    return n_pages, page, heads
-
-
-def _kv_args(k, v, n_pages, page, heads, dim):
-    return (_ptr(k[0]), _ptr(k[1]), k[2], _ptr(v[0]), _ptr(v[1]), v[2], n_pages, page, heads, dim)
+    return shape[0], shape[1], shape[2]
 
 
 def _tokens(t, what):
     """Distance in elements between the tokens of a [T, heads, dim] tensor whose
     tokens are contiguous (a slice of a projection's rows, say)."""
-    if t.dim() != 3:
+    shape = t.shape
+    if len(shape) != 3:
         raise ValueError(f"{what} must be [T, heads, dim]")
-    T, H, d = t.shape
-    if (d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d):
+    T, H, d = shape
+    ld, sh, sd = t.stride()
+    if (sd != 1 and d > 1) or (sh != d and H > 1):
         raise ValueError(f"{what} must have contiguous tokens")
-    return t.stride(0) if T > 1 else H * d
-
-
-def _same(dev, *ts):
-    for t in ts:
-        if t is not None and t.device != dev:
-            raise ValueError("all tensors must be on the same device")
+    return ld if T > 1 else H * d
 
 
 def qt_kv_write(K, V, slots, k, v, stream=None):
@@ -777,40 +804,53 @@ def qt_kv_write(K, V, slots, k, v, stream=None):
         raise ValueError("K and V must have the same shape and type")
     xt = _xtype(K, "K")
     T, H, d = K.shape
-    n_pages, page, heads = _kv(k, v, d)
+    n_pages, heads, page = _kv(k, v, d)
     if heads != H:
         raise ValueError("K and the cache must have the same heads")
-    _is(slots, (T,), torch.int32, "slots")
-    with _on(K.device, stream):
-        dev = _dev(slots, k[0], k[1], v[0], v[1])
-        _same(dev, K, V)
-        _check(lib().qt_kv_write(_ptr(K), ldk, _ptr(V), ldv, xt, T, _ptr(slots),
-                                 *_kv_args(k, v, n_pages, page, heads, d), _stream(stream, dev)),
-               "qt_kv_write")
+    if slots.shape != (T,) or slots.dtype != torch.int32:
+        raise ValueError(f"slots must be {torch.int32} of shape {(T,)}")
+    dev = K.device
+    if not _current(dev, stream):
+        with _on(dev, stream):
+            return qt_kv_write(K, V, slots, k, v)
+    kc, ks, kb = k
+    vc, vs, vb = v
+    _there(dev.index, slots, kc, ks, vc, vs)
+    if V.get_device() != dev.index:
+        raise ValueError("all tensors must be on the same device")
+    _check(lib().qt_kv_write(K.data_ptr(), ldk, V.data_ptr(), ldv, xt, T, slots.data_ptr(),
+                             kc.data_ptr(), ks.data_ptr(), kb, vc.data_ptr(), vs.data_ptr(), vb,
+                             n_pages, page, heads, d, _raw_stream(dev)), "qt_kv_write")
 
 
 def qt_kv_read(slots, k, v, dim: int, dtype=torch.bfloat16, K=None, V=None, stream=None):
     """-> (K, V) [R, heads, dim] of the slots [R] int32 of the cache, in dtype
     (f32 or bf16); slots outside the cache give zeros."""
-    n_pages, page, heads = _kv(k, v, dim)
-    if slots.dim() != 1:
-        raise ValueError("slots must be [R]")
-    R = slots.shape[0]
-    _is(slots, (R,), torch.int32, "slots")
-    with _on(slots.device, stream):
-        if K is None:
-            K = torch.empty((R, heads, dim), dtype=dtype, device=slots.device)
-        if V is None:
-            V = torch.empty((R, heads, dim), dtype=K.dtype, device=slots.device)
-        xt = _xtype(K, "K")
-        _is(K, (R, heads, dim), K.dtype, "K")
-        _is(V, (R, heads, dim), K.dtype, "V")
-        dev = _dev(slots, k[0], k[1], v[0], v[1], K, V)
-        _check(lib().qt_kv_read(_ptr(slots), R, *_kv_args(k, v, n_pages, page, heads, dim),
-                                _ptr(K), _ptr(V), xt, _stream(stream, dev)), "qt_kv_read")
+    n_pages, heads, page = _kv(k, v, dim)
+    if slots.dim() != 1 or slots.dtype != torch.int32:
+        raise ValueError("slots must be [R] of torch.int32")
+    shape = (slots.shape[0], heads, dim)
+    dev = slots.device
+    if not _current(dev, stream):
+        with _on(dev, stream):
+            return qt_kv_read(slots, k, v, dim, dtype, K, V)
+    if K is None:
+        K = torch.empty(shape, dtype=dtype, device=dev)
+    if V is None:
+        V = torch.empty(shape, dtype=K.dtype, device=dev)
+    xt = _xtype(K, "K")
+    _is(K, shape, K.dtype, "K")
+    _is(V, shape, K.dtype, "V")
+    kc, ks, kb = k
+    vc, vs, vb = v
+    _there(dev.index, slots, kc, ks, vc, vs, K, V)
+    _check(lib().qt_kv_read(slots.data_ptr(), shape[0], kc.data_ptr(), ks.data_ptr(), kb,
+                            vc.data_ptr(), vs.data_ptr(), vb, n_pages, page, heads, dim,
+                            K.data_ptr(), V.data_ptr(), xt, _raw_stream(dev)), "qt_kv_read")
     return K, V
 
 
+@functools.lru_cache(maxsize=1024)
 def qt_attn_decode_workspace_bytes(B: int, q_heads: int, heads: int, dim: int, table_pages: int,
                                    page: int, window: int = 0) -> int:
     return int(lib().qt_attn_decode_workspace_bytes(B, q_heads, heads, dim, table_pages, page,
@@ -826,47 +866,61 @@ def qt_attn_decode(Q, k, v, page_table, lens, scale=None, window: int = 0, out=N
     a given lse [B, q_heads] f32 (ln of the softmax's sum) -> (out, lse)."""
     ldq = _tokens(Q, "Q")
     xt = _xtype(Q, "Q")
-    B, q_heads, d = Q.shape
-    n_pages, page, heads = _kv(k, v, d)
-    if page_table.dim() != 2 or page_table.shape[0] != B:
-        raise ValueError("page_table must be [B, table_pages]")
+    B, q_heads, d = shape = Q.shape
+    n_pages, heads, page = _kv(k, v, d)
+    if page_table.dim() != 2 or page_table.shape[0] != B or page_table.dtype != torch.int32:
+        raise ValueError("page_table must be [B, table_pages] of torch.int32")
+    if lens.shape != (B,) or lens.dtype != torch.int32:
+        raise ValueError("lens must be [B] of torch.int32")
     pages = page_table.shape[1]
-    _is(page_table, (B, pages), torch.int32, "page_table")
-    _is(lens, (B,), torch.int32, "lens")
     if scale is None:
         scale = d ** -0.5
-    with _on(Q.device, stream):
-        if out is None:
-            out = torch.empty((B, q_heads, d), dtype=Q.dtype, device=Q.device)
-        if lse is None and want_lse:
-            lse = torch.empty((B, q_heads), dtype=torch.float32, device=Q.device)
-        _is(out, (B, q_heads, d), Q.dtype, "out")
+    dev = Q.device
+    if not _current(dev, stream):
+        with _on(dev, stream):
+            return qt_attn_decode(Q, k, v, page_table, lens, scale, window, out, lse, want_lse,
+                                  workspace)
+    if out is None:
+        out = torch.empty(shape, dtype=Q.dtype, device=dev)
+    else:
+        _is(out, shape, Q.dtype, "out")
+        _there(dev.index, out)
+    if lse is not None:
         _is(lse, (B, q_heads), torch.float32, "lse")
-        need = qt_attn_decode_workspace_bytes(B, q_heads, heads, d, pages, page, window)
-        workspace, wsb = _scratch(need, Q.device, workspace)
-        dev = _dev(page_table, lens, k[0], k[1], v[0], v[1], out, lse, workspace)
-        _same(dev, Q)
-        _check(lib().qt_attn_decode(_ptr(Q), ldq, xt, B, q_heads,
-                                    *_kv_args(k, v, n_pages, page, heads, d), _ptr(page_table),
-                                    pages, _ptr(lens), window, scale, _ptr(out), _ptr(lse),
-                                    _ptr(workspace), wsb, _stream(stream, dev)),
-               "qt_attn_decode")
+        _there(dev.index, lse)
+    elif want_lse:
+        lse = torch.empty((B, q_heads), dtype=torch.float32, device=dev)
+    need = qt_attn_decode_workspace_bytes(B, q_heads, heads, d, pages, page, window)
+    workspace, wsb = _scratch(need, dev, workspace)
+    if workspace is not None:
+        _there(dev.index, workspace)
+    kc, ks, kb = k
+    vc, vs, vb = v
+    _there(dev.index, page_table, lens, kc, ks, vc, vs)
+    _check(lib().qt_attn_decode(Q.data_ptr(), ldq, xt, B, q_heads, kc.data_ptr(), ks.data_ptr(),
+                                kb, vc.data_ptr(), vs.data_ptr(), vb, n_pages, page, heads, d,
+                                page_table.data_ptr(), pages, lens.data_ptr(), window, scale,
+                                out.data_ptr(), _adr(lse), _adr(workspace), wsb,
+                                _raw_stream(dev)), "qt_attn_decode")
     return out if lse is None else (out, lse)
 
 
 # ------------------------------------------------ expert layer, a few tokens
+@functools.lru_cache(maxsize=1024)
 def qt_moe_decode_workspace_bytes(T: int, k: int, E: int, D: int, F: int, xt: int) -> int:
     return int(lib().qt_moe_decode_workspace_bytes(T, k, E, D, F, xt))
 
 
 def _expert_weight(w, E, rows, cols, what):
     packed, scales, bits = w
-    if bits not in (3, 4):
+    if bits != 3 and bits != 4:
         raise ValueError(f"{what}: bits must be 3 or 4")
     G = -(-cols // 64)
-    _is(scales, (E, rows, G), torch.float32, f"{what}: scales")
+    if scales.shape != (E, rows, G) or scales.dtype != torch.float32:
+        raise ValueError(f"{what}: scales must be {torch.float32} of shape {(E, rows, G)}")
     if packed.dtype != torch.uint8 or packed.numel() != E * rows * G * (24 if bits == 3 else 32):
         raise ValueError(f"{what}: packed bytes do not match the scales' shape and {bits} bits")
+    return packed, scales
 
 
 def qt_moe_decode(X, logits, k: int, gate, up, down, act: str = "silu", out=None, workspace=None,
@@ -878,23 +932,28 @@ def qt_moe_decode(X, logits, k: int, gate, up, down, act: str = "silu", out=None
         raise ValueError(f"act must be one of {sorted(QT_ACT)}")
     if X.dim() != 2 or logits.dim() != 2 or gate[1].dim() != 3:
         raise ValueError("X must be [T, D], logits [T, E], scales [E, O, G]")
-    T, D = X.shape
+    T, D = shape = X.shape
     E, F = logits.shape[1], gate[1].shape[1]
     xt = _xtype(X, "X")
-    _is(logits, (T, E), torch.float32, "logits")
-    _expert_weight(gate, E, F, D, "gate")
-    _expert_weight(up, E, F, D, "up")
-    _expert_weight(down, E, D, F, "down")
-    with _on(X.device, stream):
-        if out is None:
-            out = torch.empty((T, D), dtype=X.dtype, device=X.device)
-        _is(out, (T, D), X.dtype, "out")
-        workspace, wsb = _scratch(qt_moe_decode_workspace_bytes(T, k, E, D, F, xt), X.device,
-                                  workspace)
-        dev = _dev(X, logits, gate[0], gate[1], up[0], up[1], down[0], down[1], out, workspace)
-        _check(lib().qt_moe_decode(_ptr(X), xt, T, D, F, _ptr(logits), E, k, QT_ACT[act],
-                                   _ptr(gate[0]), _ptr(gate[1]), gate[2], _ptr(up[0]),
-                                   _ptr(up[1]), up[2], _ptr(down[0]), _ptr(down[1]), down[2],
-                                   _ptr(out), _ptr(workspace), wsb, _stream(stream, dev)),
-               "qt_moe_decode")
+    if logits.shape[0] != T or logits.dtype != torch.float32:
+        raise ValueError(f"logits must be {torch.float32} of shape {(T, E)}")
+    gp, gs = _expert_weight(gate, E, F, D, "gate")
+    up_, us = _expert_weight(up, E, F, D, "up")
+    dp, ds = _expert_weight(down, E, D, F, "down")
+    dev = X.device
+    if not _current(dev, stream):
+        with _on(dev, stream):
+            return qt_moe_decode(X, logits, k, gate, up, down, act, out, workspace)
+    if out is None:
+        out = torch.empty(shape, dtype=X.dtype, device=dev)
+    _is(out, shape, X.dtype, "out")
+    workspace, wsb = _scratch(qt_moe_decode_workspace_bytes(T, k, E, D, F, xt), dev, workspace)
+    _there(dev.index, X, logits, gp, gs, up_, us, dp, ds, out)
+    if workspace is not None:
+        _there(dev.index, workspace)
+    _check(lib().qt_moe_decode(X.data_ptr(), xt, T, D, F, logits.data_ptr(), E, k, QT_ACT[act],
+                               gp.data_ptr(), gs.data_ptr(), gate[2], up_.data_ptr(),
+                               us.data_ptr(), up[2], dp.data_ptr(), ds.data_ptr(), down[2],
+                               out.data_ptr(), _adr(workspace), wsb, _raw_stream(dev)),
+           "qt_moe_decode")
     return out
