@@ -12,15 +12,21 @@
 // bound it; both products run on the bf16 matrix cores, whatever the number of
 // heads, so that the vector instructions per cache value stay below two.
 //
-// First product: the keys' codes as 16 x 32 operands (rows are tokens), the
-// queries' values as the other (f32 queries as three exact bf16 pieces); each
-// group's sum takes its f32 scale afterwards.  Row r of the tile's half s is
-// token 8 (r / 4) + 4 s + r % 4: the results of the two halves are then, lane
-// by lane, eight consecutive tokens of one head, which is what the second
-// product's operand wants: no probability moves between lanes.  It takes p sV
-// as two bf16 pieces (three in f32 calls; one alone would add an error as
-// large as the output's own rounding) and the values' codes, of which a lane
-// loads eight tokens x four values in one piece (the layout of the pages).
+// First product: rows are the queries' values (f32 queries as three exact bf16
+// pieces), columns the keys' codes of 16 tokens; each group's sum takes its f32
+// scale afterwards.  Row 4 g + r is head 4 r + g, so that the scores of up to 4
+// heads come in one register of every lane, 8 in two, 16 in four (NR), and the
+// softmax's instructions go by the heads there are.  A lane's two columns of a
+// tile are tokens 2 c and 2 c + 1: its probabilities, times the values' scales
+// and split into two bf16 pieces (three in f32 calls; one alone would add an
+// error as large as the output's own rounding), go to LDS as pairs and come
+// back as the second product's operand, whose other side is the values' codes:
+// a lane loads eight tokens x four values in one piece (the layout of the
+// pages).
+//
+// The running maximum need not be one: it moves when a score passes it by more
+// than 24 powers of two, which f32 sums and bf16 pieces have room for; else a tile costs
+// one comparison a score.
 //
 // bf16 calls take int4 codes as u = v + 8: the nibble is the FP8 (E4M3)
 // encoding of u / 512, so a mask and a packed conversion make two operands,
@@ -40,7 +46,8 @@ struct AttnKernelArgs {
     AttnArgs a;
     int chunk, splits, tiles;   // tiles: of 16 query heads per key-value head
     uint32_t page_mul, page_sh; // x / page for x < 2^31
-    float* part;                // splits > 1: [rows][splits] x (G 64 values, max, sum)
+    bool q_vec;                 // eight query values may be loaded at once
+    float* part;                // splits > 1: [rows][splits] x (G 64 values, max, sum, 2 unused)
 };
 
 hipError_t launch_attn_bf16(const AttnKernelArgs& k, hipStream_t s);
@@ -50,16 +57,28 @@ namespace {
 
 constexpr int kAttnWaves = 4;
 constexpr int kAttnTile = 32;
+constexpr int kHop = kAttnWaves * kAttnTile;
+static_assert(kAttnMaxChunk <= 64 * kHop, "a wave's tiles are kept one a lane");
 
-// max / sum over the four lanes that share l % 16
-__device__ __forceinline__ float quad_max(float v) {
-    const uint32_t u = __float_as_uint(v);
-    const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-    const float m = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
-    const uint32_t w = __float_as_uint(m);
-    const auto b = __builtin_amdgcn_permlane16_swap(w, w, false, false);
-    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+// max / sum over a 16-lane row
+template <int N>
+__device__ __forceinline__ float row_ror(float v) {
+    return __builtin_bit_cast(
+        float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x120 + N, 0xF, 0xF, false));
 }
+__device__ __forceinline__ float row_max(float v) {
+    v = fmaxf(v, row_ror<8>(v));
+    v = fmaxf(v, row_ror<4>(v));
+    v = fmaxf(v, row_ror<2>(v));
+    return fmaxf(v, row_ror<1>(v));
+}
+__device__ __forceinline__ float row_sum(float v) {
+    v += row_ror<8>(v);
+    v += row_ror<4>(v);
+    v += row_ror<2>(v);
+    return v + row_ror<1>(v);
+}
+// sum over the four lanes that share l % 16
 __device__ __forceinline__ float quad_sum(float v) {
     const uint32_t u = __float_as_uint(v);
     const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
@@ -69,22 +88,17 @@ __device__ __forceinline__ float quad_sum(float v) {
     return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
+// Codes as f32, by the compiler: conversions in inline assembly next to matrix
+// instructions would miss the waits that it keeps between a matrix result and
+// the next write of its registers.
 template <int B>
 __device__ __forceinline__ float signed_byte(uint32_t t) {
-    float r;
-    if constexpr (B == 0)
-        asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_0"
-            : "=v"(r) : "v"(t));
-    else if constexpr (B == 1)
-        asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_1"
-            : "=v"(r) : "v"(t));
-    else if constexpr (B == 2)
-        asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_2"
-            : "=v"(r) : "v"(t));
-    else
-        asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_3"
-            : "=v"(r) : "v"(t));
-    return r;
+    return (float)(int8_t)(t >> (8 * B));
+}
+// nibble N of w, less 8
+template <int N>
+__device__ __forceinline__ float signed_nibble(uint32_t t) {  // t = w ^ 0x88888888
+    return (float)((int32_t)(t << (28 - 4 * N)) >> 28);
 }
 // the high halves of two f32 values as a bf16 pair
 __device__ __forceinline__ uint32_t high_pair(float a, float b) {
@@ -95,12 +109,10 @@ __device__ __forceinline__ uint32_t fp8_pair(uint32_t u, bool hi) {
               : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(u, 512.0f, false));
 }
 
-// What the operand's codes stand for: u = v + 8 (bf16 calls' int4), v / 16
-// (f32 calls' int4) or v.
+// What the operand's codes stand for: u = v + 8 (bf16 calls' int4) or v.
 template <int BITS, bool F32>
 struct Code {
     static constexpr bool kOffset = BITS == 4 && !F32;
-    static constexpr float kUnit = BITS == 4 && F32 ? 16.0f : 1.0f;
 };
 
 // Eight key codes as an operand, and which of the eight the operand's value j
@@ -108,10 +120,11 @@ struct Code {
 template <bool F32>
 __device__ __forceinline__ u32x4_t key_operand4(uint32_t w) {
     if constexpr (F32) {
-        float v[8];
-        unpack_i4(w, v);
-        return u32x4_t{high_pair(v[0], v[1]), high_pair(v[2], v[3]), high_pair(v[4], v[5]),
-                       high_pair(v[6], v[7])};
+        const uint32_t t = w ^ 0x88888888u;
+        return u32x4_t{high_pair(signed_nibble<0>(t), signed_nibble<1>(t)),
+                       high_pair(signed_nibble<2>(t), signed_nibble<3>(t)),
+                       high_pair(signed_nibble<4>(t), signed_nibble<5>(t)),
+                       high_pair(signed_nibble<6>(t), signed_nibble<7>(t))};
     } else {
         const uint32_t e = w & 0x0F0F0F0Fu, o = (w >> 4) & 0x0F0F0F0Fu;
         return u32x4_t{fp8_pair(e, false), fp8_pair(e, true), fp8_pair(o, false),
@@ -126,7 +139,7 @@ __device__ __forceinline__ u32x4_t key_operand8(uint32_t lo, uint32_t hi) {
                    high_pair(signed_byte<2>(b), signed_byte<3>(b))};
 }
 template <int BITS, bool F32>
-__device__ __forceinline__ int key_order(int j) {
+__device__ __forceinline__ constexpr int key_order(int j) {
     return BITS == 4 && !F32 ? (j < 4 ? 2 * j : 2 * j - 7) : j;
 }
 
@@ -136,11 +149,11 @@ __device__ __forceinline__ void value_operands4(const u32x4_t& w, u32x4_t (&o)[4
 #pragma unroll
     for (int a = 0; a < 4; ++a) {  // a pair of tokens
         if constexpr (F32) {
-            const uint32_t t = w[a] ^ 0x88888888u, h = t >> 4;
-            o[0][a] = high_pair(nibble<0>(t), nibble<1>(t));
-            o[1][a] = high_pair(nibble<0>(h), nibble<1>(h));
-            o[2][a] = high_pair(nibble<2>(t), nibble<3>(t));
-            o[3][a] = high_pair(nibble<2>(h), nibble<3>(h));
+            const uint32_t t = w[a] ^ 0x88888888u;
+            o[0][a] = high_pair(signed_nibble<0>(t), signed_nibble<2>(t));
+            o[1][a] = high_pair(signed_nibble<1>(t), signed_nibble<3>(t));
+            o[2][a] = high_pair(signed_nibble<4>(t), signed_nibble<6>(t));
+            o[3][a] = high_pair(signed_nibble<5>(t), signed_nibble<7>(t));
         } else {
             const uint32_t e = w[a] & 0x0F0F0F0Fu, d = (w[a] >> 4) & 0x0F0F0F0Fu;
             o[0][a] = fp8_pair(e, false);
@@ -168,14 +181,37 @@ __device__ __forceinline__ f32x4_t mma(const u32x4_t& a, const u32x4_t& b, const
                                                    __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
 }
 
-// What a tile of 32 positions is read into: codes as the operands want them,
-// the tile's 32 G scales one after the other over the lanes.
-template <int KB, int VB, int G>
-struct AttnTile {
+// What a tile of 32 positions is read into: the codes of keys 2 c and 2 c + 1
+// and the scales of these keys and values, all groups; the codes of eight
+// values.
+template <int KB, int G>
+struct KeyTile {
     u32x4_t k[2][KB == 8 ? G : (G + 1) / 2];  // int4: two groups a word of four
-    u32x4_t v[VB == 8 ? 2 * G : G];
-    float sk[(G + 1) / 2], sv[(G + 1) / 2];
+    float sk[2 * G], sv[2 * G];
 };
+template <int VB, int G>
+struct ValueTile {
+    u32x4_t v[VB == 8 ? 2 * G : G];
+};
+// n floats, n = 2, 4, 6 or 8, at 8-byte alignment at least
+template <int N>
+__device__ __forceinline__ void load_floats(const float* p, float (&v)[N]) {
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            const f32x4_t w = reinterpret_cast<const f32x4_t*>(p)[i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[4 * i + j] = w[j];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const u32x2_t w = reinterpret_cast<const u32x2_t*>(p)[i];
+            v[2 * i] = __uint_as_float(w.x);
+            v[2 * i + 1] = __uint_as_float(w.y);
+        }
+    }
+}
 
 // Where a tile lies: the (page, head) and place of its halves of 16 positions.
 struct AttnPlace {
@@ -184,7 +220,10 @@ struct AttnPlace {
     bool ok[2];  // the page exists
 };
 
-template <int KB, int VB, int G, bool F32>
+// A row of probabilities in LDS: 32 tokens of a piece, 16 bytes apart in the banks.
+constexpr int kProbRow = 32 * 2 + 16;
+
+template <int KB, int VB, int G, int NR, bool F32>
 __global__ __launch_bounds__(64 * kAttnWaves) void attn_decode_kernel(const AttnKernelArgs x) {
     constexpr int NP = F32 ? 3 : 1;   // pieces of a query value
     constexpr int PP = F32 ? 3 : 2;   // pieces of a probability
@@ -209,70 +248,43 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_decode_kernel(const Attn
     const int t_begin = (int)min<int64_t>(begin, n);
     const int t_end = (int)min<int64_t>(begin + x.chunk, n);
 
-    // ---- queries as operands: column l16 is the head, values 16 g .. of each
-    // group in the order that the codes come in
-    u32x4_t q[NP][G][2];
-    float qoff[G];  // -8 times the group's sum, where the codes are offset
-    {
-        const int64_t head = (int64_t)kvh * per + r0 + min(l16, nr - 1);
-        const int64_t at = (int64_t)b * a.ldq + head * a.c.dim;
-#pragma unroll
-        for (int gr = 0; gr < G; ++gr) {
-            float sum = 0.0f;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t p[NP][8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int d = 64 * gr + 16 * g + 8 * h + key_order<KB, F32>(j);
-                    const int64_t i = at + min(d, a.c.dim - 1);
-                    if constexpr (F32) {
-                        float v = static_cast<const float*>(a.Q)[i];
-                        v = d < a.c.dim ? v : 0.0f;
-                        split3(v, p[0][j], p[NP > 1 ? 1 : 0][j], p[NP > 1 ? 2 : 0][j]);
-                    } else {
-                        uint32_t v = static_cast<const uint16_t*>(a.Q)[i];
-                        p[0][j] = d < a.c.dim ? v : 0u;
-                        sum += __uint_as_float(p[0][j] << 16);
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < NP; ++k)
-                    q[k][gr][h] = u32x4_t{p[k][0] | p[k][1] << 16, p[k][2] | p[k][3] << 16,
-                                          p[k][4] | p[k][5] << 16, p[k][6] | p[k][7] << 16};
-            }
-            qoff[gr] = KC::kOffset ? -8.0f * quad_sum(sum) : 0.0f;
-        }
-    }
-
-    // ---- a tile's place (scalar) and its loads
+    // ---- the tiles' places and loads
     const int64_t prow = (int64_t)a.c.page * G;  // scales of a (page, head)
     const int32_t* table = a.table + (int64_t)b * a.table_pages;
-    const int ka = 8 * (l16 >> 2) + (l16 & 3);  // this lane's key row of half 0
-    auto find = [&](int t0) {
+    const int first = t_begin + wave * kAttnTile;  // this wave's tiles: first + i kHop
+    // the places of all of them, tile i in lane i (vector loads once: a scalar
+    // load a tile would make every LDS wait wait for it, too)
+    int place_id[2], place_at[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t pos = min((uint32_t)(first + lane * kHop) + 16u * h, (uint32_t)reach - 16u);
+        const uint32_t pi = (uint32_t)(((uint64_t)pos * x.page_mul) >> 32) >> x.page_sh;
+        place_at[h] = (int)(pos - pi * (uint32_t)a.c.page);
+        place_id[h] = table[pi];
+    }
+    auto find = [&](int i) __attribute__((always_inline)) {
         AttnPlace w;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint32_t pos = min((uint32_t)t0 + 16u * h, (uint32_t)reach - 16u);
-            const uint32_t pi = (uint32_t)(((uint64_t)pos * x.page_mul) >> 32) >> x.page_sh;
-            w.at[h] = (int)(pos - pi * (uint32_t)a.c.page);
-            const int32_t id = table[pi];
+            const int id = __builtin_amdgcn_readlane(place_id[h], i);
+            w.at[h] = __builtin_amdgcn_readlane(place_at[h], i);
             w.ok[h] = id >= 0 && id < a.c.pages;
             w.ph[h] = (int64_t)(w.ok[h] ? id : 0) * a.c.heads + kvh;
         }
         return w;
     };
-    auto load = [&](const AttnPlace& w, AttnTile<KB, VB, G>& t) {
-        // rows of the (page, head) from which token i of the tile is row i
-        const int64_t b0 = w.ph[0] * prow + (int64_t)w.at[0] * G;
-        const int64_t b1 = w.ph[1] * prow + (int64_t)(w.at[1] - 16) * G;
-        const uint8_t* kp = a.c.kc + (l16 < 8 ? b0 : b1) * (8 * KB) + ka * KROW +
-                            (KB == 8 ? 16 : 8) * g;
+    // rows of the (page, head) from which token i of the tile is row i
+    auto rows_of = [&](const AttnPlace& w, int h) __attribute__((always_inline)) {
+        return w.ph[h] * prow + (int64_t)(w.at[h] - 16 * h) * G;
+    };
+    auto load_k = [&](const AttnPlace& w, KeyTile<KB, G>& t) __attribute__((always_inline)) {
+        const int64_t bk = l16 < 8 ? rows_of(w, 0) : rows_of(w, 1);
+        const uint8_t* kp = a.c.kc + bk * (8 * KB) + 2 * l16 * KROW + (KB == 8 ? 16 : 8) * g;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
             for (int gr = 0; gr < G; ++gr) {
-                const uint8_t* p = kp + 4 * h * KROW + 8 * KB * gr;
+                const uint8_t* p = kp + h * KROW + 8 * KB * gr;
                 if constexpr (KB == 8) {
                     t.k[h][gr] = *reinterpret_cast<const u32x4_t*>(p);
                 } else {
@@ -282,15 +294,13 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_decode_kernel(const Attn
                 }
             }
         }
-#pragma unroll
-        for (int i = 0; i < (G + 1) / 2; ++i) {
-            const int f = min(lane + 64 * i, 32 * G - 1);
-            const int64_t at = (f < 16 * G ? b0 : b1) + f;
-            t.sk[i] = a.c.ks[at];
-            t.sv[i] = a.c.vs[at];
-        }
+        load_floats(a.c.ks + bk + 2 * l16 * G, t.sk);
+        load_floats(a.c.vs + bk + 2 * l16 * G, t.sv);
+    };
+    auto load_v = [&](const AttnPlace& w, ValueTile<VB, G>& t) __attribute__((always_inline)) {
         // blocks of eight tokens; a block's 64 G values are its columns' 16 G words
-        const uint8_t* vp = a.c.vc + (g < 2 ? b0 : b1) * (8 * VB) + (8 * g * G * 16 / 8 + l16) * (4 * VB);
+        const uint8_t* vp = a.c.vc + (g < 2 ? rows_of(w, 0) : rows_of(w, 1)) * (8 * VB) +
+                            (g * G * 16 + l16) * (4 * VB);
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) {
             const u32x4_t* p = reinterpret_cast<const u32x4_t*>(vp + gr * 16 * (4 * VB));
@@ -303,189 +313,295 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_decode_kernel(const Attn
         }
     };
 
-    const float sc = a.scale * 1.4426950408889634f * KC::kUnit;  // powers of two from here on
-    float m = -INFINITY, l = 0.0f;  // head l16; l: this lane's tokens
-    float voff[G];                  // this lane's sum of p sV, where the codes are offset
+    // the first tile's loads go out before the queries' (a chunk without
+    // positions reads a place that is there and counts nothing)
+    const int last = max(0, t_end - 1 - first) / kHop;
+    KeyTile<KB, G> tk;
+    ValueTile<VB, G> tv0, tv1;
+    AttnPlace w0 = find(0), w1 = find(min(1, last));
+    load_k(w0, tk);
+    load_v(w0, tv0);
+
+    // ---- queries as operands: row l16 = 4 i + r is head 4 r + i, values 16 g ..
+    // of each group in the order that the codes come in
+    u32x4_t q[NP][G][2];
+    float qoff[NR][G];  // -8 times the group's sum of head 4 r + g, where the codes are offset
+    {
+        const int64_t head = (int64_t)kvh * per + r0 + min(4 * (l16 & 3) + (l16 >> 2), nr - 1);
+        const int64_t at = (int64_t)b * a.ldq + head * a.c.dim;
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int d0 = 64 * gr + 16 * g + 8 * h;
+                uint32_t v[8];  // the eight values' bits, in order
+                if (x.q_vec) {  // eight values lie wholly inside or outside the head
+                    const bool in = d0 < a.c.dim;
+                    const int64_t i = at + (in ? d0 : 0);
+                    if constexpr (F32) {
+                        const u32x4_t* z = reinterpret_cast<const u32x4_t*>(
+                            static_cast<const float*>(a.Q) + i);
+                        const u32x4_t z0 = z[0], z1 = z[1];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[j] = in ? (j < 4 ? z0[j & 3] : z1[j & 3]) : 0u;
+                    } else {
+                        const u32x4_t z = *reinterpret_cast<const u32x4_t*>(
+                            static_cast<const uint16_t*>(a.Q) + i);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            v[j] = in ? (j & 1 ? z[j >> 1] >> 16 : z[j >> 1] & 0xFFFFu) : 0u;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int64_t i = at + min(d0 + j, a.c.dim - 1);
+                        const uint32_t z = F32 ? static_cast<const uint32_t*>(a.Q)[i]
+                                               : (uint32_t)static_cast<const uint16_t*>(a.Q)[i];
+                        v[j] = d0 + j < a.c.dim ? z : 0u;
+                    }
+                }
+                uint32_t p[NP][8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t z = v[key_order<KB, F32>(j)];
+                    if constexpr (F32) {
+                        split3(__uint_as_float(z), p[0][j], p[NP > 1 ? 1 : 0][j],
+                               p[NP > 1 ? 2 : 0][j]);
+                    } else {
+                        p[0][j] = z;
+                        sum += __uint_as_float(z << 16);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < NP; ++k)
+                    q[k][gr][h] = u32x4_t{p[k][0] | p[k][1] << 16, p[k][2] | p[k][3] << 16,
+                                          p[k][4] | p[k][5] << 16, p[k][6] | p[k][7] << 16};
+            }
+            sum = quad_sum(sum);  // of row l16, in every lane of the column
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+                qoff[r][gr] = KC::kOffset ? -8.0f * __shfl(sum, 4 * g + r) : 0.0f;
+        }
+    }
+
+    const float sc = a.scale * 1.4426950408889634f;  // powers of two from here on
+    constexpr float kRoom = 24.0f;  // how far a score may pass the running maximum
+    float m[NR], l[NR];             // head 4 r + g; l: this lane's tokens
+    float voff[NR][G];              // this lane's sum of p sV, where the codes are offset
     f32x4_t o[G][4];                // heads 4 g .. 4 g + 3, values 64 gr + 4 l16 + i
 #pragma unroll
-    for (int gr = 0; gr < G; ++gr) {
-        voff[gr] = 0.0f;
+    for (int r = 0; r < NR; ++r) {
+        m[r] = -INFINITY;
+        l[r] = 0.0f;
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) voff[r][gr] = 0.0f;
+    }
+#pragma unroll
+    for (int gr = 0; gr < G; ++gr)
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[gr][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    }
-    __shared__ __attribute__((aligned(16))) float sl[kAttnWaves][2][32 * G];
-    auto step = [&](int t0, const AttnPlace& w, const AttnTile<KB, VB, G>& t) {
-        // the scales of this lane's tokens 8 g + j, [j][group] flat
-        f32x4_t sk[2 * G], sv[2 * G];
-        lds_wave_sync();  // the last tile's are read
-#pragma unroll
-        for (int i = 0; i < (G + 1) / 2; ++i)
-            if (32 * G >= 64 * (i + 1) || lane < 32) {
-                sl[wave][0][lane + 64 * i] = t.sk[i];
-                sl[wave][1][lane + 64 * i] = t.sv[i];
-            }
-        lds_wave_sync();
-#pragma unroll
-        for (int i = 0; i < 2 * G; ++i) {
-            sk[i] = *reinterpret_cast<const f32x4_t*>(&sl[wave][0][8 * G * g + 4 * i]);
-            sv[i] = *reinterpret_cast<const f32x4_t*>(&sl[wave][1][8 * G * g + 4 * i]);
-        }
-        float s[8];  // token 8 g + j
+
+    // the probabilities of the waves' tiles; at the end, the waves' value sums
+    union Lds {
+        uint8_t probs[kAttnWaves][G][PP][4 * NR][kProbRow];
+        float red[kAttnWaves][4 * NR][W];
+    };
+    __shared__ __attribute__((aligned(16))) Lds lds;
+    // scores of the tile in tk: token 2 l16 + h, head 4 r + g
+    auto scores = [&](float (&s)[2][NR]) __attribute__((always_inline)) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            f32x4_t r[G];
+            f32x4_t d[G];
 #pragma unroll
             for (int gr = 0; gr < G; ++gr) {
-                const float c = KC::kOffset ? qoff[gr] : 0.0f;
-                r[gr] = f32x4_t{c, c, c, c};
+                d[gr] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+                if constexpr (KC::kOffset)
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) d[gr][r] = qoff[r][gr];
                 u32x4_t k0, k1;
                 if constexpr (KB == 8) {
-                    k0 = key_operand8(t.k[h][gr][0], t.k[h][gr][1]);
-                    k1 = key_operand8(t.k[h][gr][2], t.k[h][gr][3]);
+                    k0 = key_operand8(tk.k[h][gr][0], tk.k[h][gr][1]);
+                    k1 = key_operand8(tk.k[h][gr][2], tk.k[h][gr][3]);
                 } else {
-                    k0 = key_operand4<F32>(t.k[h][gr >> 1][2 * (gr & 1)]);
-                    k1 = key_operand4<F32>(t.k[h][gr >> 1][2 * (gr & 1) + 1]);
+                    k0 = key_operand4<F32>(tk.k[h][gr >> 1][2 * (gr & 1)]);
+                    k1 = key_operand4<F32>(tk.k[h][gr >> 1][2 * (gr & 1) + 1]);
                 }
 #pragma unroll
                 for (int p = 0; p < NP; ++p) {
-                    r[gr] = mma(k0, q[p][gr][0], r[gr]);
-                    r[gr] = mma(k1, q[p][gr][1], r[gr]);
+                    d[gr] = mma(q[p][gr][0], k0, d[gr]);
+                    d[gr] = mma(q[p][gr][1], k1, d[gr]);
                 }
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int at = (4 * h + j) * G;
-                float v = sk[at >> 2][at & 3] * r[0][j];
+            for (int r = 0; r < NR; ++r) s[h][r] = (tk.sk[h * G] * sc) * d[0][r];
 #pragma unroll
-                for (int gr = 1; gr < G; ++gr)
-                    v = __builtin_fmaf(sk[(at + gr) >> 2][(at + gr) & 3], r[gr][j], v);
-                s[4 * h + j] = v * sc;
-            }
+            for (int gr = 1; gr < G; ++gr)
+#pragma unroll
+                for (int r = 0; r < NR; ++r)
+                    s[h][r] = __builtin_fmaf(tk.sk[h * G + gr] * sc, d[gr][r], s[h][r]);
         }
+    };
+    // the tile's probabilities, times the values' scales, to LDS
+    auto weigh = [&](int t0, const AttnPlace& w, float (&s)[2][NR], float (&sv)[2 * G]) __attribute__((always_inline)) {
         if (t0 < lo || t0 + kAttnTile > n || !w.ok[0] || !w.ok[1]) {
             // what is not there counts as nothing, whatever the memory holds
-            const bool ok = g < 2 ? w.ok[0] : w.ok[1];
+            const bool ok = l16 < 8 ? w.ok[0] : w.ok[1];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int pos = t0 + 8 * g + j;
+            for (int h = 0; h < 2; ++h) {
+                const int pos = t0 + 2 * l16 + h;
                 const bool in = ok && pos >= lo && pos < n;
-                s[j] = in ? s[j] : -INFINITY;
 #pragma unroll
-                for (int gr = 0; gr < G; ++gr) {
-                    const int at = j * G + gr;
-                    sv[at >> 2][at & 3] = in ? sv[at >> 2][at & 3] : 0.0f;
-                }
+                for (int r = 0; r < NR; ++r) s[h][r] = in ? s[h][r] : -INFINITY;
+#pragma unroll
+                for (int gr = 0; gr < G; ++gr) sv[h * G + gr] = in ? sv[h * G + gr] : 0.0f;
             }
         }
-        float mt = fmaxf(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])),
-                         fmaxf(fmaxf(s[4], s[5]), fmaxf(s[6], s[7])));
-        mt = fmaxf(m, quad_max(mt));
-        const float base = mt == -INFINITY ? 0.0f : mt;
-        if (__any(mt != m)) {
-            const float al = __builtin_amdgcn_exp2f(m - base);
-            l *= al;
+        bool past = false;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) past |= fmaxf(s[0][r], s[1][r]) > m[r] + kRoom;
+        if (__any(past)) {
+            float al[NR];
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                const float mt = fmaxf(m[r], row_max(fmaxf(s[0][r], s[1][r])));
+                al[r] = mt == m[r] ? 1.0f : __builtin_amdgcn_exp2f(m[r] - mt);
+                m[r] = mt;
+                l[r] *= al[r];
+#pragma unroll
+                for (int gr = 0; gr < G; ++gr) voff[r][gr] *= al[r];
+            }
+            // head 4 g + j: register g of lane row j
             float ao[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) ao[j] = __shfl(al, 4 * g + j);
+            for (int j = 0; j < 4; ++j) {
+                ao[j] = __shfl(al[0], 16 * j);
 #pragma unroll
-            for (int gr = 0; gr < G; ++gr) {
-                voff[gr] *= al;
+                for (int r = 1; r < NR; ++r) {
+                    const float v = __shfl(al[r], 16 * j);
+                    ao[j] = g == r ? v : ao[j];
+                }
+            }
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) o[gr][i][j] *= ao[j];
-            }
-            m = mt;
         }
-        float p[8];
+        lds_wave_sync();  // the last tile's probabilities are read
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            p[j] = __builtin_amdgcn_exp2f(s[j] - base);
-            l += p[j];
-        }
+        for (int r = 0; r < NR; ++r) {
+            const float base = m[r] == -INFINITY ? 0.0f : m[r];
+            const float p0 = __builtin_amdgcn_exp2f(s[0][r] - base);
+            const float p1 = __builtin_amdgcn_exp2f(s[1][r] - base);
+            l[r] += p0 + p1;
 #pragma unroll
-        for (int gr = 0; gr < G; ++gr) {
-            u32x4_t ap[PP];
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-                float w0 = p[j] * sv[(j * G + gr) >> 2][(j * G + gr) & 3];
-                float w1 = p[j + 1] * sv[((j + 1) * G + gr) >> 2][((j + 1) * G + gr) & 3];
-                if constexpr (VC::kOffset) voff[gr] += w0 + w1;
+            for (int gr = 0; gr < G; ++gr) {
+                float y0 = p0 * sv[gr], y1 = p1 * sv[G + gr];
+                if constexpr (VC::kOffset) voff[r][gr] += y0 + y1;
 #pragma unroll
                 for (int k = 0; k < PP; ++k) {
+                    uint32_t pair;
                     if (k + 1 < PP) {
-                        ap[k][j >> 1] = high_pair(w0, w1);
-                        w0 -= __uint_as_float(__float_as_uint(w0) & 0xFFFF0000u);
-                        w1 -= __uint_as_float(__float_as_uint(w1) & 0xFFFF0000u);
+                        pair = high_pair(y0, y1);
+                        y0 -= __uint_as_float(__float_as_uint(y0) & 0xFFFF0000u);
+                        y1 -= __uint_as_float(__float_as_uint(y1) & 0xFFFF0000u);
                     } else {
-                        ap[k][j >> 1] = bf16_pair(w0, w1);
+                        pair = bf16_pair(y0, y1);
                     }
+                    *reinterpret_cast<uint32_t*>(&lds.probs[wave][gr][k][4 * r + g][4 * l16]) = pair;
                 }
             }
+        }
+        lds_wave_sync();
+    };
+    // the second product of the tile in tv
+    auto values = [&](const ValueTile<VB, G>& tv) __attribute__((always_inline)) {
+        u32x4_t ap[G][PP];
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+            for (int k = 0; k < PP; ++k)  // rows past the heads repeat one that is there
+                ap[gr][k] = *reinterpret_cast<const u32x4_t*>(
+                    &lds.probs[wave][gr][k][l16 % (4 * NR)][16 * g]);
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) {
             u32x4_t bv[4];
             if constexpr (VB == 8)
-                value_operands8(t.v[2 * gr], t.v[2 * gr + 1], bv);
+                value_operands8(tv.v[2 * gr], tv.v[2 * gr + 1], bv);
             else
-                value_operands4<F32>(t.v[gr], bv);
+                value_operands4<F32>(tv.v[gr], bv);
 #pragma unroll
             for (int k = 0; k < PP; ++k)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[gr][i] = mma(ap[k], bv[i], o[gr][i]);
+                for (int i = 0; i < 4; ++i) o[gr][i] = mma(ap[gr][k], bv[i], o[gr][i]);
         }
     };
 
-    {
-        // this wave's tiles, the next two in flight meanwhile; past the last
-        // one its loads repeat (a loop without branches around its loads)
-        constexpr int kHop = kAttnWaves * kAttnTile;
-        const int first = t_begin + wave * kAttnTile;
-        if (first < t_end) {
-            const int last = first + (t_end - 1 - first) / kHop * kHop;
-            AttnTile<KB, VB, G> ta, tb, tc;
-            AttnPlace pa = find(first), pb = find(min(first + kHop, last)), pc, pn;
-            load(pa, ta);
-            load(pb, tb);
-            pc = find(min(first + 2 * kHop, last));
-            for (int t0 = first;; t0 += 3 * kHop) {
-                load(pc, tc);
-                pn = find(min(t0 + 3 * kHop, last));
-                step(t0, pa, ta);
-                if (t0 == last) break;
-                pa = pn;
-                load(pa, ta);
-                pn = find(min(t0 + 4 * kHop, last));
-                step(t0 + kHop, pb, tb);
-                if (t0 + kHop == last) break;
-                pb = pn;
-                load(pb, tb);
-                pn = find(min(t0 + 5 * kHop, last));
-                step(t0 + 2 * kHop, pc, tc);
-                if (t0 + 2 * kHop == last) break;
-                pc = pn;
-            }
+    if (first < t_end) {
+        // Tile i's second product runs next to tile i + 1's first one, which
+        // does not depend on it; loads are a whole tile ahead (past the last
+        // one they repeat: no branches around them).
+        float s[2][NR], sv[2 * G];
+        auto take = [&](const AttnPlace& next) __attribute__((always_inline)) {  // the tile in tk; then the next one's loads
+            scores(s);
+#pragma unroll
+            for (int i = 0; i < 2 * G; ++i) sv[i] = tk.sv[i];
+            load_k(next, tk);
+        };
+        take(w1);
+        weigh(first, w0, s, sv);
+        // wa: the place of tile i + 1
+        auto turn = [&](int i, AttnPlace& wa, const ValueTile<VB, G>& now, ValueTile<VB, G>& next) __attribute__((always_inline)) {
+            load_v(wa, next);
+            const AttnPlace wb = find(min(i + 2, last));
+            take(wb);
+            values(now);
+            weigh(first + (i + 1) * kHop, wa, s, sv);
+            wa = wb;
+        };
+        int i = 0;
+        for (; i + 1 < last; i += 2) {
+            turn(i, w1, tv0, tv1);
+            turn(i + 1, w1, tv1, tv0);
+        }
+        if (i < last) {
+            turn(i, w1, tv0, tv1);
+            values(tv1);
+        } else {
+            values(tv0);
         }
     }
 
     // ---- the waves' parts: a common maximum, then sums in wave order
     __shared__ float ml[kAttnWaves][2][16];
-    __shared__ __attribute__((aligned(16))) float red[kAttnWaves][16][W];
-    l = quad_sum(l);
-    if (lane < 16) {
-        ml[wave][0][l16] = m;
-        ml[wave][1][l16] = l;
-    }
+    __shared__ float vo[kAttnWaves][G][16];  // what the values' codes are offset by
+    __syncthreads();  // every wave is done with its probabilities
 #pragma unroll
-    for (int gr = 0; gr < G; ++gr) voff[gr] = VC::kOffset ? -8.0f * quad_sum(voff[gr]) : 0.0f;
-#pragma unroll
-    for (int gr = 0; gr < G; ++gr)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            f32x4_t v;
-            const float c = VC::kOffset ? __shfl(voff[gr], 4 * g + j) : 0.0f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = (o[gr][i][j] + c) * VC::kUnit;
-            *reinterpret_cast<f32x4_t*>(&red[wave][4 * g + j][64 * gr + 4 * l16]) = v;
+    for (int r = 0; r < NR; ++r) {
+        l[r] = row_sum(l[r]);
+        if (l16 == 0) {
+            ml[wave][0][4 * r + g] = m[r];
+            ml[wave][1][4 * r + g] = l[r];
         }
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr)
+            if constexpr (VC::kOffset) {
+                const float v = row_sum(voff[r][gr]);
+                if (l16 == 0) vo[wave][gr][4 * r + g] = -8.0f * v;
+            } else {
+                if (l16 == 0) vo[wave][gr][4 * r + g] = 0.0f;
+            }
+    }
+    if (g < NR) {  // heads 4 g + j that there may be
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<f32x4_t*>(&lds.red[wave][4 * g + j][64 * gr + 4 * l16]) =
+                    f32x4_t{o[gr][0][j], o[gr][1][j], o[gr][2][j], o[gr][3][j]};
+    }
     __syncthreads();
     for (int i = tid; i < nr * (W / 4); i += 64 * kAttnWaves) {
         const int r = i / (W / 4), d = i % (W / 4) * 4;
@@ -499,14 +615,14 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_decode_kernel(const Attn
         for (int w = 0; w < kAttnWaves; ++w) {
             const float e = __builtin_amdgcn_exp2f(ml[w][0][r] - base);
             sum += e * ml[w][1][r];
-            const f32x4_t z = *reinterpret_cast<const f32x4_t*>(&red[w][r][d]);
+            const f32x4_t z = *reinterpret_cast<const f32x4_t*>(&lds.red[w][r][d]);
+            const float c = vo[w][d >> 6][r];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = __builtin_fmaf(e, z[k], v[k]);
+            for (int k = 0; k < 4; ++k) v[k] = __builtin_fmaf(e, z[k] + c, v[k]);
         }
         if (x.splits > 1) {
-            float* out = x.part + ((row0 + r) * x.splits + blockIdx.x) * (W + 2);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) out[d + k] = v[k];
+            float* out = x.part + ((row0 + r) * x.splits + blockIdx.x) * (W + 4);
+            *reinterpret_cast<f32x4_t*>(out + d) = v;
             if (d == 0) {
                 out[W] = mx;
                 out[W + 1] = sum;
@@ -527,13 +643,24 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_decode_kernel(const Attn
     }
 }
 
+template <int KB, int VB, int G, bool F32>
+void attn_heads(const AttnKernelArgs& k, dim3 grid, hipStream_t s) {
+    const int per = k.a.q_heads / k.a.c.heads;
+    if (per <= 4)
+        attn_decode_kernel<KB, VB, G, 1, F32><<<grid, 64 * kAttnWaves, 0, s>>>(k);
+    else if (per <= 8)
+        attn_decode_kernel<KB, VB, G, 2, F32><<<grid, 64 * kAttnWaves, 0, s>>>(k);
+    else
+        attn_decode_kernel<KB, VB, G, 4, F32><<<grid, 64 * kAttnWaves, 0, s>>>(k);
+}
+
 template <int KB, int VB, bool F32>
 hipError_t attn_width(const AttnKernelArgs& k, dim3 grid, hipStream_t s) {
     switch (k.a.c.groups) {
-        case 1: attn_decode_kernel<KB, VB, 1, F32><<<grid, 64 * kAttnWaves, 0, s>>>(k); break;
-        case 2: attn_decode_kernel<KB, VB, 2, F32><<<grid, 64 * kAttnWaves, 0, s>>>(k); break;
-        case 3: attn_decode_kernel<KB, VB, 3, F32><<<grid, 64 * kAttnWaves, 0, s>>>(k); break;
-        default: attn_decode_kernel<KB, VB, 4, F32><<<grid, 64 * kAttnWaves, 0, s>>>(k); break;
+        case 1: attn_heads<KB, VB, 1, F32>(k, grid, s); break;
+        case 2: attn_heads<KB, VB, 2, F32>(k, grid, s); break;
+        case 3: attn_heads<KB, VB, 3, F32>(k, grid, s); break;
+        default: attn_heads<KB, VB, 4, F32>(k, grid, s); break;
     }
     return hipGetLastError();
 }

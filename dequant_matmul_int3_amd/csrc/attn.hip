@@ -20,12 +20,12 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnKernelArgs x) 
     const int first = lo & ~(kAttnTile - 1);
     // the first chunk is there even when empty
     const int parts = max(1, (int)(((int64_t)n - first + x.chunk - 1) / x.chunk));
-    const float* part = x.part + row * x.splits * (W + 2);
+    const float* part = x.part + row * x.splits * (W + 4);
     const int tid = threadIdx.x, col = tid % COLS, who = tid / COLS;
 
     __shared__ float wmax[4];
     float mx = -INFINITY;
-    for (int i = tid; i < parts; i += 256) mx = fmaxf(mx, part[(int64_t)i * (W + 2) + W]);
+    for (int i = tid; i < parts; i += 256) mx = fmaxf(mx, part[(int64_t)i * (W + 4) + W]);
     mx = wave_max(mx);
     if ((tid & 63) == 0) wmax[tid >> 6] = mx;
     __syncthreads();
@@ -37,11 +37,12 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnKernelArgs x) 
     if (who < ROWS) {
 #pragma unroll 4
         for (int i = who; i < parts; i += ROWS) {
-            const float* p = part + (int64_t)i * (W + 2);
+            const float* p = part + (int64_t)i * (W + 4);
             const float e = __builtin_amdgcn_exp2f(p[W] - base);
+            const f32x4_t z = *reinterpret_cast<const f32x4_t*>(p + 4 * col);
             sum += e * p[W + 1];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = __builtin_fmaf(e, p[4 * col + k], v[k]);
+            for (int k = 0; k < 4; ++k) v[k] = __builtin_fmaf(e, z[k], v[k]);
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) red[who][4 * col + k] = v[k];
@@ -87,7 +88,10 @@ hipError_t launch_attn_bf16(const AttnKernelArgs& k, hipStream_t s) {
 hipError_t launch_attn_decode(const AttnArgs& a, void* workspace, hipStream_t s) {
     const AttnPlan p = attn_plan(a.B, a.c.heads, a.q_heads, a.c.dim, a.table_pages, a.c.page,
                                  a.window);
-    AttnKernelArgs k{a, p.chunk, p.splits, (a.q_heads / a.c.heads + 15) / 16, 0, 0,
+    const int64_t qe = a.bf16 ? 8 : 4;  // elements of 16 bytes
+    const bool q_vec = a.c.dim % 8 == 0 && a.ldq % qe == 0 &&
+                       (reinterpret_cast<uintptr_t>(a.Q) & 15) == 0;
+    AttnKernelArgs k{a, p.chunk, p.splits, (a.q_heads / a.c.heads + 15) / 16, 0, 0, q_vec,
                      static_cast<float*>(workspace)};
     // x / page = (x * mul >> 32) >> sh for x < 2^31: mul = ceil(2^(32 + sh) / page)
     // with 2^sh < page <= 2^(sh + 1), so that mul < 2^32 and the error x / 2^(32 + sh) is

@@ -18,6 +18,7 @@ constexpr int64_t kKvMaxHeads = 1024;
 constexpr int64_t kKvMaxDim = 256;
 constexpr int64_t kAttnMaxBatch = 65535;
 constexpr int64_t kAttnMaxGroupHeads = 256;  // query heads per key-value head
+constexpr int64_t kAttnMaxChunk = 8192;
 
 // A paged cache: codes [pages][heads][page][groups * 8 bits] and scales
 // [pages][heads][page][groups] of the keys and of the values.
@@ -68,7 +69,7 @@ struct AttnPlan {
 inline AttnPlan attn_plan(int64_t B, int64_t heads, int64_t q_heads, int64_t dim,
                           int64_t table_pages, int64_t page, int64_t window) {
     constexpr int64_t kStep = 128;      // four waves of 32 positions
-    constexpr int64_t kBlocks = 1024;   // four blocks for every CU
+    constexpr int64_t kBlocks = 512;    // two blocks for every CU
     int64_t span = table_pages * page;
     // a window may start inside a tile of 32
     if (window) span = std::min(span, window + 31);
@@ -77,12 +78,12 @@ inline AttnPlan attn_plan(int64_t B, int64_t heads, int64_t q_heads, int64_t dim
     const int64_t want = std::max<int64_t>(1, (kBlocks + rows - 1) / rows);
     int64_t chunk = (span + want - 1) / want;
     chunk = (chunk + kStep - 1) / kStep * kStep;
-    chunk = std::min<int64_t>(std::max<int64_t>(chunk, 2 * kStep), 4096);
+    chunk = std::min<int64_t>(std::max<int64_t>(chunk, 2 * kStep), kAttnMaxChunk);
     AttnPlan p;
     p.chunk = (int)chunk;
     p.splits = (int)std::max<int64_t>(1, (span + chunk - 1) / chunk);
     const int64_t G = (dim + kGroup - 1) / kGroup;
-    p.bytes = p.splits == 1 ? 0 : B * q_heads * p.splits * (G * kGroup + 2) * 4;
+    p.bytes = p.splits == 1 ? 0 : B * q_heads * p.splits * (G * kGroup + 4) * 4;
     return p;
 }
 hipError_t launch_attn_decode(const AttnArgs& a, void* workspace, hipStream_t s);
