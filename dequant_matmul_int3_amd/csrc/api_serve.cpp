@@ -128,7 +128,8 @@ bool attn_sizes_ok(int64_t B, int64_t q_heads, int64_t heads, int64_t dim, int64
     return kv_sizes_ok(1, page, heads, dim) && B >= 1 && B <= qt::kAttnMaxBatch &&
            q_heads >= 1 && q_heads % heads == 0 && q_heads / heads <= qt::kAttnMaxGroupHeads &&
            table_pages >= 1 && table_pages <= qt::kKvMaxSlots / page && window >= 0 &&
-           heads * ((q_heads / heads + 15) / 16) <= 65535;
+           qt::attn_fits(qt::attn_plan(B, heads, q_heads, dim, table_pages, page, window), B,
+                         heads, q_heads);
 }
 
 }  // namespace

@@ -91,8 +91,9 @@ hipError_t launch_attn_decode(const AttnArgs& a, void* workspace, hipStream_t s)
     const int64_t qe = a.bf16 ? 8 : 4;  // elements of 16 bytes
     const bool q_vec = a.c.dim % 8 == 0 && a.ldq % qe == 0 &&
                        (reinterpret_cast<uintptr_t>(a.Q) & 15) == 0;
-    AttnKernelArgs k{a, p.chunk, p.splits, (a.q_heads / a.c.heads + 15) / 16, 0, 0, q_vec,
-                     static_cast<float*>(workspace)};
+    const uint32_t rows = (uint32_t)(a.B * a.c.heads);
+    AttnKernelArgs k{a, p.chunk, p.splits, (a.q_heads / a.c.heads + 15) / 16,
+                     rows, rows * (uint32_t)p.splits, 0, 0, q_vec, static_cast<float*>(workspace)};
     // x / page = (x * mul >> 32) >> sh for x < 2^31: mul = ceil(2^(32 + sh) / page)
     // with 2^sh < page <= 2^(sh + 1), so that mul < 2^32 and the error x / 2^(32 + sh) is
     // below 1 / page

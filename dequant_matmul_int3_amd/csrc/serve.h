@@ -18,7 +18,7 @@ constexpr int64_t kKvMaxHeads = 1024;
 constexpr int64_t kKvMaxDim = 256;
 constexpr int64_t kAttnMaxBatch = 65535;
 constexpr int64_t kAttnMaxGroupHeads = 256;  // query heads per key-value head
-constexpr int64_t kAttnMaxChunk = 8192;
+constexpr int64_t kAttnMaxChunk = 2048;
 
 // A paged cache: codes [pages][heads][page][groups * 8 bits] and scales
 // [pages][heads][page][groups] of the keys and of the values.
@@ -85,6 +85,11 @@ inline AttnPlan attn_plan(int64_t B, int64_t heads, int64_t q_heads, int64_t dim
     const int64_t G = (dim + kGroup - 1) / kGroup;
     p.bytes = p.splits == 1 ? 0 : B * q_heads * p.splits * (G * kGroup + 4) * 4;
     return p;
+}
+// Blocks of the first launch, which are numbered in 31 bits.
+inline bool attn_fits(const AttnPlan& p, int64_t B, int64_t heads, int64_t q_heads) {
+    return (B * heads * p.splits + 7) / 8 * 8 * ((q_heads / heads + 15) / 16) < (int64_t(1) << 31) &&
+           B * q_heads < (int64_t(1) << 24);  // blocks of 256 threads of the second
 }
 hipError_t launch_attn_decode(const AttnArgs& a, void* workspace, hipStream_t s);
 
