@@ -25,7 +25,7 @@ def test_workspace_sizes():
     w = qt.qt_attn_decode_workspace_bytes
     assert w(1, 32, 8, 128, 16, 16) == 0                    # one chunk
     assert w(1, 32, 8, 128, 64, 64) > 0                     # a long context is cut
-    assert w(256, 32, 8, 128, 64, 64) == 0                  # a batch fills the card uncut
+    assert w(256, 32, 8, 128, 32, 64) == 0                  # a batch fills the card uncut
     assert w(1, 32, 8, 128, 4096, 64, window=100) == 0      # a window bounds the span
     assert w(1, 8, 8, 64, 1 << 20, 16) == 8 * 8192 * 68 * 4  # chunks of 2048 at most
     for bad in ((0, 8, 8, 64, 1, 16), (1, 8, 3, 64, 1, 16), (1, 8, 8, 64, 0, 16),
