@@ -40,7 +40,8 @@ EXTRA = {"grouped.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          "moe.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          "factor.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          "attn.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-         "attn_f32.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+         "attn_f32.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+         "moe_few.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def _compile(src, verbose):

@@ -46,7 +46,7 @@ struct AttnKernelArgs {
     AttnArgs a;
     int chunk, splits, tiles;   // tiles: of 16 query heads per key-value head
     uint32_t rows, items;       // B heads; rows * splits
-    uint32_t page_mul, page_sh; // x / page for x < 2^31
+    FastDiv page;
     bool q_vec;                 // eight query values may be loaded at once
     float* part;                // splits > 1: [rows][splits] x (G 64 values, max, sum, 2 unused)
 };
@@ -271,7 +271,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_decode_kernel(const Attn
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const uint32_t pos = min((uint32_t)(first + lane * kHop) + 16u * h, (uint32_t)reach - 16u);
-        const uint32_t pi = (uint32_t)(((uint64_t)pos * x.page_mul) >> 32) >> x.page_sh;
+        const uint32_t pi = x.page.div(pos);
         place_at[h] = (int)(pos - pi * (uint32_t)a.c.page);
         place_id[h] = table[pi];
     }

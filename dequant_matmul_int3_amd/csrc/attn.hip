@@ -93,12 +93,8 @@ hipError_t launch_attn_decode(const AttnArgs& a, void* workspace, hipStream_t s)
                        (reinterpret_cast<uintptr_t>(a.Q) & 15) == 0;
     const uint32_t rows = (uint32_t)(a.B * a.c.heads);
     AttnKernelArgs k{a, p.chunk, p.splits, (a.q_heads / a.c.heads + 15) / 16,
-                     rows, rows * (uint32_t)p.splits, 0, 0, q_vec, static_cast<float*>(workspace)};
-    // x / page = (x * mul >> 32) >> sh for x < 2^31: mul = ceil(2^(32 + sh) / page)
-    // with 2^sh < page <= 2^(sh + 1), so that mul < 2^32 and the error x / 2^(32 + sh) is
-    // below 1 / page
-    while ((int64_t(2) << k.page_sh) < a.c.page) ++k.page_sh;
-    k.page_mul = (uint32_t)(((uint64_t(1) << (32 + k.page_sh)) + a.c.page - 1) / a.c.page);
+                     rows, rows * (uint32_t)p.splits,
+                     FastDiv::of((uint32_t)a.c.page), q_vec, static_cast<float*>(workspace)};
     hipError_t e = a.bf16 ? launch_attn_bf16(k, s) : launch_attn_f32(k, s);
     if (e != hipSuccess || p.splits == 1) return e;
     return a.bf16 ? join<false>(k, s) : join<true>(k, s);

@@ -17,7 +17,7 @@ namespace {
 constexpr int kUpWaves = 4, kDownWaves = 8;
 // The first launch keeps its blocks for all tiles; four of them fit a CU.
 constexpr int kUpBlocks = 4 * 256;
-// Inputs staged at a time: 12 rows of at least 16 groups (a round of the
+// Tokens of a pass at most, and the inputs staged at a time: 12 rows of at least 16 groups (a round of the
 // waves' chunks), rows 16 bytes apart in the banks.
 constexpr int kPassRows = 12;
 constexpr int kSlabBytes = kPassRows * (4 * kUpWaves * 128 + 16);
@@ -26,11 +26,11 @@ struct FewKernelArgs {
     FewArgs a;
     int GD, GF;          // groups of D and of F
     int pairs;           // T k
-    int32_t* count;      // active experts; from 4 on: [pairs] expert, [pairs] first pair
-    float* weight;       // [pairs][T] weight of (active expert, token), 0: not its token
-    int32_t* prow;       // [pairs][T] pair of (active expert, token)
+    int32_t* count;      // active experts; from 4 on: expert | first pair << 16 of each
+    int32_t* token;      // [pairs] token of a pair; pairs go by expert, then token
+    float* weight;       // [pairs] weight of a pair
     uint16_t* planes;    // [pieces][pairs][64 GF]
-    bool x_vec;          // four inputs may be loaded at once
+    bool x_vec;          // eight inputs may be loaded at once
 };
 
 // A logit's bits made monotone as an unsigned number, above 0 (-0 as +0).
@@ -145,19 +145,42 @@ __device__ __forceinline__ void route(const FewKernelArgs& x, Route& r, Picks& c
     __syncthreads();
 }
 
-// Sixteen codes as two exact operands: v for int3, 16 v for int4 (the nibbles
-// of a word as the high halves of signed bytes).
+// Sixteen codes as two exact operands: v for int3 (the byte table and packed
+// conversion of exact_quarter, without its reordering), 16 v for int4 (the
+// nibbles of a word as the high halves of signed bytes).  Both come in the
+// order 0 4 1 5 2 6 3 7 within each eight, which is the order that the inputs
+// are staged in.
+__device__ __forceinline__ constexpr int code_at(int place) { return (place & 1) * 4 + (place >> 1); }
+__device__ __forceinline__ constexpr int place_of(int code) { return (code & 3) * 2 + (code >> 2); }
 template <int BITS>
 __device__ __forceinline__ void operands(const Quarter& q, int h4, u32x4_t& lo8, u32x4_t& hi8) {
     if constexpr (BITS == 3) {
-        exact_quarter(q, h4, 3, lo8, hi8);
+        // byte b of f[i] is code 4 b + i
+        const uint32_t b = __builtin_amdgcn_perm(0u, q.b, high_sel(h4));
+        const uint32_t t = (b | (b << 4)) & 0x0F0F0F0Fu;
+        uint32_t f[4];
+        f[0] = (q.a & 0x03030303u) | ((t << 2) & 0x04040404u);
+        f[1] = ((q.a >> 2) & 0x03030303u) | ((t << 1) & 0x04040404u);
+        f[2] = ((q.a >> 4) & 0x03030303u) | (t & 0x04040404u);
+        f[3] = ((q.a >> 6) & 0x03030303u) | ((t >> 1) & 0x04040404u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[i] = __builtin_amdgcn_perm(0x06040200u, 0x82848688u, f[i]);
+            lo8[i] = __builtin_bit_cast(
+                uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f[i], 256.0f, false));
+            hi8[i] = __builtin_bit_cast(
+                uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f[i], 256.0f, true));
+        }
     } else {
         auto word = [](uint32_t w) {
+            // byte b of e is code 2 b, of o code 2 b + 1
             const uint32_t t = w ^ 0x88888888u, e = (t << 4) & 0xF0F0F0F0u, o = t & 0xF0F0F0F0u;
-            auto at = [](uint32_t v, int b) { return __float_as_uint((float)(int8_t)(v >> (8 * b))); };
+            auto at = [&](int c) {
+                return __float_as_uint((float)(int8_t)((c & 1 ? o : e) >> (8 * (c >> 1))));
+            };
             u32x4_t r;
 #pragma unroll
-            for (int b = 0; b < 4; ++b) r[b] = __builtin_amdgcn_perm(at(o, b), at(e, b), 0x07060302u);
+            for (int i = 0; i < 4; ++i) r[i] = __builtin_amdgcn_perm(at(4 + i), at(i), 0x07060302u);
             return r;
         };
         lo8 = word(q.a);
@@ -193,17 +216,16 @@ __global__ __launch_bounds__(64 * kUpWaves) void moe_few_up_kernel(const FewKern
     const int rounds = ((G + 3) / 4 + W - 1) / W;  // of the waves' chunks
     if (blockIdx.x == 0) {
         if (tid == 0) x.count[0] = rt.n;
-        for (int i = tid; i < rt.n; i += 64 * W) {
-            x.count[4 + i] = (int)(rt.act[i] & 0xFFFFu);
-            x.count[4 + x.pairs + i] = (int)(rt.act[i] >> 16);
-        }
+        for (int i = tid; i < rt.n; i += 64 * W) x.count[4 + i] = (int)rt.act[i];
         for (int i = tid; i < rt.n * a.T; i += 64 * W) {
             const int n = i / a.T, t = i % a.T, e = (int)(rt.act[n] & 0xFFFFu);
+            const uint32_t m = rt.mask[e];
+            if (!(m >> t & 1)) continue;
             float w = 0.0f;
             for (int j = 0; j < a.k; ++j) w = lds.picks.sel[t][j] == e ? lds.picks.wgt[t][j] : w;
-            const uint32_t m = rt.mask[e];
-            x.weight[i] = w;
-            x.prow[i] = (int)(rt.act[n] >> 16) + (m >> t & 1 ? __popc(m & ((1u << t) - 1)) : 0);
+            const int p = (int)(rt.act[n] >> 16) + __popc(m & ((1u << t) - 1));
+            x.token[p] = t;
+            x.weight[p] = w;
         }
     }
     // this block's tiles, next to each other: mostly of one expert
@@ -231,6 +253,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void moe_few_up_kernel(const FewKern
     };
     f32x4_t acc[2];
     const uint8_t* arow = lds.stage;
+    int regs = 1;  // registers of the results that hold rows
     auto mul = [&](int c, int s0, const Chunk& k) __attribute__((always_inline)) {
         const int q0 = 4 * (c * W + wave);
         Quarter qg[4], qu[4];
@@ -256,267 +279,311 @@ __global__ __launch_bounds__(64 * kUpWaves) void moe_few_up_kernel(const FewKern
             for (int z = 0; z < 2; ++z) {
                 const f32x4_t p = mma(x1, wh[z], mma(x0, wl[z], f32x4_t{0.f, 0.f, 0.f, 0.f}));
                 const float s = __uint_as_float(z == 0 ? sg[j] : su[j]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) acc[z][r] = __builtin_fmaf(s, p[r], acc[z][r]);
+                acc[z][0] = __builtin_fmaf(s, p[0], acc[z][0]);
+                if (regs > 1) {  // uniform
+                    acc[z][1] = __builtin_fmaf(s, p[1], acc[z][1]);
+                    acc[z][2] = __builtin_fmaf(s, p[2], acc[z][2]);
+                }
             }
         }
     };
-    int have_e = -1, have_p = -1, have_s = -1;  // what the stage holds
-    Chunk k0, k1;
-    load(it0, 0, k0);
-    for (int it = it0; it < it1; ++it) {
-        const uint32_t act = rt.act[it / FT];
-        const int e = (int)(act & 0xFFFFu), f0 = it % FT * 16;
-        const uint32_t who = rt.mask[e];
-        const int n = __popc(who);
-        // tokens in passes of RT; a pass reads the weights (again)
-        for (int p0 = 0; p0 < n; p0 += RT) {
-            const int nt = min(RT, n - p0);
-            const int rows = BF16 ? nt : 3 * nt;
-            // rounds staged at a time
-            const int S = min((kSlabBytes / rows - 16) / (512 * W), rounds);
-            const int pitch = S * (512 * W) + 16;
-            const int lrow = BF16 ? min(l16, nt - 1) : min(l16 >> 2, nt - 1) * 3 + min(l16 & 3, 2);
-            arow = lds.stage + lrow * pitch + 32 * h4;
-            acc[0] = acc[1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-            const bool tail = p0 + RT >= n;  // the tile's last pass
-            for (int c0 = 0; c0 < rounds; c0 += S) {
-                if (have_e != e || have_p != p0 || have_s != c0) {
-                    have_e = e;
-                    have_p = p0;
-                    have_s = c0;
-                    lds_barrier();  // the stage is read
-                    // token rows of the rounds, zero past D
-                    const int vals = min(S, rounds - c0) * (64 * W);  // of four
-                    uint32_t left = who;
-                    for (int z = 0; z < p0; ++z) left &= left - 1;
-                    for (int m = 0; m < nt; ++m, left &= left - 1) {
-                        const int64_t t = __ffs(left) - 1;
-                        for (int v = tid; v < vals; v += 64 * W) {
-                            const int64_t d = (int64_t)c0 * (256 * W) + 4 * v;
-                            uint32_t q[4], b[3][4];
-                            if (x.x_vec) {
-                                const int64_t at = t * a.D + (d < a.D ? d : 0);
-                                if constexpr (BF16) {
-                                    const u32x2_t z = *reinterpret_cast<const u32x2_t*>(
-                                        static_cast<const uint16_t*>(a.X) + at);
-                                    q[0] = z.x & 0xFFFFu;
-                                    q[1] = z.x >> 16;
-                                    q[2] = z.y & 0xFFFFu;
-                                    q[3] = z.y >> 16;
-                                } else {
-                                    const u32x4_t z = *reinterpret_cast<const u32x4_t*>(
-                                        static_cast<const float*>(a.X) + at);
+    // A block's work as steps of one round each: tile after tile, its tokens in
+    // passes of RT (a pass reads the weights again).
+    struct Step {
+        int it, p0, c;
+    };
+    auto tokens_of = [&](int it) __attribute__((always_inline)) {
+        return __builtin_amdgcn_readfirstlane((int)rt.mask[rt.act[it / FT] & 0xFFFFu]);
+    };
+    auto advance = [&](Step& t) __attribute__((always_inline)) {
+        if (t.it >= it1 || ++t.c < rounds) return;
+        t.c = 0;
+        t.p0 += RT;
+        if (a.T <= RT || t.p0 >= __popc(tokens_of(t.it))) {
+            t.p0 = 0;
+            ++t.it;
+        }
+    };
+    Step now{it0, 0, 0}, ahead = now;
+    auto load_ahead = [&](Chunk& k) __attribute__((always_inline)) {
+        // past the last step its loads repeat
+        load(min(ahead.it, it1 - 1), ahead.it < it1 ? ahead.c : rounds - 1, k);
+        advance(ahead);
+    };
+    int have_e = -1, have_p = 0, have_c = 0;  // what the stage holds: rounds have_c ..
+    int S = 1;                                // .. have_c + S - 1
+    // the rows of the pass's tokens for rounds c .. c + S - 1, zero past D
+    auto stage = [&](int e, int who, int nt) __attribute__((always_inline)) {
+        const int rows = BF16 ? nt : 3 * nt;
+        S = min((kSlabBytes / rows - 16) / (512 * W), rounds);
+        const int pitch = S * (512 * W) + 16;
+        // bf16: token m is row 4 (m % 4) + m / 4, so that up to four tokens take one
+        // register of the results; f32: row 4 m + piece
+        const int lrow = BF16 ? min(4 * (l16 & 3) + (l16 >> 2), nt - 1)
+                              : min(l16 >> 2, nt - 1) * 3 + min(l16 & 3, 2);
+        regs = BF16 ? (nt + 3) / 4 : 3;
+        arow = lds.stage + lrow * pitch + 32 * h4;
+        have_e = e;
+        have_p = now.p0;
+        have_c = now.c;
+        lds_barrier();  // the stage is read
+        const int vals = min(S, rounds - now.c) * (32 * W);  // of eight
+        uint32_t left = (uint32_t)who;
+        for (int z = 0; z < now.p0; ++z) left &= left - 1;
+        for (int m = 0; m < nt; ++m, left &= left - 1) {
+            const int64_t t = __ffs(left) - 1;
+            for (int v = tid; v < vals; v += 64 * W) {
+                const int64_t d = (int64_t)now.c * (256 * W) + 8 * v;
+                uint32_t q[8], b[3][8];
+                if (x.x_vec) {
+                    const int64_t at = t * a.D + (d < a.D ? d : 0);
+                    if constexpr (BF16) {
+                        const u32x4_t z = *reinterpret_cast<const u32x4_t*>(
+                            static_cast<const uint16_t*>(a.X) + at);
 #pragma unroll
-                                    for (int y = 0; y < 4; ++y) q[y] = z[y];
-                                }
-                            } else {
+                        for (int y = 0; y < 8; ++y) q[y] = y & 1 ? z[y >> 1] >> 16 : z[y >> 1] & 0xFFFFu;
+                    } else {
+                        const u32x4_t* z =
+                            reinterpret_cast<const u32x4_t*>(static_cast<const float*>(a.X) + at);
+                        const u32x4_t z0 = z[0], z1 = z[1];
 #pragma unroll
-                                for (int y = 0; y < 4; ++y) {
-                                    const int64_t at = t * a.D + (d + y < a.D ? d + y : 0);
-                                    q[y] = BF16 ? (uint32_t)static_cast<const uint16_t*>(a.X)[at]
-                                                : static_cast<const uint32_t*>(a.X)[at];
-                                }
-                            }
-#pragma unroll
-                            for (int y = 0; y < 4; ++y) {
-                                if (d + y >= a.D) q[y] = 0u;
-                                if constexpr (BF16)
-                                    b[0][y] = q[y];
-                                else
-                                    split3(__uint_as_float(q[y]), b[0][y], b[1][y], b[2][y]);
-                            }
-#pragma unroll
-                            for (int pc = 0; pc < (BF16 ? 1 : 3); ++pc)
-                                *reinterpret_cast<u32x2_t*>(
-                                    lds.stage + (BF16 ? m : 3 * m + pc) * pitch + 8 * v) =
-                                    u32x2_t{b[pc][0] | b[pc][1] << 16, b[pc][2] | b[pc][3] << 16};
-                        }
+                        for (int y = 0; y < 8; ++y) q[y] = y < 4 ? z0[y & 3] : z1[y & 3];
                     }
-                    lds_barrier();
-                }
-                const int c1 = min(rounds, c0 + S);
-                for (int c = c0; c < c1; ++c) {
-                    // the next chunk: of this pass, of the next pass or of the next tile
-                    const bool on = c + 1 < rounds;
-                    load(on || !tail ? it : min(it + 1, it1 - 1), on ? c + 1 : 0, k1);
-                    mul(c, c0 * (4 * W), k0);
-                    k0 = k1;
-                }
-            }
-            lds_barrier();  // the sums of the pass before are read
-            red[wave][0][lane] = acc[0];
-            red[wave][1][lane] = acc[1];
-            lds_barrier();
-            // element (row m, column c): lane 16 (m / 4) + c, register m % 4
-            for (int z = tid; z < nt * 16; z += 64 * W) {
-                const int m = z >> 4, c = z & 15;
-                float s[2] = {0.0f, 0.0f};
-#pragma unroll
-                for (int y = 0; y < 2; ++y)
-#pragma unroll
-                    for (int w = 0; w < W; ++w) {
-                        if constexpr (BF16) {
-                            s[y] += red[w][y][16 * (m >> 2) + c][m & 3];
-                        } else {
-                            const f32x4_t v = red[w][y][16 * m + c];
-                            s[y] += (v[0] + v[1]) + v[2];
-                        }
-                    }
-                const bool in = f0 + c < a.F;
-                const float h = in ? act_value(s[0], a.act) * s[1] : 0.0f;
-                const int64_t at = (int64_t)((int)(act >> 16) + p0 + m) * (x.GF * 64) + f0 + c;
-                const int64_t plane = (int64_t)x.pairs * x.GF * 64;
-                if constexpr (BF16) {
-                    const float hi = __uint_as_float(__float_as_uint(h) & 0xFFFF0000u);
-                    x.planes[at] = (uint16_t)(__float_as_uint(hi) >> 16);
-                    x.planes[plane + at] = __builtin_bit_cast(uint16_t, (__bf16)(h - hi));
                 } else {
-                    uint32_t b0, b1, b2;
-                    split3(h, b0, b1, b2);
-                    x.planes[at] = (uint16_t)b0;
-                    x.planes[plane + at] = (uint16_t)b1;
-                    x.planes[2 * plane + at] = (uint16_t)b2;
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) {
+                        const int64_t at = t * a.D + (d + y < a.D ? d + y : 0);
+                        q[y] = BF16 ? (uint32_t)static_cast<const uint16_t*>(a.X)[at]
+                                    : static_cast<const uint32_t*>(a.X)[at];
+                    }
                 }
+#pragma unroll
+                for (int y = 0; y < 8; ++y) {
+                    const uint32_t z = d + code_at(y) < a.D ? q[code_at(y)] : 0u;
+                    if constexpr (BF16)
+                        b[0][y] = z;
+                    else
+                        split3(__uint_as_float(z), b[0][y], b[1][y], b[2][y]);
+                }
+#pragma unroll
+                for (int pc = 0; pc < (BF16 ? 1 : 3); ++pc)
+                    *reinterpret_cast<u32x4_t*>(lds.stage + (BF16 ? m : 3 * m + pc) * pitch +
+                                                16 * v) =
+                        u32x4_t{b[pc][0] | b[pc][1] << 16, b[pc][2] | b[pc][3] << 16,
+                                b[pc][4] | b[pc][5] << 16, b[pc][6] | b[pc][7] << 16};
             }
         }
+        lds_barrier();
+    };
+    // the pass's sums of all waves, and its activations
+    auto finish = [&](int first, int nt, int f0) __attribute__((always_inline)) {
+        lds_barrier();  // the sums of the pass before are read
+        red[wave][0][lane] = acc[0];
+        red[wave][1][lane] = acc[1];
+        lds_barrier();
+        for (int z = tid; z < nt * 16; z += 64 * W) {
+            const int m = z >> 4, c = z & 15;
+            float s[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    if constexpr (BF16) {
+                        s[y] += red[w][y][16 * (m & 3) + c][m >> 2];
+                    } else {
+                        const f32x4_t v = red[w][y][16 * m + c];
+                        s[y] += (v[0] + v[1]) + v[2];
+                    }
+                }
+            const bool in = f0 + c < a.F;
+            const float h = in ? act_value(s[0], a.act) * s[1] : 0.0f;
+            const int64_t at =
+                (int64_t)(first + m) * (x.GF * 64) + f0 + (c & 8) + place_of(c & 7);
+            const int64_t plane = (int64_t)x.pairs * x.GF * 64;
+            if constexpr (BF16) {
+                const float hi = __uint_as_float(__float_as_uint(h) & 0xFFFF0000u);
+                x.planes[at] = (uint16_t)(__float_as_uint(hi) >> 16);
+                x.planes[plane + at] = __builtin_bit_cast(uint16_t, (__bf16)(h - hi));
+            } else {
+                uint32_t b0, b1, b2;
+                split3(h, b0, b1, b2);
+                x.planes[at] = (uint16_t)b0;
+                x.planes[plane + at] = (uint16_t)b1;
+                x.planes[2 * plane + at] = (uint16_t)b2;
+            }
+        }
+    };
+    // one step from the chunk in k; false after the last one
+    auto turn = [&](const Chunk& k) __attribute__((always_inline)) {
+        const uint32_t act = __builtin_amdgcn_readfirstlane((int)rt.act[now.it / FT]);
+        const int e = (int)(act & 0xFFFFu), who = tokens_of(now.it);
+        const int nt = min(RT, __popc(who) - now.p0);
+        if (have_e != e || have_p != now.p0 || now.c < have_c || now.c >= have_c + S)
+            stage(e, who, nt);
+        if (now.c == 0) acc[0] = acc[1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        mul(now.c, have_c * (4 * W), k);
+        if (now.c + 1 == rounds) finish((int)(act >> 16) + now.p0, nt, now.it % FT * 16);
+        advance(now);
+        return now.it < it1;
+    };
+    // the weights two steps ahead
+    Chunk k0, k1, k2;
+    load_ahead(k0);
+    load_ahead(k1);
+    for (;;) {
+        load_ahead(k2);
+        if (!turn(k0)) break;
+        load_ahead(k0);
+        if (!turn(k1)) break;
+        load_ahead(k1);
+        if (!turn(k2)) break;
     }
 }
 
 // Second launch: a block of 8 waves owns 16 outputs of every token and walks
-// all active experts; its waves take chunks of four groups in turn.  A row of
-// the matrix operand is a token's piece, so that the sums over the experts
-// stay in place; rows of tokens that an expert does not have get the weight 0.
-// MT: row tiles of 8 (two pieces) or 4 (three) tokens.
+// all active experts; its waves take chunks of four groups in turn and add each
+// chunk's products, times the pairs' weights, to sums of their own in LDS, which
+// are added at the end in wave order.  Rows of the matrix operand are the
+// pieces of an expert's tokens.
 //
-// A chunk's weights and activations are loaded a chunk ahead, its expert and
-// its tokens' pairs another one: each is an address for the next.
-template <int DB, int MT, bool BF16>
-__global__ __launch_bounds__(64 * kDownWaves) void moe_few_down_kernel(const FewKernelArgs x) {
+// Weights are loaded three chunks ahead and activations one; a chunk's expert
+// and pairs, the addresses of both, come from LDS.
+template <int DB, bool BF16>
+__global__ __launch_bounds__(64 * kDownWaves) __attribute__((amdgpu_waves_per_eu(4))) void
+moe_few_down_kernel(const FewKernelArgs x) {
     constexpr int W = kDownWaves;
-    constexpr int TPT = BF16 ? 8 : 4;  // tokens of a row tile
+    constexpr int PT = BF16 ? 2 : 4;   // rows of a token: its pieces (and one unused)
+    constexpr int RT = 16 / PT;        // tokens of a row tile
+    constexpr int NW = 4 / PT;         // tokens of a lane's four result rows
     constexpr int BY = DB == 3 ? kGroupBytes : kGroupBytesI4;
-    constexpr int NW = BF16 ? 2 : 1;   // tokens of a lane's four result rows
     const FewArgs& a = x.a;
-    __shared__ __attribute__((aligned(16))) f32x4_t red[W][MT][64];
+    constexpr int kPairs = kFewMaxTokens * kFewMaxTopK;
+    __shared__ uint32_t act[kPairs + 1];
+    __shared__ int32_t token[kPairs];
+    __shared__ float weight[kPairs];
+    __shared__ float sums[W][kFewMaxTokens][16];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int h4 = lane >> 4, l16 = lane & 15;
     const int G = x.GF, nchunk = (G + 3) / 4;
     const int64_t o0 = (int64_t)blockIdx.x * 16;
     const int n = x.count[0], units = n * nchunk;
+    for (int i = tid; i < x.pairs; i += 64 * W) {
+        act[i] = (uint32_t)x.count[4 + i];
+        token[i] = x.token[i];
+        weight[i] = x.weight[i];
+    }
+    for (int i = lane; i < a.T * 16; i += 64) sums[wave][i >> 4][i & 15] = 0.0f;
+    __syncthreads();
+    if (tid == 0) act[n] = (uint32_t)x.pairs << 16;
+    __syncthreads();
     const int64_t orow = min<int64_t>(o0 + l16, a.D - 1);
     const int piece = BF16 ? l16 & 1 : min(l16 & 3, 2);
     const uint16_t* plane = x.planes + piece * ((int64_t)x.pairs * G * 64) + 16 * h4;
-    f32x4_t acc[MT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) acc[mt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-    struct Who {  // of a unit: its expert, this lane's operand row and result rows
-        int e, row[MT];
-        float wt[MT][NW];
-    };
     struct Weights {
         RowGroup<DB> w;
         float s;
     };
-    auto look = [&](int u, Who& k) __attribute__((always_inline)) {
-        const int i = min(u, units - 1) / nchunk;
-        k.e = x.count[4 + i];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            k.row[mt] = x.prow[i * a.T + min(mt * TPT + (BF16 ? l16 >> 1 : l16 >> 2), a.T - 1)];
-#pragma unroll
-            for (int z = 0; z < NW; ++z) {
-                const int t = mt * TPT + (BF16 ? 2 * h4 + z : h4);
-                const float v = x.weight[i * a.T + min(t, a.T - 1)];
-                k.wt[mt][z] = t < a.T ? v : 0.0f;
-            }
-        }
-    };
-    auto load = [&](int u, const Who& k, Weights& w) __attribute__((always_inline)) {
-        const int q = min(4 * (min(u, units - 1) % nchunk) + h4, G - 1);
-        const int64_t r = ((int64_t)k.e * a.D + orow) * G + q;
+    auto expert_of = [&](int u) __attribute__((always_inline)) { return min(u, units - 1) / nchunk; };
+    auto load = [&](int u, Weights& w) __attribute__((always_inline)) {
+        const int i = expert_of(u);
+        const int q = min(4 * (min(u, units - 1) - i * nchunk) + h4, G - 1);
+        const int64_t r = ((int64_t)(act[i] & 0xFFFFu) * a.D + orow) * G + q;
         w.w.load(a.down.packed + r * BY);
         w.s = a.down.scales[r];
     };
-    // group j of the unit's operand rows (past the row a valid group, scale 0)
-    auto operand = [&](int u, const Who& k, int j, u32x4_t (&v)[MT][2])
+    // this lane's operand row of unit u's first group, tokens from p0 on
+    auto row_of = [&](int u, int p0) __attribute__((always_inline)) {
+        const int i = expert_of(u), first = (int)(act[i] >> 16), end = (int)(act[i + 1] >> 16);
+        const int p = min(first + p0 + l16 / PT, end - 1);
+        return plane + ((int64_t)p * G + 4 * (min(u, units - 1) - i * nchunk)) * 64;
+    };
+    // group j of it (past the row the last one, scale 0)
+    auto operand = [&](const uint16_t* row, int left, int j, u32x4_t (&v)[2])
                        __attribute__((always_inline)) {
-        const int q = min(4 * (min(u, units - 1) % nchunk) + j, G - 1);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            const u32x4_t* p =
-                reinterpret_cast<const u32x4_t*>(plane + ((int64_t)k.row[mt] * G + q) * 64);
-            v[mt][0] = p[0];
-            v[mt][1] = p[1];
-        }
+        const u32x4_t* p = reinterpret_cast<const u32x4_t*>(row + min(j, left) * 64);
+        v[0] = p[0];
+        v[1] = p[1];
+    };
+    auto left_of = [&](int u) __attribute__((always_inline)) {
+        return G - 1 - 4 * (min(u, units - 1) - expert_of(u) * nchunk);
     };
     if (wave < units) {
-        Who cur, next, then;
-        Weights w0, w1;
-        u32x4_t v[4][MT][2];
-        look(wave, cur);
-        look(wave + W, next);
-        load(wave, cur, w0);
+        Weights w[4];
+        u32x4_t v[4][2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) operand(wave, cur, j, v[j]);
-        for (int u = wave; u < units; u += W) {
-            look(u + 2 * W, then);
-            load(u + W, next, w1);
+        for (int i = 0; i < 3; ++i) load(wave + i * W, w[i]);
+        {
+            const uint16_t* row = row_of(wave, 0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) operand(row, left_of(wave), j, v[j]);
+        }
+        auto turn = [&](int u, const Weights& w0, Weights& w3) __attribute__((always_inline)) {
+            load(u + 3 * W, w3);
+            const int i = u / nchunk, first = (int)(act[i] >> 16), end = (int)(act[i + 1] >> 16);
+            const uint16_t* ahead = row_of(u + W, 0);
+            const int left = left_of(u + W);
             Quarter qd[4];
             w0.w.quarters(qd);
             uint32_t sd[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                sd[j] = 4 * (u % nchunk) + h4 < G ? __float_as_uint(w0.s * kUnit<DB>) : 0u;
+                sd[j] = 4 * (u - i * nchunk) + h4 < G ? __float_as_uint(w0.s * kUnit<DB>) : 0u;
             transpose_rows(sd);
-            f32x4_t part[MT];
+            auto product = [&](bool last) __attribute__((always_inline)) {
+                f32x4_t part = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) part[mt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                u32x4_t wl, wh;
-                operands<DB>(qd[j], h4, wl, wh);
-                const float s = __uint_as_float(sd[j]);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
+                for (int j = 0; j < 4; ++j) {
+                    u32x4_t wl, wh;
+                    operands<DB>(qd[j], h4, wl, wh);
+                    const float s = __uint_as_float(sd[j]);
                     const f32x4_t p =
-                        mma(v[j][mt][1], wh, mma(v[j][mt][0], wl, f32x4_t{0.f, 0.f, 0.f, 0.f}));
+                        mma(v[j][1], wh, mma(v[j][0], wl, f32x4_t{0.f, 0.f, 0.f, 0.f}));
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) part[mt][r] = __builtin_fmaf(s, p[r], part[mt][r]);
+                    for (int r = 0; r < 4; ++r) part[r] = __builtin_fmaf(s, p[r], part[r]);
+                    if (last) operand(ahead, left, j, v[j]);
                 }
-                operand(u + W, next, j, v[j]);
+                return part;
+            };
+            // the products of the tokens from p0 on, to this wave's sums
+            auto add = [&](int p0, const f32x4_t& part) __attribute__((always_inline)) {
+                lds_wave_sync();  // another lane may have added to this token before
+#pragma unroll
+                for (int z = 0; z < NW; ++z) {
+                    const int p = first + p0 + NW * h4 + z;
+                    if (p < end) {
+                        const float y = BF16 ? part[2 * z] + part[2 * z + 1]
+                                             : (part[0] + part[1]) + part[2];
+                        float& sum = sums[wave][token[p]][l16];
+                        sum = __builtin_fmaf(weight[p], y, sum);
+                    }
+                }
+            };
+            // more tokens than a row tile: their rows are loaded as they come
+            for (int p0 = 0; p0 + RT < end - first; p0 += RT) {
+                add(p0, product(false));
+                const uint16_t* row = row_of(u, p0 + RT);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) operand(row, left_of(u), j, v[j]);
             }
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    // another token's products, whatever they are, do not count
-                    const float w = cur.wt[mt][BF16 ? r >> 1 : 0];
-                    acc[mt][r] = __builtin_fmaf(w, w != 0.0f ? part[mt][r] : 0.0f, acc[mt][r]);
-                }
-            cur = next;
-            next = then;
-            w0 = w1;
+            add((end - first - 1) / RT * RT, product(true));
+            return u + W < units;
+        };
+        for (int u = wave;; u += 4 * W) {
+            if (!turn(u, w[0], w[3])) break;
+            if (!turn(u + W, w[1], w[0])) break;
+            if (!turn(u + 2 * W, w[2], w[1])) break;
+            if (!turn(u + 3 * W, w[3], w[2])) break;
         }
     }
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) red[wave][mt][lane] = acc[mt];
     __syncthreads();
     for (int z = tid; z < a.T * 16; z += 64 * W) {
-        const int t = z >> 4, c = z & 15, mt = t / TPT, m = t % TPT;
+        const int t = z >> 4, c = z & 15;
         if (o0 + c >= a.D) continue;
         float s = 0.0f;
-        for (int w = 0; w < W; ++w) {
-            if constexpr (BF16) {
-                const f32x4_t v = red[w][mt][16 * (m >> 1) + c];
-                s += m & 1 ? v[2] + v[3] : v[0] + v[1];
-            } else {
-                const f32x4_t v = red[w][mt][16 * m + c];
-                s += (v[0] + v[1]) + v[2];
-            }
-        }
+#pragma unroll
+        for (int w = 0; w < W; ++w) s += sums[w][t][c];
         if constexpr (BF16)
             static_cast<__bf16*>(a.out)[t * a.D + o0 + c] = (__bf16)s;
         else
@@ -544,13 +611,7 @@ hipError_t up_bits(const FewKernelArgs& x, hipStream_t s) {
 template <int DB, bool BF16>
 hipError_t run_down(const FewKernelArgs& x, hipStream_t s) {
     const unsigned grid = (unsigned)((x.a.D + 15) / 16);
-    const int mt = (x.a.T + (BF16 ? 7 : 3)) / (BF16 ? 8 : 4);
-    if (mt == 1)
-        moe_few_down_kernel<DB, 1, BF16><<<grid, 64 * kDownWaves, 0, s>>>(x);
-    else if (mt == 2)
-        moe_few_down_kernel<DB, 2, BF16><<<grid, 64 * kDownWaves, 0, s>>>(x);
-    else if constexpr (!BF16)
-        moe_few_down_kernel<DB, 4, BF16><<<grid, 64 * kDownWaves, 0, s>>>(x);
+    moe_few_down_kernel<DB, BF16><<<grid, 64 * kDownWaves, 0, s>>>(x);
     return hipGetLastError();
 }
 
@@ -565,10 +626,10 @@ hipError_t launch_moe_few(const FewArgs& a, void* workspace, hipStream_t s) {
     x.GF = (int)(p.fp / kGroup);
     x.pairs = (int)p.pairs;
     x.count = reinterpret_cast<int32_t*>(w);
-    x.weight = reinterpret_cast<float*>(w + p.weight);
-    x.prow = reinterpret_cast<int32_t*>(x.weight + p.pairs * a.T);
+    x.token = reinterpret_cast<int32_t*>(w + p.pair);
+    x.weight = reinterpret_cast<float*>(x.token + p.pairs);
     x.planes = reinterpret_cast<uint16_t*>(w + p.planes);
-    x.x_vec = a.D % 4 == 0 && (reinterpret_cast<uintptr_t>(a.X) & (a.bf16 ? 7 : 15)) == 0;
+    x.x_vec = a.D % 8 == 0 && (reinterpret_cast<uintptr_t>(a.X) & 15) == 0;
     const hipError_t e = a.bf16 ? up_bits<true>(x, s) : up_bits<false>(x, s);
     if (e != hipSuccess) return e;
     if (a.down.bits == 3) return a.bf16 ? run_down<3, true>(x, s) : run_down<3, false>(x, s);

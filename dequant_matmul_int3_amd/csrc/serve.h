@@ -20,6 +20,22 @@ constexpr int64_t kAttnMaxBatch = 65535;
 constexpr int64_t kAttnMaxGroupHeads = 256;  // query heads per key-value head
 constexpr int64_t kAttnMaxChunk = 2048;
 
+// x / d for x < 2^31 as a product: mul = ceil(2^(32 + sh) / d) with
+// 2^sh < d <= 2^(sh + 1), so that mul < 2^32 and the excess x / 2^(32 + sh) is
+// below 1 / d.
+struct FastDiv {
+    uint32_t d, mul, sh;
+    __host__ __device__ static FastDiv of(uint32_t d) {
+        FastDiv f{d, 0, 0};
+        while ((uint64_t(2) << f.sh) < d) ++f.sh;
+        if (d > 1) f.mul = (uint32_t)(((uint64_t(1) << (32 + f.sh)) + d - 1) / d);
+        return f;
+    }
+    __host__ __device__ uint32_t div(uint32_t x) const {
+        return d > 1 ? (uint32_t)(((uint64_t)x * mul) >> 32) >> sh : x;
+    }
+};
+
 // A paged cache: codes [pages][heads][page][groups * 8 bits] and scales
 // [pages][heads][page][groups] of the keys and of the values.
 struct KvCache {
@@ -114,13 +130,12 @@ struct FewArgs {
     void* out;  // [T x D]
 };
 
-// Workspace: the routing of the call (FewTables), then the activations of the
-// pairs as bf16 pieces [pieces][pairs][groups of F x 64].
+// Workspace: the routing of the call, then the activations of the pairs as bf16 pieces [pieces][pairs][groups of F x 64].
 constexpr int64_t few_align(int64_t b) { return (b + 15) / 16 * 16; }
 struct FewPlan {
     int64_t pairs, fp;        // pairs at most, F padded to whole groups
     int pieces;               // of an activation: two (bf16 calls) or three
-    int64_t weight, planes;   // offsets of the parts in bytes; the counts are first
+    int64_t pair, planes;     // offsets of the parts in bytes; the experts are first
     int64_t bytes;
 };
 inline FewPlan few_plan(int64_t T, int64_t k, int64_t F, bool bf16) {
@@ -128,10 +143,10 @@ inline FewPlan few_plan(int64_t T, int64_t k, int64_t F, bool bf16) {
     p.pairs = T * k;
     p.fp = (F + kGroup - 1) / kGroup * kGroup;
     p.pieces = bf16 ? 2 : 3;
-    // active experts: their number (16 bytes), then each one's expert and
-    // first pair; then for each the tokens' weights and pairs
-    p.weight = 16 + few_align(p.pairs * 8);
-    p.planes = p.weight + few_align(p.pairs * T * 8);
+    // the number of active experts (16 bytes) and each one's expert and first
+    // pair; then the pairs' tokens and weights
+    p.pair = 16 + few_align(p.pairs * 4);
+    p.planes = p.pair + few_align(p.pairs * 8);
     p.bytes = p.planes + p.pieces * p.pairs * p.fp * 2;
     return p;
 }
