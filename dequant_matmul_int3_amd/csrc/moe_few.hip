@@ -15,12 +15,46 @@ namespace qt {
 namespace {
 
 constexpr int kUpWaves = 4, kDownWaves = 8;
-// The first launch keeps its blocks for all tiles; four of them fit a CU.
-constexpr int kUpBlocks = 4 * 256;
-// Tokens of a pass at most, and the inputs staged at a time: 12 rows of at least 16 groups (a round of the
-// waves' chunks), rows 16 bytes apart in the banks.
+// Groups of a chunk, a wave's unit of work.
+constexpr int kUpCG = 4, kDownCG = 8;
+// Tokens of a pass at most, and the inputs staged at a time: 12 rows of at least
+// 16 groups (a round of the waves' chunks), rows 16 bytes apart in the banks.
 constexpr int kPassRows = 12;
-constexpr int kSlabBytes = kPassRows * (4 * kUpWaves * 128 + 16);
+constexpr int kRoundGroups = kUpWaves * kUpCG;
+constexpr int kSlabBytes = kPassRows * (kRoundGroups * 128 + 16);
+
+// Weights of 16 rows come in 16-byte pieces, consecutive lanes on consecutive
+// pieces of a row, and go through LDS of the wave's own: lane 16 h + r reads its
+// 16 codes of a group of row r from there (a lane loading its row's groups
+// itself touches a line of its own with every load, which the address path of
+// the caches takes one after the other).  Rows are 16 bytes apart in the banks:
+// conflict-free.
+template <int BITS, int CG>
+struct Tile {
+    static constexpr int kGB = BITS == 3 ? kGroupBytes : kGroupBytesI4;
+    static constexpr int kRow = CG * kGB;        // bytes of a row's chunk
+    static constexpr int kPitch = kRow + 16;
+    static constexpr int kParts = kRow / 16;     // pieces of a row
+    static constexpr int kPieces = 16 * kParts;  // of the tile
+    static_assert(kRow % 16 == 0, "whole pieces");
+    // the 16 codes of lane (row, h4) of group j
+    static __device__ __forceinline__ Quarter quarter(const uint8_t* tile, int j, int h4, int row) {
+        const uint8_t* p = tile + row * kPitch + j * kGB;
+        if constexpr (BITS == 3)
+            return Quarter{*reinterpret_cast<const uint32_t*>(p + 4 * h4),
+                           *reinterpret_cast<const uint32_t*>(p + 16 + 4 * (h4 >> 1))};
+        const u32x2_t w = *reinterpret_cast<const u32x2_t*>(p + 8 * h4);
+        return Quarter{w.x, w.y};
+    }
+};
+typedef u32x4_t u32x4_g __attribute__((aligned(8)));  // rows of an odd number of groups
+// 16 bytes of which the last 8 or all may lie past the row (zeros then)
+__device__ __forceinline__ u32x4_t piece(const uint8_t* p, int left) {
+    if (left >= 16) return *reinterpret_cast<const u32x4_g*>(p);
+    if (left < 8) return u32x4_t{0u, 0u, 0u, 0u};
+    const u32x2_t w = *reinterpret_cast<const u32x2_t*>(p);
+    return u32x4_t{w.x, w.y, 0u, 0u};
+}
 
 struct FewKernelArgs {
     FewArgs a;
@@ -31,6 +65,7 @@ struct FewKernelArgs {
     float* weight;       // [pairs] weight of a pair
     uint16_t* planes;    // [pieces][pairs][64 GF]
     bool x_vec;          // eight inputs may be loaded at once
+    int slab;            // bytes of the staged inputs
 };
 
 // A logit's bits made monotone as an unsigned number, above 0 (-0 as +0).
@@ -196,24 +231,34 @@ __device__ __forceinline__ f32x4_t mma(const u32x4_t& a, const u32x4_t& b, const
 }
 
 template <int GB, int UB, int M, bool BF16>
-__global__ __launch_bounds__(64 * kUpWaves) void moe_few_up_kernel(const FewKernelArgs x) {
+__global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(4))) void
+moe_few_up_kernel(const FewKernelArgs x) {
     constexpr int W = kUpWaves;
     constexpr int RT = BF16 ? kPassRows : 4;   // tokens a pass
-    constexpr int GBY = GB == 3 ? kGroupBytes : kGroupBytesI4;
-    constexpr int UBY = UB == 3 ? kGroupBytes : kGroupBytesI4;
     const FewArgs& a = x.a;
+    using TG = Tile<GB, kUpCG>;
+    using TU = Tile<UB, kUpCG>;
     __shared__ Route rt;
-    __shared__ __attribute__((aligned(16))) union {
-        Picks picks;
-        uint8_t stage[kSlabBytes];
-    } lds;
-    __shared__ __attribute__((aligned(16))) f32x4_t red[W][2][64];
-    route<M>(x, rt, lds.picks);
+    // a wave's chunk; at a tile's end its sums
+    struct Own {
+        union {
+            struct {
+                uint8_t g[16 * TG::kPitch], u[16 * TU::kPitch];
+            } w;
+            f32x4_t red[2][64];
+        };
+        float s[2][kUpCG][16];
+    };
+    __shared__ __attribute__((aligned(16))) Own own[W];
+    // the staged inputs; before them what only the routing needs
+    extern __shared__ __attribute__((aligned(16))) uint8_t slab[];
+    Picks& picks = *reinterpret_cast<Picks*>(slab);
+    route<M>(x, rt, picks);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int h4 = lane >> 4, l16 = lane & 15;
     const int G = x.GD, FT = x.GF * 4;
-    const int rounds = ((G + 3) / 4 + W - 1) / W;  // of the waves' chunks
+    const int rounds = (G + kRoundGroups - 1) / kRoundGroups;
     if (blockIdx.x == 0) {
         if (tid == 0) x.count[0] = rt.n;
         for (int i = tid; i < rt.n; i += 64 * W) x.count[4 + i] = (int)rt.act[i];
@@ -222,7 +267,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void moe_few_up_kernel(const FewKern
             const uint32_t m = rt.mask[e];
             if (!(m >> t & 1)) continue;
             float w = 0.0f;
-            for (int j = 0; j < a.k; ++j) w = lds.picks.sel[t][j] == e ? lds.picks.wgt[t][j] : w;
+            for (int j = 0; j < a.k; ++j) w = picks.sel[t][j] == e ? picks.wgt[t][j] : w;
             const int p = (int)(rt.act[n] >> 16) + __popc(m & ((1u << t) - 1));
             x.token[p] = t;
             x.weight[p] = w;
@@ -234,51 +279,76 @@ __global__ __launch_bounds__(64 * kUpWaves) void moe_few_up_kernel(const FewKern
     const int it1 = (int)((int64_t)items * (blockIdx.x + 1) / gridDim.x);
     if (it0 >= it1) return;
 
+    constexpr int NL = (TG::kPieces + TU::kPieces + 63) / 64;
     struct Chunk {
-        RowGroup<GB> g;
-        RowGroup<UB> u;
+        u32x4_t p[NL];
         float sg, su;
     };
-    // the chunk of this wave in round c of a tile (past the row a valid group,
-    // whose scale is 0)
+    // the chunk of this wave in round c of a tile (zeros past the row)
     auto load = [&](int it, int c, Chunk& k) __attribute__((always_inline)) {
         const int e = (int)(rt.act[it / FT] & 0xFFFFu), f0 = it % FT * 16;
-        const int64_t row = (int64_t)e * a.F + min<int64_t>(f0 + l16, a.F - 1);
-        const int q = 4 * (c * W + wave) + h4;
-        const int64_t at = row * G + min(q, G - 1);
-        k.g.load(a.gate.packed + at * GBY);
-        k.u.load(a.up.packed + at * UBY);
+        const int q0 = kUpCG * (c * W + wave);
+        const int64_t base = (int64_t)e * a.F + f0;
+        const int last = min(15, a.F - 1 - f0 > 15 ? 15 : (int)(a.F - 1 - f0));
+        const int rowmax = max(last, 0);
+        const int64_t base0 = f0 < a.F ? base : (int64_t)e * a.F;
+        auto get = [&](int i, int left_groups) __attribute__((always_inline)) {
+            const int id = lane + 64 * i;
+            const bool up = id >= TG::kPieces;
+            const int r = up ? id - TG::kPieces : id;
+            const int parts = up ? TU::kParts : TG::kParts, gb = up ? TU::kGB : TG::kGB;
+            const int row = min(up ? r / TU::kParts : r / TG::kParts, 15), part = r % parts;
+            const uint8_t* m = up ? a.up.packed : a.gate.packed;
+            const uint8_t* p = m + ((base0 + min(row, rowmax)) * G + q0) * gb + 16 * part;
+            return left_groups >= kUpCG ? *reinterpret_cast<const u32x4_g*>(p)
+                                        : piece(p, left_groups * gb - 16 * part);
+        };
+        if (q0 + kUpCG <= G) {
+#pragma unroll
+            for (int i = 0; i < NL; ++i) k.p[i] = get(i, kUpCG);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NL; ++i) k.p[i] = get(i, G - q0);
+        }
+        // scales: row lane / 4, group lane % 4
+        const int64_t at = (base0 + min(lane >> 2, rowmax)) * G + min(q0 + (lane & 3), G - 1);
+        const bool in = q0 + (lane & 3) < G;
         k.sg = a.gate.scales[at];
         k.su = a.up.scales[at];
+        if (!in) k.sg = k.su = 0.0f;
     };
     f32x4_t acc[2];
-    const uint8_t* arow = lds.stage;
+    const uint8_t* arow = slab;
     int regs = 1;  // registers of the results that hold rows
     auto mul = [&](int c, int s0, const Chunk& k) __attribute__((always_inline)) {
-        const int q0 = 4 * (c * W + wave);
-        Quarter qg[4], qu[4];
-        k.g.quarters(qg);
-        k.u.quarters(qu);
-        uint32_t sg[4], su[4];
-        const bool in = q0 + h4 < G;
+        const int q0 = kUpCG * (c * W + wave);
+        Own& o = own[wave];
+        lds_wave_sync();  // the chunk before is read
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            sg[j] = in ? __float_as_uint(k.sg * kUnit<GB>) : 0u;
-            su[j] = in ? __float_as_uint(k.su * kUnit<UB>) : 0u;
+        for (int i = 0; i < NL; ++i) {
+            const int id = lane + 64 * i;
+            if (id < TG::kPieces)
+                *reinterpret_cast<u32x4_t*>(o.w.g + id / TG::kParts * TG::kPitch +
+                                            id % TG::kParts * 16) = k.p[i];
+            else if (id < TG::kPieces + TU::kPieces)
+                *reinterpret_cast<u32x4_t*>(
+                    o.w.u + (id - TG::kPieces) / TU::kParts * TU::kPitch +
+                    (id - TG::kPieces) % TU::kParts * 16) = k.p[i];
         }
-        transpose_rows(sg);
-        transpose_rows(su);
+        o.s[0][lane & 3][lane >> 2] = k.sg * kUnit<GB>;
+        o.s[1][lane & 3][lane >> 2] = k.su * kUnit<UB>;
+        lds_wave_sync();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kUpCG; ++j) {
             const u32x4_t* xp = reinterpret_cast<const u32x4_t*>(arow + (q0 + j - s0) * 128);
             const u32x4_t x0 = xp[0], x1 = xp[1];
             u32x4_t wl[2], wh[2];
-            operands<GB>(qg[j], h4, wl[0], wh[0]);
-            operands<UB>(qu[j], h4, wl[1], wh[1]);
+            operands<GB>(TG::quarter(o.w.g, j, h4, l16), h4, wl[0], wh[0]);
+            operands<UB>(TU::quarter(o.w.u, j, h4, l16), h4, wl[1], wh[1]);
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
                 const f32x4_t p = mma(x1, wh[z], mma(x0, wl[z], f32x4_t{0.f, 0.f, 0.f, 0.f}));
-                const float s = __uint_as_float(z == 0 ? sg[j] : su[j]);
+                const float s = o.s[z][j][l16];
                 acc[z][0] = __builtin_fmaf(s, p[0], acc[z][0]);
                 if (regs > 1) {  // uniform
                     acc[z][1] = __builtin_fmaf(s, p[1], acc[z][1]);
@@ -315,14 +385,14 @@ __global__ __launch_bounds__(64 * kUpWaves) void moe_few_up_kernel(const FewKern
     // the rows of the pass's tokens for rounds c .. c + S - 1, zero past D
     auto stage = [&](int e, int who, int nt) __attribute__((always_inline)) {
         const int rows = BF16 ? nt : 3 * nt;
-        S = min((kSlabBytes / rows - 16) / (512 * W), rounds);
-        const int pitch = S * (512 * W) + 16;
+        S = min((x.slab / rows - 16) / (kRoundGroups * 128), rounds);
+        const int pitch = S * (kRoundGroups * 128) + 16;
         // bf16: token m is row 4 (m % 4) + m / 4, so that up to four tokens take one
         // register of the results; f32: row 4 m + piece
         const int lrow = BF16 ? min(4 * (l16 & 3) + (l16 >> 2), nt - 1)
                               : min(l16 >> 2, nt - 1) * 3 + min(l16 & 3, 2);
         regs = BF16 ? (nt + 3) / 4 : 3;
-        arow = lds.stage + lrow * pitch + 32 * h4;
+        arow = slab + lrow * pitch + 32 * h4;
         have_e = e;
         have_p = now.p0;
         have_c = now.c;
@@ -367,7 +437,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void moe_few_up_kernel(const FewKern
                 }
 #pragma unroll
                 for (int pc = 0; pc < (BF16 ? 1 : 3); ++pc)
-                    *reinterpret_cast<u32x4_t*>(lds.stage + (BF16 ? m : 3 * m + pc) * pitch +
+                    *reinterpret_cast<u32x4_t*>(slab + (BF16 ? m : 3 * m + pc) * pitch +
                                                 16 * v) =
                         u32x4_t{b[pc][0] | b[pc][1] << 16, b[pc][2] | b[pc][3] << 16,
                                 b[pc][4] | b[pc][5] << 16, b[pc][6] | b[pc][7] << 16};
@@ -377,9 +447,9 @@ __global__ __launch_bounds__(64 * kUpWaves) void moe_few_up_kernel(const FewKern
     };
     // the pass's sums of all waves, and its activations
     auto finish = [&](int first, int nt, int f0) __attribute__((always_inline)) {
-        lds_barrier();  // the sums of the pass before are read
-        red[wave][0][lane] = acc[0];
-        red[wave][1][lane] = acc[1];
+        lds_wave_sync();  // the chunk is read
+        own[wave].red[0][lane] = acc[0];
+        own[wave].red[1][lane] = acc[1];
         lds_barrier();
         for (int z = tid; z < nt * 16; z += 64 * W) {
             const int m = z >> 4, c = z & 15;
@@ -389,9 +459,9 @@ __global__ __launch_bounds__(64 * kUpWaves) void moe_few_up_kernel(const FewKern
 #pragma unroll
                 for (int w = 0; w < W; ++w) {
                     if constexpr (BF16) {
-                        s[y] += red[w][y][16 * (m & 3) + c][m >> 2];
+                        s[y] += own[w].red[y][16 * (m & 3) + c][m >> 2];
                     } else {
-                        const f32x4_t v = red[w][y][16 * m + c];
+                        const f32x4_t v = own[w].red[y][16 * m + c];
                         s[y] += (v[0] + v[1]) + v[2];
                     }
                 }
@@ -412,6 +482,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void moe_few_up_kernel(const FewKern
                 x.planes[2 * plane + at] = (uint16_t)b2;
             }
         }
+        lds_barrier();  // the sums are read
     };
     // one step from the chunk in k; false after the last one
     auto turn = [&](const Chunk& k) __attribute__((always_inline)) {
@@ -446,103 +517,155 @@ __global__ __launch_bounds__(64 * kUpWaves) void moe_few_up_kernel(const FewKern
 // are added at the end in wave order.  Rows of the matrix operand are the
 // pieces of an expert's tokens.
 //
-// Weights are loaded three chunks ahead and activations one; a chunk's expert
-// and pairs, the addresses of both, come from LDS.
-template <int DB, bool BF16>
+// Weights are loaded two chunks ahead and activations one; a chunk's expert and
+// pairs, the addresses of both, come from LDS.
+//
+// ROWS: operand rows of an expert that are staged in LDS; an expert with more
+// tokens reads them from the caches.
+template <int DB, bool BF16, int ROWS>
 __global__ __launch_bounds__(64 * kDownWaves) __attribute__((amdgpu_waves_per_eu(4))) void
 moe_few_down_kernel(const FewKernelArgs x) {
-    constexpr int W = kDownWaves;
+    constexpr int W = kDownWaves, CG = kDownCG;
+    constexpr int NP = BF16 ? 2 : 3;   // pieces of an activation
     constexpr int PT = BF16 ? 2 : 4;   // rows of a token: its pieces (and one unused)
     constexpr int RT = 16 / PT;        // tokens of a row tile
     constexpr int NW = 4 / PT;         // tokens of a lane's four result rows
-    constexpr int BY = DB == 3 ? kGroupBytes : kGroupBytesI4;
+    constexpr int kRowPitch = CG * 128 + 16;
+    using TD = Tile<DB, CG>;
+    constexpr int NL = TD::kPieces / 64;
+    static_assert(TD::kPieces % 64 == 0, "whole loads");
     const FewArgs& a = x.a;
     constexpr int kPairs = kFewMaxTokens * kFewMaxTopK;
+    struct Own {
+        uint8_t w[16 * TD::kPitch];
+        uint8_t h[ROWS * kRowPitch];
+        float s[CG][16];
+    };
+    __shared__ __attribute__((aligned(16))) Own own[W];
     __shared__ uint32_t act[kPairs + 1];
-    __shared__ int32_t token[kPairs];
+    __shared__ uint8_t token[kPairs];
     __shared__ float weight[kPairs];
     __shared__ float sums[W][kFewMaxTokens][16];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int h4 = lane >> 4, l16 = lane & 15;
-    const int G = x.GF, nchunk = (G + 3) / 4;
+    const int G = x.GF, nchunk = (G + CG - 1) / CG;
     const int64_t o0 = (int64_t)blockIdx.x * 16;
     const int n = x.count[0], units = n * nchunk;
     for (int i = tid; i < x.pairs; i += 64 * W) {
         act[i] = (uint32_t)x.count[4 + i];
-        token[i] = x.token[i];
+        token[i] = (uint8_t)x.token[i];
         weight[i] = x.weight[i];
     }
     for (int i = lane; i < a.T * 16; i += 64) sums[wave][i >> 4][i & 15] = 0.0f;
     __syncthreads();
     if (tid == 0) act[n] = (uint32_t)x.pairs << 16;
     __syncthreads();
-    const int64_t orow = min<int64_t>(o0 + l16, a.D - 1);
-    const int piece = BF16 ? l16 & 1 : min(l16 & 3, 2);
-    const uint16_t* plane = x.planes + piece * ((int64_t)x.pairs * G * 64) + 16 * h4;
+    const int rowmax = (int)min<int64_t>(15, a.D - 1 - o0);
+    const int64_t plane = (int64_t)x.pairs * G * 64;
+    Own& o = own[wave];
 
+    // a wave's units in turn: expert i and chunk c, kept as it goes
+    struct At {
+        int i, c;
+    };
+    auto advance = [&](At t) __attribute__((always_inline)) {
+        t.c += W;
+        while (t.c >= nchunk) {
+            t.c -= nchunk;
+            ++t.i;
+        }
+        if (t.i >= n) t = At{n - 1, nchunk - 1};  // past the last unit: it repeats
+        return t;
+    };
     struct Weights {
-        RowGroup<DB> w;
-        float s;
+        u32x4_t p[NL];
+        float s[2];
     };
-    auto expert_of = [&](int u) __attribute__((always_inline)) { return min(u, units - 1) / nchunk; };
-    auto load = [&](int u, Weights& w) __attribute__((always_inline)) {
-        const int i = expert_of(u);
-        const int q = min(4 * (min(u, units - 1) - i * nchunk) + h4, G - 1);
-        const int64_t r = ((int64_t)(act[i] & 0xFFFFu) * a.D + orow) * G + q;
-        w.w.load(a.down.packed + r * BY);
-        w.s = a.down.scales[r];
+    auto load = [&](const At& t, Weights& w) __attribute__((always_inline)) {
+        const int q0 = t.c * CG;
+        const int64_t base = (int64_t)(act[t.i] & 0xFFFFu) * a.D + o0;
+        const int left = G - q0;
+        auto get = [&](int i) __attribute__((always_inline)) {
+            const int id = lane + 64 * i, row = min(id / TD::kParts, rowmax), part = id % TD::kParts;
+            return a.down.packed + ((base + row) * G + q0) * TD::kGB + 16 * part;
+        };
+        if (left >= CG) {
+#pragma unroll
+            for (int i = 0; i < NL; ++i) w.p[i] = *reinterpret_cast<const u32x4_g*>(get(i));
+        } else {
+#pragma unroll
+            for (int i = 0; i < NL; ++i)
+                w.p[i] = piece(get(i), left * TD::kGB - 16 * ((lane + 64 * i) % TD::kParts));
+        }
+        // scales: row lane / 4, groups lane % 4 and lane % 4 + 4
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            const int q = (lane & 3) + 4 * z;
+            const float s = a.down.scales[(base + min(lane >> 2, rowmax)) * G + q0 + min(q, left - 1)];
+            w.s[z] = q < left ? s : 0.0f;
+        }
     };
-    // this lane's operand row of unit u's first group, tokens from p0 on
-    auto row_of = [&](int u, int p0) __attribute__((always_inline)) {
-        const int i = expert_of(u), first = (int)(act[i] >> 16), end = (int)(act[i + 1] >> 16);
-        const int p = min(first + p0 + l16 / PT, end - 1);
-        return plane + ((int64_t)p * G + 4 * (min(u, units - 1) - i * nchunk)) * 64;
+    // operand row r of tokens from p0 on: pieces of token after token
+    auto row_of = [&](const At& t, int p0, int r) __attribute__((always_inline)) {
+        const int first = (int)(act[t.i] >> 16), end = (int)(act[t.i + 1] >> 16);
+        return x.planes + r % NP * plane +
+               ((int64_t)min(first + p0 + r / NP, end - 1) * G + t.c * CG) * 64;
     };
-    // group j of it (past the row the last one, scale 0)
-    auto operand = [&](const uint16_t* row, int left, int j, u32x4_t (&v)[2])
-                       __attribute__((always_inline)) {
-        const u32x4_t* p = reinterpret_cast<const u32x4_t*>(row + min(j, left) * 64);
-        v[0] = p[0];
-        v[1] = p[1];
-    };
-    auto left_of = [&](int u) __attribute__((always_inline)) {
-        return G - 1 - 4 * (min(u, units - 1) - expert_of(u) * nchunk);
+    auto load_h = [&](const At& t, u32x4_t (&h)[ROWS]) __attribute__((always_inline)) {
+        // a lane's 16 bytes of each row (past the row its last group's)
+        const int at = min(lane, 8 * (G - t.c * CG) - 1) * 8;
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r)
+            h[r] = *reinterpret_cast<const u32x4_t*>(row_of(t, 0, r) + at);
     };
     if (wave < units) {
-        Weights w[4];
-        u32x4_t v[4][2];
-#pragma unroll
-        for (int i = 0; i < 3; ++i) load(wave + i * W, w[i]);
-        {
-            const uint16_t* row = row_of(wave, 0);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) operand(row, left_of(wave), j, v[j]);
+        Weights w[3];
+        u32x4_t h[ROWS];
+        At now{0, wave};
+        while (now.c >= nchunk) {
+            now.c -= nchunk;
+            ++now.i;
         }
-        auto turn = [&](int u, const Weights& w0, Weights& w3) __attribute__((always_inline)) {
-            load(u + 3 * W, w3);
-            const int i = u / nchunk, first = (int)(act[i] >> 16), end = (int)(act[i + 1] >> 16);
-            const uint16_t* ahead = row_of(u + W, 0);
-            const int left = left_of(u + W);
-            Quarter qd[4];
-            w0.w.quarters(qd);
-            uint32_t sd[4];
+        At next = advance(now), then;
+        load(now, w[0]);
+        load(next, w[1]);
+        load_h(now, h);
+        auto turn = [&](int u, const Weights& w0, Weights& w2) __attribute__((always_inline)) {
+            then = advance(next);
+            load(then, w2);
+            const int first = (int)(act[now.i] >> 16), end = (int)(act[now.i + 1] >> 16);
+            lds_wave_sync();  // the chunk before is read
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                sd[j] = 4 * (u - i * nchunk) + h4 < G ? __float_as_uint(w0.s * kUnit<DB>) : 0u;
-            transpose_rows(sd);
-            auto product = [&](bool last) __attribute__((always_inline)) {
+            for (int i = 0; i < NL; ++i) {
+                const int id = lane + 64 * i;
+                *reinterpret_cast<u32x4_t*>(o.w + id / TD::kParts * TD::kPitch +
+                                            id % TD::kParts * 16) = w0.p[i];
+            }
+            o.s[lane & 3][lane >> 2] = w0.s[0] * kUnit<DB>;
+            o.s[(lane & 3) + 4][lane >> 2] = w0.s[1] * kUnit<DB>;
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r)
+                *reinterpret_cast<u32x4_t*>(o.h + r * kRowPitch + 16 * lane) = h[r];
+            load_h(next, h);
+            lds_wave_sync();
+            // this lane's operand row: piece of a token, a valid one past them
+            const int tok = l16 / PT, pc = min(l16 % PT, NP - 1);
+            auto product = [&](const uint8_t* hp, int pitch) __attribute__((always_inline)) {
                 f32x4_t part = {0.f, 0.f, 0.f, 0.f};
+                const int live = min(CG, G - now.c * CG);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < CG; ++j) {
+                    // (past the row the scale is 0 and any group will do)
+                    const u32x4_t* p =
+                        reinterpret_cast<const u32x4_t*>(hp + min(j, live - 1) * 128 + 32 * h4);
                     u32x4_t wl, wh;
-                    operands<DB>(qd[j], h4, wl, wh);
-                    const float s = __uint_as_float(sd[j]);
-                    const f32x4_t p =
-                        mma(v[j][1], wh, mma(v[j][0], wl, f32x4_t{0.f, 0.f, 0.f, 0.f}));
+                    operands<DB>(TD::quarter(o.w, j, h4, l16), h4, wl, wh);
+                    const float s = o.s[j][l16];
+                    const f32x4_t y = mma(p[1], wh, mma(p[0], wl, f32x4_t{0.f, 0.f, 0.f, 0.f}));
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) part[r] = __builtin_fmaf(s, p[r], part[r]);
-                    if (last) operand(ahead, left, j, v[j]);
+                    for (int r = 0; r < (BF16 ? 4 : 3); ++r)
+                        part[r] = __builtin_fmaf(s, y[r], part[r]);
                 }
                 return part;
             };
@@ -560,21 +683,23 @@ moe_few_down_kernel(const FewKernelArgs x) {
                     }
                 }
             };
-            // more tokens than a row tile: their rows are loaded as they come
-            for (int p0 = 0; p0 + RT < end - first; p0 += RT) {
-                add(p0, product(false));
-                const uint16_t* row = row_of(u, p0 + RT);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) operand(row, left_of(u), j, v[j]);
+            if ((end - first) * NP <= ROWS) {
+                const int r = min(tok, end - first - 1) * NP + pc;
+                add(0, product(o.h + r * kRowPitch, kRowPitch));
+            } else {
+                for (int p0 = 0; p0 < end - first; p0 += RT)
+                    add(p0, product(reinterpret_cast<const uint8_t*>(
+                                        row_of(now, p0, min(tok, end - first - 1 - p0) * NP + pc)),
+                                    0));
             }
-            add((end - first - 1) / RT * RT, product(true));
+            now = next;
+            next = then;
             return u + W < units;
         };
-        for (int u = wave;; u += 4 * W) {
-            if (!turn(u, w[0], w[3])) break;
+        for (int u = wave;; u += 3 * W) {
+            if (!turn(u, w[0], w[2])) break;
             if (!turn(u + W, w[1], w[0])) break;
             if (!turn(u + 2 * W, w[2], w[1])) break;
-            if (!turn(u + 3 * W, w[3], w[2])) break;
         }
     }
     __syncthreads();
@@ -591,15 +716,23 @@ moe_few_down_kernel(const FewKernelArgs x) {
     }
 }
 
+template <int GB, int UB, int M, bool BF16>
+hipError_t start_up(const FewKernelArgs& x, int64_t items, hipStream_t s) {
+    // all blocks resident: as many as the LDS of a CU takes, four at most (their
+    // registers)
+    const int64_t fixed = sizeof(Route) + kUpWaves * (16 * (Tile<GB, kUpCG>::kPitch +
+                                                            Tile<UB, kUpCG>::kPitch) +
+                                                      2 * kUpCG * 16 * 4);
+    const int64_t per_cu = std::min<int64_t>(4, 160 * 1024 / (fixed + x.slab + 512));
+    const unsigned grid = (unsigned)std::min<int64_t>(items, 256 * per_cu);
+    moe_few_up_kernel<GB, UB, M, BF16><<<grid, 64 * kUpWaves, x.slab, s>>>(x);
+    return hipGetLastError();
+}
 template <int GB, int UB, bool BF16>
 hipError_t run_up(const FewKernelArgs& x, hipStream_t s) {
     const int64_t items = std::min<int64_t>(x.pairs, x.a.E) * x.GF * 4;
-    const unsigned grid = (unsigned)std::min<int64_t>(items, kUpBlocks);
-    if (x.a.E <= 128)
-        moe_few_up_kernel<GB, UB, 2, BF16><<<grid, 64 * kUpWaves, 0, s>>>(x);
-    else
-        moe_few_up_kernel<GB, UB, 8, BF16><<<grid, 64 * kUpWaves, 0, s>>>(x);
-    return hipGetLastError();
+    return x.a.E <= 128 ? start_up<GB, UB, 2, BF16>(x, items, s)
+                        : start_up<GB, UB, 8, BF16>(x, items, s);
 }
 template <bool BF16>
 hipError_t up_bits(const FewKernelArgs& x, hipStream_t s) {
@@ -611,7 +744,12 @@ hipError_t up_bits(const FewKernelArgs& x, hipStream_t s) {
 template <int DB, bool BF16>
 hipError_t run_down(const FewKernelArgs& x, hipStream_t s) {
     const unsigned grid = (unsigned)((x.a.D + 15) / 16);
-    moe_few_down_kernel<DB, BF16><<<grid, 64 * kDownWaves, 0, s>>>(x);
+    // one token's rows, or as many as leave two blocks a CU
+    constexpr int kOne = BF16 ? 2 : 3, kMore = DB == 3 ? (BF16 ? 4 : 3) : kOne;
+    if (x.a.T == 1)
+        moe_few_down_kernel<DB, BF16, kOne><<<grid, 64 * kDownWaves, 0, s>>>(x);
+    else
+        moe_few_down_kernel<DB, BF16, kMore><<<grid, 64 * kDownWaves, 0, s>>>(x);
     return hipGetLastError();
 }
 
@@ -630,6 +768,11 @@ hipError_t launch_moe_few(const FewArgs& a, void* workspace, hipStream_t s) {
     x.weight = reinterpret_cast<float*>(x.token + p.pairs);
     x.planes = reinterpret_cast<uint16_t*>(w + p.planes);
     x.x_vec = a.D % 8 == 0 && (reinterpret_cast<uintptr_t>(a.X) & 15) == 0;
+    // the tokens' rows whole, where they fit; the routing's picks lie there first
+    const int64_t rounds = (x.GD + kRoundGroups - 1) / kRoundGroups;
+    const int64_t rows = a.bf16 ? std::min(a.T, kPassRows) : 3 * std::min(a.T, 4);
+    x.slab = (int)std::max<int64_t>(
+        sizeof(Picks), std::min<int64_t>(kSlabBytes, rows * (rounds * kRoundGroups * 128 + 16)));
     const hipError_t e = a.bf16 ? up_bits<true>(x, s) : up_bits<false>(x, s);
     if (e != hipSuccess) return e;
     if (a.down.bits == 3) return a.bf16 ? run_down<3, true>(x, s) : run_down<3, false>(x, s);
