@@ -243,7 +243,7 @@ moe_few_up_kernel(const FewKernelArgs x) {
     struct Own {
         union {
             struct {
-                uint8_t g[16 * TG::kPitch], u[16 * TU::kPitch];
+                uint8_t g[16 * TG::kPitch], u[16 * TU::kPitch];  // u right after g
             } w;
             f32x4_t red[2][64];
         };
@@ -284,35 +284,57 @@ moe_few_up_kernel(const FewKernelArgs x) {
         u32x4_t p[NL];
         float sg, su;
     };
-    // the chunk of this wave in round c of a tile (zeros past the row)
+    // The chunk of this wave in round c of a tile (zeros past the row): the tile's
+    // and chunk's place is the wave's, a lane's own place in it stays.
+    int off[NL], own_at[NL];  // of a lane's pieces, in the weights and in LDS
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+        const int id = lane + 64 * i;
+        own_at[i] = id < TG::kPieces
+                        ? id / TG::kParts * TG::kPitch + id % TG::kParts * 16
+                        : 16 * TG::kPitch + (id - TG::kPieces) / TU::kParts * TU::kPitch +
+                              (id - TG::kPieces) % TU::kParts * 16;
+        off[i] = id < TG::kPieces
+                     ? id / TG::kParts * G * TG::kGB + id % TG::kParts * 16
+                     : min((id - TG::kPieces) / TU::kParts, 15) * G * TU::kGB +
+                           (id - TG::kPieces) % TU::kParts * 16;
+    }
+    const int soff = (lane >> 2) * G + (lane & 3);  // row lane / 4, group lane % 4
     auto load = [&](int it, int c, Chunk& k) __attribute__((always_inline)) {
-        const int e = (int)(rt.act[it / FT] & 0xFFFFu), f0 = it % FT * 16;
-        const int q0 = kUpCG * (c * W + wave);
-        const int64_t base = (int64_t)e * a.F + f0;
-        const int last = min(15, a.F - 1 - f0 > 15 ? 15 : (int)(a.F - 1 - f0));
-        const int rowmax = max(last, 0);
-        const int64_t base0 = f0 < a.F ? base : (int64_t)e * a.F;
-        auto get = [&](int i, int left_groups) __attribute__((always_inline)) {
-            const int id = lane + 64 * i;
+        const int e = __builtin_amdgcn_readfirstlane((int)(rt.act[it / FT] & 0xFFFFu));
+        const int f0 = it % FT * 16, q0 = kUpCG * (c * W + wave);
+        if (q0 + kUpCG <= G && f0 + 16 <= a.F) {
+            const int64_t at = ((int64_t)e * a.F + f0) * G + q0;
+            const uint8_t *g = a.gate.packed + at * TG::kGB, *u = a.up.packed + at * TU::kGB;
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                const uint8_t* p = 64 * i + 63 < TG::kPieces ? g
+                                   : 64 * i >= TG::kPieces   ? u
+                                   : lane + 64 * i < TG::kPieces ? g : u;
+                k.p[i] = *reinterpret_cast<const u32x4_g*>(p + (uint32_t)off[i]);
+            }
+            k.sg = (a.gate.scales + at)[(uint32_t)soff];
+            k.su = (a.up.scales + at)[(uint32_t)soff];
+            return;
+        }
+        // at an edge: rows past F are the last one, groups past the row zeros (a
+        // chunk past it loads its last group's scales)
+        const int rowmax = max(min(15, (int)(a.F - 1 - f0)), 0);
+        const int64_t base = (int64_t)e * a.F + (f0 < a.F ? f0 : 0);
+        int here = lane;
+        asm volatile("" : "+v"(here));  // this path's places are worked out in it, not kept
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const int id = here + 64 * i;
             const bool up = id >= TG::kPieces;
             const int r = up ? id - TG::kPieces : id;
             const int parts = up ? TU::kParts : TG::kParts, gb = up ? TU::kGB : TG::kGB;
-            const int row = min(up ? r / TU::kParts : r / TG::kParts, 15), part = r % parts;
+            const int row = min(r / parts, rowmax), part = r % parts;
             const uint8_t* m = up ? a.up.packed : a.gate.packed;
-            const uint8_t* p = m + ((base0 + min(row, rowmax)) * G + q0) * gb + 16 * part;
-            return left_groups >= kUpCG ? *reinterpret_cast<const u32x4_g*>(p)
-                                        : piece(p, left_groups * gb - 16 * part);
-        };
-        if (q0 + kUpCG <= G) {
-#pragma unroll
-            for (int i = 0; i < NL; ++i) k.p[i] = get(i, kUpCG);
-        } else {
-#pragma unroll
-            for (int i = 0; i < NL; ++i) k.p[i] = get(i, G - q0);
+            k.p[i] = piece(m + ((base + row) * G + q0) * gb + 16 * part, (G - q0) * gb - 16 * part);
         }
-        // scales: row lane / 4, group lane % 4
-        const int64_t at = (base0 + min(lane >> 2, rowmax)) * G + min(q0 + (lane & 3), G - 1);
-        const bool in = q0 + (lane & 3) < G;
+        const int64_t at = (base + min(here >> 2, rowmax)) * G + min(q0 + (here & 3), G - 1);
+        const bool in = q0 + (here & 3) < G;
         k.sg = a.gate.scales[at];
         k.su = a.up.scales[at];
         if (!in) k.sg = k.su = 0.0f;
@@ -325,16 +347,9 @@ moe_few_up_kernel(const FewKernelArgs x) {
         Own& o = own[wave];
         lds_wave_sync();  // the chunk before is read
 #pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            const int id = lane + 64 * i;
-            if (id < TG::kPieces)
-                *reinterpret_cast<u32x4_t*>(o.w.g + id / TG::kParts * TG::kPitch +
-                                            id % TG::kParts * 16) = k.p[i];
-            else if (id < TG::kPieces + TU::kPieces)
-                *reinterpret_cast<u32x4_t*>(
-                    o.w.u + (id - TG::kPieces) / TU::kParts * TU::kPitch +
-                    (id - TG::kPieces) % TU::kParts * 16) = k.p[i];
-        }
+        for (int i = 0; i < NL; ++i)
+            if (64 * i + 63 < TG::kPieces + TU::kPieces || lane + 64 * i < TG::kPieces + TU::kPieces)
+                *reinterpret_cast<u32x4_t*>(reinterpret_cast<uint8_t*>(&o.w) + own_at[i]) = k.p[i];
         o.s[0][lane & 3][lane >> 2] = k.sg * kUnit<GB>;
         o.s[1][lane & 3][lane >> 2] = k.su * kUnit<UB>;
         lds_wave_sync();
@@ -582,27 +597,39 @@ moe_few_down_kernel(const FewKernelArgs x) {
         u32x4_t p[NL];
         float s[2];
     };
+    // a lane's place in a chunk stays, the chunk's is the wave's
+    int off[NL];
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+        const int id = lane + 64 * i;
+        off[i] = min(id / TD::kParts, rowmax) * G * TD::kGB + id % TD::kParts * 16;
+    }
+    // scales: row lane / 4, groups lane % 4 and lane % 4 + 4
+    const int soff = min(lane >> 2, rowmax) * G;
     auto load = [&](const At& t, Weights& w) __attribute__((always_inline)) {
-        const int q0 = t.c * CG;
-        const int64_t base = (int64_t)(act[t.i] & 0xFFFFu) * a.D + o0;
-        const int left = G - q0;
-        auto get = [&](int i) __attribute__((always_inline)) {
-            const int id = lane + 64 * i, row = min(id / TD::kParts, rowmax), part = id % TD::kParts;
-            return a.down.packed + ((base + row) * G + q0) * TD::kGB + 16 * part;
-        };
+        const int q0 = t.c * CG, left = G - q0;
+        const int e = __builtin_amdgcn_readfirstlane((int)(act[t.i] & 0xFFFFu));
+        const int64_t at = ((int64_t)e * a.D + o0) * G + q0;
+        const uint8_t* p = a.down.packed + at * TD::kGB;
+        const float* sc = a.down.scales + at;
         if (left >= CG) {
 #pragma unroll
-            for (int i = 0; i < NL; ++i) w.p[i] = *reinterpret_cast<const u32x4_g*>(get(i));
-        } else {
-#pragma unroll
             for (int i = 0; i < NL; ++i)
-                w.p[i] = piece(get(i), left * TD::kGB - 16 * ((lane + 64 * i) % TD::kParts));
+                w.p[i] = *reinterpret_cast<const u32x4_g*>(p + (uint32_t)off[i]);
+#pragma unroll
+            for (int z = 0; z < 2; ++z) w.s[z] = (sc + 4 * z)[(uint32_t)(soff + (lane & 3))];
+            return;
         }
-        // scales: row lane / 4, groups lane % 4 and lane % 4 + 4
+        int here = lane;
+        asm volatile("" : "+v"(here));  // this path's places are worked out in it, not kept
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+            w.p[i] = piece(p + (uint32_t)off[i],
+                           left * TD::kGB - 16 * ((here + 64 * i) % TD::kParts));
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
-            const int q = (lane & 3) + 4 * z;
-            const float s = a.down.scales[(base + min(lane >> 2, rowmax)) * G + q0 + min(q, left - 1)];
+            const int q = (here & 3) + 4 * z;
+            const float s = sc[(uint32_t)(soff + min(q, left - 1))];
             w.s[z] = q < left ? s : 0.0f;
         }
     };
