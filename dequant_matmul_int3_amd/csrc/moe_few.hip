@@ -17,11 +17,18 @@ namespace {
 constexpr int kUpWaves = 4, kDownWaves = 8;
 // Groups of a chunk, a wave's unit of work.
 constexpr int kUpCG = 4, kDownCG = 8;
-// Tokens of a pass at most, and the inputs staged at a time: 12 rows of at least
-// 16 groups (a round of the waves' chunks), rows 16 bytes apart in the banks.
-constexpr int kPassRows = 12;
 constexpr int kRoundGroups = kUpWaves * kUpCG;
-constexpr int kSlabBytes = kPassRows * (kRoundGroups * 128 + 16);
+// Tokens of a pass at most, and the inputs staged at a time: their rows (an f32
+// token has three) of at least 16 groups (a round of the waves' chunks), rows 16
+// bytes apart in the banks.  With eight rows four blocks fit a CU, which pays more
+// than the second pass (from the caches) of an expert with more tokens costs: twelve
+// tokens' 68 experts of 7168 x 2048 took 310 us with twelve rows, 296 with eight.
+template <bool BF16>
+constexpr int kPassTokens = BF16 ? 8 : 4;
+template <bool BF16>
+constexpr int kPassRows = BF16 ? kPassTokens<true> : 3 * kPassTokens<false>;
+template <bool BF16>
+constexpr int kSlabBytes = kPassRows<BF16> * (kRoundGroups * 128 + 16);
 
 // Weights of 16 rows come in 16-byte pieces, consecutive lanes on consecutive
 // pieces of a row, and go through LDS of the wave's own: lane 16 h + r reads its
@@ -222,6 +229,8 @@ __device__ __forceinline__ void operands(const Quarter& q, int h4, u32x4_t& lo8,
         hi8 = word(q.b);
     }
 }
+// Blocks (of a wave a SIMD) on a CU: widths that differ take more registers.
+constexpr int up_blocks(int gb, int ub) { return gb == ub ? 4 : 3; }
 template <int BITS>
 constexpr float kUnit = BITS == 3 ? 1.0f : 0.0625f;
 
@@ -231,10 +240,10 @@ __device__ __forceinline__ f32x4_t mma(const u32x4_t& a, const u32x4_t& b, const
 }
 
 template <int GB, int UB, int M, bool BF16>
-__global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(4))) void
+__global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(up_blocks(GB, UB)))) void
 moe_few_up_kernel(const FewKernelArgs x) {
     constexpr int W = kUpWaves;
-    constexpr int RT = BF16 ? kPassRows : 4;   // tokens a pass
+    constexpr int RT = kPassTokens<BF16>;      // tokens a pass
     const FewArgs& a = x.a;
     using TG = Tile<GB, kUpCG>;
     using TU = Tile<UB, kUpCG>;
@@ -366,8 +375,9 @@ moe_few_up_kernel(const FewKernelArgs x) {
                 const float s = o.s[z][j][l16];
                 acc[z][0] = __builtin_fmaf(s, p[0], acc[z][0]);
                 if (regs > 1) {  // uniform
-                    acc[z][1] = __builtin_fmaf(s, p[1], acc[z][1]);
-                    acc[z][2] = __builtin_fmaf(s, p[2], acc[z][2]);
+#pragma unroll
+                    for (int r = 1; r < (BF16 ? RT / 4 : 3); ++r)
+                        acc[z][r] = __builtin_fmaf(s, p[r], acc[z][r]);
                 }
             }
         }
@@ -750,7 +760,7 @@ hipError_t start_up(const FewKernelArgs& x, int64_t items, hipStream_t s) {
     const int64_t fixed = sizeof(Route) + kUpWaves * (16 * (Tile<GB, kUpCG>::kPitch +
                                                             Tile<UB, kUpCG>::kPitch) +
                                                       2 * kUpCG * 16 * 4);
-    const int64_t per_cu = std::min<int64_t>(4, 160 * 1024 / (fixed + x.slab + 512));
+    const int64_t per_cu = std::min<int64_t>(up_blocks(GB, UB), 160 * 1024 / (fixed + x.slab + 512));
     const unsigned grid = (unsigned)std::min<int64_t>(items, 256 * per_cu);
     moe_few_up_kernel<GB, UB, M, BF16><<<grid, 64 * kUpWaves, x.slab, s>>>(x);
     return hipGetLastError();
@@ -797,9 +807,10 @@ hipError_t launch_moe_few(const FewArgs& a, void* workspace, hipStream_t s) {
     x.x_vec = a.D % 8 == 0 && (reinterpret_cast<uintptr_t>(a.X) & 15) == 0;
     // the tokens' rows whole, where they fit; the routing's picks lie there first
     const int64_t rounds = (x.GD + kRoundGroups - 1) / kRoundGroups;
-    const int64_t rows = a.bf16 ? std::min(a.T, kPassRows) : 3 * std::min(a.T, 4);
+    const int64_t rows = a.bf16 ? std::min(a.T, kPassTokens<true>) : 3 * std::min(a.T, kPassTokens<false>);
     x.slab = (int)std::max<int64_t>(
-        sizeof(Picks), std::min<int64_t>(kSlabBytes, rows * (rounds * kRoundGroups * 128 + 16)));
+        sizeof(Picks), std::min<int64_t>(a.bf16 ? kSlabBytes<true> : kSlabBytes<false>,
+                                         rows * (rounds * kRoundGroups * 128 + 16)));
     const hipError_t e = a.bf16 ? up_bits<true>(x, s) : up_bits<false>(x, s);
     if (e != hipSuccess) return e;
     if (a.down.bits == 3) return a.bf16 ? run_down<3, true>(x, s) : run_down<3, false>(x, s);
