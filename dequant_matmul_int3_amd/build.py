@@ -23,7 +23,7 @@ ARCH = "gfx950"
 SOURCES = ["api.cpp", "quantize.hip", "gemv.hip", "grouped.hip", "gemm.hip", "hessian.hip",
            "syrk.hip", "factor.hip", "gptq.hip", "moe.hip",
            "api_tune.cpp", "ffn.hip", "qgrad.hip", "distill.hip",
-           "api_serve.cpp", "kvcache.hip", "attn.hip", "attn_f32.hip",
+           "api_serve.cpp", "kvcache.hip", "attn.hip", "attn_f32.hip", "attn_short.hip",
            "moe_few.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -41,6 +41,7 @@ EXTRA = {"grouped.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          "factor.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          "attn.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          "attn_f32.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+         "attn_short.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          "moe_few.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 

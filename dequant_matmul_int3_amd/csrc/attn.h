@@ -6,7 +6,7 @@
 //   out_j = sum_t p_t sV[t,g(j)] vV[t,j]
 //
 // A block owns a chunk of one sequence's positions for one key-value head and
-// up to 16 of its query heads; its four waves take tiles of 32 positions in
+// up to 16 of its query heads; its four or eight waves take tiles of 32 positions in
 // turn, each with an online softmax of its own (running maximum and sum in
 // f32), and join them in LDS at the end.  The cache's bytes are read once and
 // bound it; both products run on the bf16 matrix cores, whatever the number of
@@ -53,13 +53,12 @@ struct AttnKernelArgs {
 
 hipError_t launch_attn_bf16(const AttnKernelArgs& k, hipStream_t s);
 hipError_t launch_attn_f32(const AttnKernelArgs& k, hipStream_t s);
+hipError_t launch_attn_short(const AttnKernelArgs& k, hipStream_t s);  // kAttnMaxWaves waves
 
 namespace {
 
-constexpr int kAttnWaves = 4;
 constexpr int kAttnTile = 32;
-constexpr int kHop = kAttnWaves * kAttnTile;
-static_assert(kAttnMaxChunk <= 64 * kHop, "a wave's tiles are kept one a lane");
+static_assert(kAttnMaxChunk <= 64 * kAttnWaves * kAttnTile, "a wave's tiles are kept one a lane");
 
 // max / sum over a 16-lane row
 template <int N>
@@ -224,8 +223,16 @@ struct AttnPlace {
 // A row of probabilities in LDS: 32 tokens of a piece, 16 bytes apart in the banks.
 constexpr int kProbRow = 32 * 2 + 16;
 
-template <int KB, int VB, int G, int NR, bool F32>
-__global__ __launch_bounds__(64 * kAttnWaves) void attn_decode_kernel(const AttnKernelArgs x) {
+// A wave's LDS: the probabilities of its tile; at the end its value sums.
+template <int G, int NR, bool F32>
+union AttnWaveLds {
+    uint8_t probs[G][F32 ? 3 : 2][4 * NR][kProbRow];
+    float red[4 * NR][G * kGroup];
+};
+
+template <int WAVES, int KB, int VB, int G, int NR, bool F32>
+__global__ __launch_bounds__(64 * WAVES) void attn_decode_kernel(const AttnKernelArgs x) {
+    constexpr int kHop = WAVES * kAttnTile;  // to a wave's next tile
     constexpr int NP = F32 ? 3 : 1;   // pieces of a query value
     constexpr int PP = F32 ? 3 : 2;   // pieces of a probability
     constexpr int KROW = G * 8 * KB, W = G * kGroup;
@@ -415,12 +422,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_decode_kernel(const Attn
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[gr][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-    // the probabilities of the waves' tiles; at the end, the waves' value sums
-    union Lds {
-        uint8_t probs[kAttnWaves][G][PP][4 * NR][kProbRow];
-        float red[kAttnWaves][4 * NR][W];
-    };
-    __shared__ __attribute__((aligned(16))) Lds lds;
+    __shared__ __attribute__((aligned(16))) AttnWaveLds<G, NR, F32> lds[WAVES];
     // scores of the tile in tk: token 2 l16 + h, head 4 r + g
     auto scores = [&](float (&s)[2][NR]) __attribute__((always_inline)) {
 #pragma unroll
@@ -523,7 +525,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_decode_kernel(const Attn
                     } else {
                         pair = bf16_pair(y0, y1);
                     }
-                    *reinterpret_cast<uint32_t*>(&lds.probs[wave][gr][k][4 * r + g][4 * l16]) = pair;
+                    *reinterpret_cast<uint32_t*>(&lds[wave].probs[gr][k][4 * r + g][4 * l16]) = pair;
                 }
             }
         }
@@ -537,7 +539,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_decode_kernel(const Attn
 #pragma unroll
             for (int k = 0; k < PP; ++k)  // rows past the heads repeat one that is there
                 ap[gr][k] = *reinterpret_cast<const u32x4_t*>(
-                    &lds.probs[wave][gr][k][l16 % (4 * NR)][16 * g]);
+                    &lds[wave].probs[gr][k][l16 % (4 * NR)][16 * g]);
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) {
             u32x4_t bv[4];
@@ -588,8 +590,8 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_decode_kernel(const Attn
     }
 
     // ---- the waves' parts: a common maximum, then sums in wave order
-    __shared__ float ml[kAttnWaves][2][16];
-    __shared__ float vo[kAttnWaves][G][16];  // what the values' codes are offset by
+    __shared__ float ml[WAVES][2][16];
+    __shared__ float vo[WAVES][G][16];  // what the values' codes are offset by
     __syncthreads();  // every wave is done with its probabilities
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
@@ -612,23 +614,23 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_decode_kernel(const Attn
         for (int gr = 0; gr < G; ++gr)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<f32x4_t*>(&lds.red[wave][4 * g + j][64 * gr + 4 * l16]) =
+                *reinterpret_cast<f32x4_t*>(&lds[wave].red[4 * g + j][64 * gr + 4 * l16]) =
                     f32x4_t{o[gr][0][j], o[gr][1][j], o[gr][2][j], o[gr][3][j]};
     }
     __syncthreads();
-    for (int i = tid; i < nr * (W / 4); i += 64 * kAttnWaves) {
+    for (int i = tid; i < nr * (W / 4); i += 64 * WAVES) {
         const int r = i / (W / 4), d = i % (W / 4) * 4;
         float mx = ml[0][0][r];
 #pragma unroll
-        for (int w = 1; w < kAttnWaves; ++w) mx = fmaxf(mx, ml[w][0][r]);
+        for (int w = 1; w < WAVES; ++w) mx = fmaxf(mx, ml[w][0][r]);
         const float base = mx == -INFINITY ? 0.0f : mx;
         float sum = 0.0f;
         f32x4_t v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int w = 0; w < kAttnWaves; ++w) {
+        for (int w = 0; w < WAVES; ++w) {
             const float e = __builtin_amdgcn_exp2f(ml[w][0][r] - base);
             sum += e * ml[w][1][r];
-            const f32x4_t z = *reinterpret_cast<const f32x4_t*>(&lds.red[w][r][d]);
+            const f32x4_t z = *reinterpret_cast<const f32x4_t*>(&lds[w].red[r][d]);
             const float c = vo[w][d >> 6][r];
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[k] = __builtin_fmaf(e, z[k] + c, v[k]);
@@ -656,36 +658,44 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_decode_kernel(const Attn
     }
 }
 
-template <int KB, int VB, int G, bool F32>
+template <int WAVES, int KB, int VB, int G, bool F32>
 void attn_heads(const AttnKernelArgs& k, dim3 grid, hipStream_t s) {
     const int per = k.a.q_heads / k.a.c.heads;
     if (per <= 4)
-        attn_decode_kernel<KB, VB, G, 1, F32><<<grid, 64 * kAttnWaves, 0, s>>>(k);
+        attn_decode_kernel<WAVES, KB, VB, G, 1, F32><<<grid, 64 * WAVES, 0, s>>>(k);
     else if (per <= 8)
-        attn_decode_kernel<KB, VB, G, 2, F32><<<grid, 64 * kAttnWaves, 0, s>>>(k);
+        attn_decode_kernel<WAVES, KB, VB, G, 2, F32><<<grid, 64 * WAVES, 0, s>>>(k);
     else
-        attn_decode_kernel<KB, VB, G, 4, F32><<<grid, 64 * kAttnWaves, 0, s>>>(k);
+        attn_decode_kernel<WAVES, KB, VB, G, 4, F32><<<grid, 64 * WAVES, 0, s>>>(k);
 }
 
-template <int KB, int VB, bool F32>
+template <int WAVES, int KB, int VB, bool F32>
 hipError_t attn_width(const AttnKernelArgs& k, dim3 grid, hipStream_t s) {
-    switch (k.a.c.groups) {
-        case 1: attn_heads<KB, VB, 1, F32>(k, grid, s); break;
-        case 2: attn_heads<KB, VB, 2, F32>(k, grid, s); break;
-        case 3: attn_heads<KB, VB, 3, F32>(k, grid, s); break;
-        default: attn_heads<KB, VB, 4, F32>(k, grid, s); break;
+    if (k.a.c.groups == 1) {
+        attn_heads<WAVES, KB, VB, 1, F32>(k, grid, s);
+    } else if (k.a.c.groups == 2) {
+        attn_heads<WAVES, KB, VB, 2, F32>(k, grid, s);
+    } else if constexpr (WAVES == kAttnWaves) {
+        if (k.a.c.groups == 3)
+            attn_heads<WAVES, KB, VB, 3, F32>(k, grid, s);
+        else
+            attn_heads<WAVES, KB, VB, 4, F32>(k, grid, s);
+    } else {
+        return hipErrorInvalidValue;  // the plan takes four waves here
     }
     return hipGetLastError();
 }
 
-template <bool F32>
+template <int WAVES, bool F32>
 hipError_t attn_bits(const AttnKernelArgs& k, hipStream_t s) {
     const uint32_t blocks = (k.items + 7) / 8 * 8 * (uint32_t)k.tiles;  // below 2^31
     const uint32_t gx = std::min<uint32_t>(blocks, 1u << 20);
     const dim3 grid(gx, (blocks + gx - 1) / gx);
     if (k.a.c.kbits == 4)
-        return k.a.c.vbits == 4 ? attn_width<4, 4, F32>(k, grid, s) : attn_width<4, 8, F32>(k, grid, s);
-    return k.a.c.vbits == 4 ? attn_width<8, 4, F32>(k, grid, s) : attn_width<8, 8, F32>(k, grid, s);
+        return k.a.c.vbits == 4 ? attn_width<WAVES, 4, 4, F32>(k, grid, s)
+                                : attn_width<WAVES, 4, 8, F32>(k, grid, s);
+    return k.a.c.vbits == 4 ? attn_width<WAVES, 8, 4, F32>(k, grid, s)
+                            : attn_width<WAVES, 8, 8, F32>(k, grid, s);
 }
 
 }  // namespace

@@ -82,7 +82,7 @@ hipError_t join(const AttnKernelArgs& k, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_attn_bf16(const AttnKernelArgs& k, hipStream_t s) {
-    return attn_bits<false>(k, s);
+    return attn_bits<kAttnWaves, false>(k, s);
 }
 
 hipError_t launch_attn_decode(const AttnArgs& a, void* workspace, hipStream_t s) {
@@ -95,7 +95,8 @@ hipError_t launch_attn_decode(const AttnArgs& a, void* workspace, hipStream_t s)
     AttnKernelArgs k{a, p.chunk, p.splits, (a.q_heads / a.c.heads + 15) / 16,
                      rows, rows * (uint32_t)p.splits,
                      FastDiv::of((uint32_t)a.c.page), q_vec, static_cast<float*>(workspace)};
-    hipError_t e = a.bf16 ? launch_attn_bf16(k, s) : launch_attn_f32(k, s);
+    hipError_t e = p.waves == kAttnMaxWaves ? launch_attn_short(k, s)
+                   : a.bf16                 ? launch_attn_bf16(k, s) : launch_attn_f32(k, s);
     if (e != hipSuccess || p.splits == 1) return e;
     return a.bf16 ? join<false>(k, s) : join<true>(k, s);
 }

@@ -3,6 +3,8 @@
 
 namespace qt {
 
-hipError_t launch_attn_f32(const AttnKernelArgs& k, hipStream_t s) { return attn_bits<true>(k, s); }
+hipError_t launch_attn_f32(const AttnKernelArgs& k, hipStream_t s) {
+    return attn_bits<kAttnWaves, true>(k, s);
+}
 
 }  // namespace qt

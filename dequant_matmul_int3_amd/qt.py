@@ -718,7 +718,7 @@ def _current(device, stream):
     current and the stream is torch's."""
     if device.type != "cuda":
         raise ValueError("libqt takes device tensors only")
-    return stream is None and device.index == torch.cuda.current_device()
+    return stream is None and device.index == torch._C._cuda_getDevice()
 
 
 def _raw_stream(device):
@@ -834,16 +834,22 @@ def qt_kv_read(slots, k, v, dim: int, dtype=torch.bfloat16, K=None, V=None, stre
     if not _current(dev, stream):
         with _on(dev, stream):
             return qt_kv_read(slots, k, v, dim, dtype, K, V)
-    if K is None:
-        K = torch.empty(shape, dtype=dtype, device=dev)
-    if V is None:
-        V = torch.empty(shape, dtype=K.dtype, device=dev)
-    xt = _xtype(K, "K")
-    _is(K, shape, K.dtype, "K")
-    _is(V, shape, K.dtype, "V")
     kc, ks, kb = k
     vc, vs, vb = v
-    _there(dev.index, slots, kc, ks, vc, vs, K, V)
+    _there(dev.index, slots, kc, ks, vc, vs)
+    if K is None and V is None:
+        K = torch.empty(shape, dtype=dtype, device=dev)
+        V = torch.empty_like(K)
+        xt = _xtype(K, "K")
+    else:
+        if K is None:
+            K = torch.empty(shape, dtype=dtype, device=dev)
+        if V is None:
+            V = torch.empty(shape, dtype=K.dtype, device=dev)
+        xt = _xtype(K, "K")
+        _is(K, shape, K.dtype, "K")
+        _is(V, shape, K.dtype, "V")
+        _there(dev.index, K, V)
     _check(lib().qt_kv_read(slots.data_ptr(), shape[0], kc.data_ptr(), ks.data_ptr(), kb,
                             vc.data_ptr(), vs.data_ptr(), vb, n_pages, page, heads, dim,
                             K.data_ptr(), V.data_ptr(), xt, _raw_stream(dev)), "qt_kv_read")
@@ -891,9 +897,9 @@ def qt_attn_decode(Q, k, v, page_table, lens, scale=None, window: int = 0, out=N
     elif want_lse:
         lse = torch.empty((B, q_heads), dtype=torch.float32, device=dev)
     need = qt_attn_decode_workspace_bytes(B, q_heads, heads, d, pages, page, window)
-    workspace, wsb = _scratch(need, dev, workspace)
     if workspace is not None:
         _there(dev.index, workspace)
+    workspace, wsb = _scratch(need, dev, workspace)
     kc, ks, kb = k
     vc, vs, vb = v
     _there(dev.index, page_table, lens, kc, ks, vc, vs)
@@ -944,13 +950,16 @@ def qt_moe_decode(X, logits, k: int, gate, up, down, act: str = "silu", out=None
     if not _current(dev, stream):
         with _on(dev, stream):
             return qt_moe_decode(X, logits, k, gate, up, down, act, out, workspace)
+    _there(dev.index, X, logits, gp, gs, up_, us, dp, ds)
     if out is None:
-        out = torch.empty(shape, dtype=X.dtype, device=dev)
-    _is(out, shape, X.dtype, "out")
-    workspace, wsb = _scratch(qt_moe_decode_workspace_bytes(T, k, E, D, F, xt), dev, workspace)
-    _there(dev.index, X, logits, gp, gs, up_, us, dp, ds, out)
+        out = torch.empty_like(X)
+    else:
+        _is(out, shape, X.dtype, "out")
+        _there(dev.index, out)
+    need = qt_moe_decode_workspace_bytes(T, k, E, D, F, xt)
     if workspace is not None:
         _there(dev.index, workspace)
+    workspace, wsb = _scratch(need, dev, workspace)
     _check(lib().qt_moe_decode(X.data_ptr(), xt, T, D, F, logits.data_ptr(), E, k, QT_ACT[act],
                                gp.data_ptr(), gs.data_ptr(), gate[2], up_.data_ptr(),
                                us.data_ptr(), up[2], dp.data_ptr(), ds.data_ptr(), down[2],

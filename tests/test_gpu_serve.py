@@ -207,6 +207,28 @@ def test_attention_in_chunks(H, per, d, P, kb, vb, lens, window, scale, dtype):
     assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kb,vb", [(4, 4), (8, 8), (4, 8), (8, 4)])
+@pytest.mark.parametrize("H,per,d,P,window", [(2, 3, 128, 16, 0), (1, 7, 64, 48, 0),
+                                              (2, 16, 100, 32, 990), (1, 33, 24, 64, 500)])
+def test_attention_in_one_block(H, per, d, P, window, kb, vb, dtype):
+    """Short contexts that one block takes, without a second launch."""
+    say(f"one block H={H} per={per} d={d} P={P} w={window} k{kb} v{vb} {dtype}")
+    g = gen(d + 5 * kb + vb)
+    lens = torch.tensor([1024 // P * P, 1000, 257, 256, 33, 0], device=DEV, dtype=torch.int32)
+    B, wide = 6, (2048 if window else 1024) // P
+    if window:
+        lens[1] = 2000
+    assert qt.qt_attn_decode_workspace_bytes(B, H * per, H, d, wide, P, window) == 0
+    k, v = cache(B * wide + 2, P, H, d, kb, vb, g)
+    table = tables(B, wide, g)
+    Q = normal(g, B, H * per, d).to(DT[dtype])
+    got = qt.qt_attn_decode(Q, k, v, table, lens, window=window, want_lse=True)
+    check(Q, k, v, table, lens, got, window)
+    again = qt.qt_attn_decode(Q, k, v, table, lens, window=window, want_lse=True)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
 @pytest.mark.parametrize("kb,vb", [(4, 4), (8, 8)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_memory_that_does_not_count(kb, vb, dtype):

@@ -24,6 +24,8 @@ def test_cache_sizes():
 def test_workspace_sizes():
     w = qt.qt_attn_decode_workspace_bytes
     assert w(1, 32, 8, 128, 16, 16) == 0                    # one chunk
+    assert w(1, 32, 8, 128, 64, 16) == 0                    # short: one block of eight waves
+    assert w(1, 32, 8, 129, 64, 16) > 0                     # but for wide heads
     assert w(1, 32, 8, 128, 64, 64) > 0                     # a long context is cut
     assert w(256, 32, 8, 128, 32, 64) == 0                  # a batch fills the card uncut
     assert w(1, 32, 8, 128, 4096, 64, window=100) == 0      # a window bounds the span
@@ -85,11 +87,11 @@ def test_attention_refusals():
     assert call(page=17) == SHAPE and call(dim=300) == SHAPE
     assert call(kb=2) == ARG and call(vb=0) == ARG
     assert call(scale=float("nan")) == ARG and call(scale=float("inf")) == ARG
-    assert call(pages=64) == WORKSPACE and call(pages=64, ws=J, wsb=64) == WORKSPACE
-    assert call(pages=64, ws=J + 4, wsb=1 << 24) == ALIGN
+    assert call(pages=128) == WORKSPACE and call(pages=128, ws=J, wsb=64) == WORKSPACE
+    assert call(pages=128, ws=J + 4, wsb=1 << 24) == ALIGN
     assert call(out=H + 1) == ALIGN and call(lse=I_ + 2) == ALIGN and call(lens=C_ + 1) == ALIGN
     assert call(out=A) == ALIAS and call(lse=H) == ALIAS and call(out=D + 16) == ALIAS
-    assert call(lse=B) == ALIAS and call(pages=64, ws=A, wsb=1 << 24) == ALIAS
+    assert call(lse=B) == ALIAS and call(pages=128, ws=A, wsb=1 << 24) == ALIAS
 
 
 def test_binding_refusals():
