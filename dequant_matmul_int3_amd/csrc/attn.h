@@ -230,12 +230,17 @@ union AttnWaveLds {
     float red[4 * NR][G * kGroup];
 };
 
+// Waves a SIMD at least: two, but where the LDS of a block is more than half a CU's.
+constexpr int attn_waves(int G, int NR, bool f32) { return f32 && G == 4 && NR == 4 ? 1 : 2; }
+
 template <int WAVES, int KB, int VB, int G, int NR, bool F32>
-__global__ __launch_bounds__(64 * WAVES) void attn_decode_kernel(const AttnKernelArgs x) {
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(attn_waves(G, NR, F32)))) void
+attn_decode_kernel(const AttnKernelArgs x) {
     constexpr int kHop = WAVES * kAttnTile;  // to a wave's next tile
     constexpr int NP = F32 ? 3 : 1;   // pieces of a query value
     constexpr int PP = F32 ? 3 : 2;   // pieces of a probability
     constexpr int KROW = G * 8 * KB, W = G * kGroup;
+    constexpr bool kWide = G > 2;  // registers are short: see there
     using KC = Code<KB, F32>;
     using VC = Code<VB, F32>;
     const AttnArgs& a = x.a;
@@ -297,7 +302,16 @@ __global__ __launch_bounds__(64 * WAVES) void attn_decode_kernel(const AttnKerne
     auto rows_of = [&](const AttnPlace& w, int h) __attribute__((always_inline)) {
         return w.ph[h] * prow + (int64_t)(w.at[h] - 16 * h) * G;
     };
+    // Wide heads leave no registers for the lane's part of every address: it is
+    // worked out anew for a tile (a value that did not fit would be reloaded
+    // in the loop, behind all loads in flight).
+    auto here = [&]() __attribute__((always_inline)) {
+        int v = lane;
+        if constexpr (kWide) asm volatile("" : "+v"(v));
+        return v;
+    };
     auto load_k = [&](const AttnPlace& w, KeyTile<KB, G>& t) __attribute__((always_inline)) {
+        const int at = here(), l16 = at & 15, g = at >> 4;
         const int64_t bk = l16 < 8 ? rows_of(w, 0) : rows_of(w, 1);
         const uint8_t* kp = a.c.kc + bk * (8 * KB) + 2 * l16 * KROW + (KB == 8 ? 16 : 8) * g;
 #pragma unroll
@@ -318,6 +332,7 @@ __global__ __launch_bounds__(64 * WAVES) void attn_decode_kernel(const AttnKerne
         load_floats(a.c.vs + bk + 2 * l16 * G, t.sv);
     };
     auto load_v = [&](const AttnPlace& w, ValueTile<VB, G>& t) __attribute__((always_inline)) {
+        const int at = here(), l16 = at & 15, g = at >> 4;
         // blocks of eight tokens; a block's 64 G values are its columns' 16 G words
         const uint8_t* vp = a.c.vc + (g < 2 ? rows_of(w, 0) : rows_of(w, 1)) * (8 * VB) +
                             (g * G * 16 + l16) * (4 * VB);
@@ -343,62 +358,86 @@ __global__ __launch_bounds__(64 * WAVES) void attn_decode_kernel(const AttnKerne
     load_v(w0, tv0);
 
     // ---- queries as operands: row l16 = 4 i + r is head 4 r + i, values 16 g ..
-    // of each group in the order that the codes come in
-    u32x4_t q[NP][G][2];
-    float qoff[NR][G];  // -8 times the group's sum of head 4 r + g, where the codes are offset
-    {
+    // of each group in the order that the codes come in.  All waves' are the same:
+    // those of wide heads lie in LDS, a group made by a wave each, so that the
+    // registers leave room for two blocks a CU.
+    static_assert(!kWide || G <= WAVES, "a wave a group");
+    __shared__ u32x4_t ql[kWide ? NP : 1][kWide ? G : 1][2][64];
+    __shared__ __attribute__((aligned(16))) float qsum[G][16];
+    u32x4_t q[NP][kWide ? 1 : G][2];
+    // -8 times the group's sum of head 4 r + g, where the codes are offset
+    float qoff[NR][kWide ? 1 : G];
+    auto query = [&](int gr, u32x4_t (&to)[NP][2]) __attribute__((always_inline)) {
         const int64_t head = (int64_t)kvh * per + r0 + min(4 * (l16 & 3) + (l16 >> 2), nr - 1);
         const int64_t at = (int64_t)b * a.ldq + head * a.c.dim;
+        float sum = 0.0f;
 #pragma unroll
-        for (int gr = 0; gr < G; ++gr) {
-            float sum = 0.0f;
+        for (int h = 0; h < 2; ++h) {
+            const int d0 = 64 * gr + 16 * g + 8 * h;
+            uint32_t v[8];  // the eight values' bits, in order
+            if (x.q_vec) {  // eight values lie wholly inside or outside the head
+                const bool in = d0 < a.c.dim;
+                const int64_t i = at + (in ? d0 : 0);
+                if constexpr (F32) {
+                    const u32x4_t* z =
+                        reinterpret_cast<const u32x4_t*>(static_cast<const float*>(a.Q) + i);
+                    const u32x4_t z0 = z[0], z1 = z[1];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int d0 = 64 * gr + 16 * g + 8 * h;
-                uint32_t v[8];  // the eight values' bits, in order
-                if (x.q_vec) {  // eight values lie wholly inside or outside the head
-                    const bool in = d0 < a.c.dim;
-                    const int64_t i = at + (in ? d0 : 0);
-                    if constexpr (F32) {
-                        const u32x4_t* z = reinterpret_cast<const u32x4_t*>(
-                            static_cast<const float*>(a.Q) + i);
-                        const u32x4_t z0 = z[0], z1 = z[1];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) v[j] = in ? (j < 4 ? z0[j & 3] : z1[j & 3]) : 0u;
-                    } else {
-                        const u32x4_t z = *reinterpret_cast<const u32x4_t*>(
-                            static_cast<const uint16_t*>(a.Q) + i);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            v[j] = in ? (j & 1 ? z[j >> 1] >> 16 : z[j >> 1] & 0xFFFFu) : 0u;
-                    }
+                    for (int j = 0; j < 8; ++j) v[j] = in ? (j < 4 ? z0[j & 3] : z1[j & 3]) : 0u;
                 } else {
+                    const u32x4_t z = *reinterpret_cast<const u32x4_t*>(
+                        static_cast<const uint16_t*>(a.Q) + i);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int64_t i = at + min(d0 + j, a.c.dim - 1);
-                        const uint32_t z = F32 ? static_cast<const uint32_t*>(a.Q)[i]
-                                               : (uint32_t)static_cast<const uint16_t*>(a.Q)[i];
-                        v[j] = d0 + j < a.c.dim ? z : 0u;
-                    }
+                    for (int j = 0; j < 8; ++j)
+                        v[j] = in ? (j & 1 ? z[j >> 1] >> 16 : z[j >> 1] & 0xFFFFu) : 0u;
                 }
-                uint32_t p[NP][8];
+            } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const uint32_t z = v[key_order<KB, F32>(j)];
-                    if constexpr (F32) {
-                        split3(__uint_as_float(z), p[0][j], p[NP > 1 ? 1 : 0][j],
-                               p[NP > 1 ? 2 : 0][j]);
-                    } else {
-                        p[0][j] = z;
-                        sum += __uint_as_float(z << 16);
-                    }
+                    const int64_t i = at + min(d0 + j, a.c.dim - 1);
+                    const uint32_t z = F32 ? static_cast<const uint32_t*>(a.Q)[i]
+                                           : (uint32_t)static_cast<const uint16_t*>(a.Q)[i];
+                    v[j] = d0 + j < a.c.dim ? z : 0u;
                 }
-#pragma unroll
-                for (int k = 0; k < NP; ++k)
-                    q[k][gr][h] = u32x4_t{p[k][0] | p[k][1] << 16, p[k][2] | p[k][3] << 16,
-                                          p[k][4] | p[k][5] << 16, p[k][6] | p[k][7] << 16};
             }
-            sum = quad_sum(sum);  // of row l16, in every lane of the column
+            uint32_t p[NP][8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t z = v[key_order<KB, F32>(j)];
+                if constexpr (F32) {
+                    split3(__uint_as_float(z), p[0][j], p[NP > 1 ? 1 : 0][j], p[NP > 1 ? 2 : 0][j]);
+                } else {
+                    p[0][j] = z;
+                    sum += __uint_as_float(z << 16);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < NP; ++k)
+                to[k][h] = u32x4_t{p[k][0] | p[k][1] << 16, p[k][2] | p[k][3] << 16,
+                                   p[k][4] | p[k][5] << 16, p[k][6] | p[k][7] << 16};
+        }
+        return quad_sum(sum);  // of row l16, in every lane of the column
+    };
+    if constexpr (kWide) {
+        if (wave < G) {
+            u32x4_t to[NP][2];
+            const float sum = query(wave, to);
+#pragma unroll
+            for (int k = 0; k < NP; ++k)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) ql[k][wave][h][lane] = to[k][h];
+            if (g == 0) qsum[wave][l16] = -8.0f * sum;
+        }
+        __syncthreads();
+    } else {
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) {
+            u32x4_t to[NP][2];
+            const float sum = query(gr, to);
+#pragma unroll
+            for (int k = 0; k < NP; ++k)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) q[k][gr][h] = to[k][h];
 #pragma unroll
             for (int r = 0; r < NR; ++r)
                 qoff[r][gr] = KC::kOffset ? -8.0f * __shfl(sum, 4 * g + r) : 0.0f;
@@ -426,14 +465,22 @@ __global__ __launch_bounds__(64 * WAVES) void attn_decode_kernel(const AttnKerne
     // scores of the tile in tk: token 2 l16 + h, head 4 r + g
     auto scores = [&](float (&s)[2][NR]) __attribute__((always_inline)) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            f32x4_t d[G];
+        for (int gr = 0; gr < G; ++gr) {
+            u32x4_t qa[NP][2];
 #pragma unroll
-            for (int gr = 0; gr < G; ++gr) {
-                d[gr] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-                if constexpr (KC::kOffset)
+            for (int p = 0; p < NP; ++p)
 #pragma unroll
-                    for (int r = 0; r < NR; ++r) d[gr][r] = qoff[r][gr];
+                for (int i = 0; i < 2; ++i) qa[p][i] = kWide ? ql[p][gr][i][lane] : q[p][gr][i];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                f32x4_t d = {0.f, 0.f, 0.f, 0.f};
+                if constexpr (KC::kOffset) {
+                    if constexpr (kWide)
+                        d = *reinterpret_cast<const f32x4_t*>(&qsum[gr][4 * g]);
+                    else
+#pragma unroll
+                        for (int r = 0; r < NR; ++r) d[r] = qoff[r][gr];
+                }
                 u32x4_t k0, k1;
                 if constexpr (KB == 8) {
                     k0 = key_operand8(tk.k[h][gr][0], tk.k[h][gr][1]);
@@ -444,17 +491,16 @@ __global__ __launch_bounds__(64 * WAVES) void attn_decode_kernel(const AttnKerne
                 }
 #pragma unroll
                 for (int p = 0; p < NP; ++p) {
-                    d[gr] = mma(q[p][gr][0], k0, d[gr]);
-                    d[gr] = mma(q[p][gr][1], k1, d[gr]);
+                    d = mma(qa[p][0], k0, d);
+                    d = mma(qa[p][1], k1, d);
+                }
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    const float f = tk.sk[h * G + gr] * sc;
+                    s[h][r] = gr == 0 ? f * d[r] : __builtin_fmaf(f, d[r], s[h][r]);
                 }
             }
-#pragma unroll
-            for (int r = 0; r < NR; ++r) s[h][r] = (tk.sk[h * G] * sc) * d[0][r];
-#pragma unroll
-            for (int gr = 1; gr < G; ++gr)
-#pragma unroll
-                for (int r = 0; r < NR; ++r)
-                    s[h][r] = __builtin_fmaf(tk.sk[h * G + gr] * sc, d[gr][r], s[h][r]);
+            if constexpr (kWide) __builtin_amdgcn_sched_barrier(0);
         }
     };
     // the tile's probabilities, times the values' scales, to LDS
@@ -533,15 +579,13 @@ __global__ __launch_bounds__(64 * WAVES) void attn_decode_kernel(const AttnKerne
     };
     // the second product of the tile in tv
     auto values = [&](const ValueTile<VB, G>& tv) __attribute__((always_inline)) {
-        u32x4_t ap[G][PP];
-#pragma unroll
-        for (int gr = 0; gr < G; ++gr)
-#pragma unroll
-            for (int k = 0; k < PP; ++k)  // rows past the heads repeat one that is there
-                ap[gr][k] = *reinterpret_cast<const u32x4_t*>(
-                    &lds[wave].probs[gr][k][l16 % (4 * NR)][16 * g]);
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) {
+            u32x4_t ap[PP];
+#pragma unroll
+            for (int k = 0; k < PP; ++k)  // rows past the heads repeat one that is there
+                ap[k] = *reinterpret_cast<const u32x4_t*>(
+                    &lds[wave].probs[gr][k][l16 % (4 * NR)][16 * g]);
             u32x4_t bv[4];
             if constexpr (VB == 8)
                 value_operands8(tv.v[2 * gr], tv.v[2 * gr + 1], bv);
@@ -550,7 +594,7 @@ __global__ __launch_bounds__(64 * WAVES) void attn_decode_kernel(const AttnKerne
 #pragma unroll
             for (int k = 0; k < PP; ++k)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[gr][i] = mma(ap[gr][k], bv[i], o[gr][i]);
+                for (int i = 0; i < 4; ++i) o[gr][i] = mma(ap[k], bv[i], o[gr][i]);
         }
     };
 
@@ -564,28 +608,38 @@ __global__ __launch_bounds__(64 * WAVES) void attn_decode_kernel(const AttnKerne
 #pragma unroll
             for (int i = 0; i < 2 * G; ++i) sv[i] = tk.sv[i];
             load_k(next, tk);
+            if constexpr (kWide) __builtin_amdgcn_sched_barrier(0);
         };
         take(w1);
         weigh(first, w0, s, sv);
         // wa: the place of tile i + 1
         auto turn = [&](int i, AttnPlace& wa, const ValueTile<VB, G>& now, ValueTile<VB, G>& next) __attribute__((always_inline)) {
-            load_v(wa, next);
+            if constexpr (!kWide) load_v(wa, next);
             const AttnPlace wb = find(min(i + 2, last));
             take(wb);
             values(now);
+            if constexpr (kWide) {  // now and next are one: not before its last use
+                __builtin_amdgcn_sched_barrier(0);
+                load_v(wa, next);
+            }
             weigh(first + (i + 1) * kHop, wa, s, sv);
             wa = wb;
         };
-        int i = 0;
-        for (; i + 1 < last; i += 2) {
-            turn(i, w1, tv0, tv1);
-            turn(i + 1, w1, tv1, tv0);
-        }
-        if (i < last) {
-            turn(i, w1, tv0, tv1);
-            values(tv1);
-        } else {
+        if constexpr (kWide) {
+            for (int i = 0; i < last; ++i) turn(i, w1, tv0, tv0);
             values(tv0);
+        } else {
+            int i = 0;
+            for (; i + 1 < last; i += 2) {
+                turn(i, w1, tv0, tv1);
+                turn(i + 1, w1, tv1, tv0);
+            }
+            if (i < last) {
+                turn(i, w1, tv0, tv1);
+                values(tv1);
+            } else {
+                values(tv0);
+            }
         }
     }
 
