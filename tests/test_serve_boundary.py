@@ -1,14 +1,34 @@
 """The C ABI of the cache, attention and few-token expert calls on the CPU: sizes and refusals
-through the built library (nothing may reach the GPU here)."""
+through the built library (nothing may reach the GPU here), and the validation layer under the
+sanitizers with its launchers replaced by stubs."""
+import os
+import shutil
+
 import pytest
 import torch
 
 import dequant_matmul_int3_amd as qt
+from tests.test_sanitizers import HIP_INCLUDE, ROOT, SAN, _env, _run
 
 A, B, C_, D = 0x7F0000000000, 0x7F1000000000, 0x7F2000000000, 0x7F3000000000
 E, F_, G_, H = 0x7F4000000000, 0x7F5000000000, 0x7F6000000000, 0x7F7000000000
 I_, J = 0x7E0000000000, 0x7E1000000000
 NULL, SHAPE, ALIGN, DTYPE, ARG, ALIAS, WORKSPACE = 1, 2, 3, 4, 5, 6, 8
+
+
+@pytest.mark.skipif(shutil.which("g++") is None or not os.path.isdir(os.path.join(HIP_INCLUDE, "hip")),
+                    reason="g++ or the HIP headers not available")
+def test_serving_validation_under_sanitizers(tmp_path):
+    exe = str(tmp_path / "serve_driver")
+    csrc = os.path.join(ROOT, "dequant_matmul_int3_amd", "csrc")
+    rc, out = _run(["g++", "-std=c++17", "-D__HIP_PLATFORM_AMD__", *SAN, "-I", HIP_INCLUDE,
+                    "-I", os.path.join(ROOT, "include"), "-I", csrc,
+                    os.path.join(csrc, "api_serve.cpp"),
+                    os.path.join(ROOT, "tests", "sanitize", "serve_stubs.cpp"),
+                    os.path.join(ROOT, "tests", "sanitize", "serve_driver.cpp"), "-o", exe])
+    assert rc == 0, out
+    rc, out = _run([exe], env=_env())
+    assert rc == 0 and "0 failures" in out and "runtime error" not in out, out
 
 
 def test_cache_sizes():
