@@ -33,6 +33,11 @@
 // and the eightfold sums are taken out again (in the keys' product as its
 // initial value, in the values' at the end).  f32 calls convert to v itself
 // (over a long flat softmax the offset costs more than f32's accuracy).
+//
+// Measured, this kernel alone: one sequence of 131072 positions, 8 heads of 128
+// with 8 queries each, 4 bits: 34 us (151 MB, 4.4 TB/s); 64 sequences of up to
+// 8192, 8 and 4 bits: 88-91 us (401 MB, 4.5 TB/s), where loads and conversions
+// alone take 64; about 9 us of a block are its start, first loads and end.
 #pragma once
 #include "lds_barrier.h"
 #include "serve.h"
