@@ -772,14 +772,30 @@ def _kv_part(part, dim, what):
     return shape
 
 
-def _kv(k, v, dim):
-    """(n_pages, heads, page) of a cache for heads of dim values, checked."""
+def _kv(k, v, dim, index):
+    """(n_pages, heads, page) of a cache for heads of dim values on the device of
+    this index, checked."""
+    kc, ks, kb = k
+    vc, vs, vb = v
+    shape, n = ks.shape, ks.numel()
+    if not (1 <= dim <= 256 and len(shape) == 4 and shape[3] == -(-dim // 64) and vs.shape == shape
+            and (kb == 8 or kb == 4) and (vb == 8 or vb == 4)
+            and kc.numel() == 8 * kb * n and vc.numel() == 8 * vb * n
+            and ks.dtype == vs.dtype == torch.float32 and kc.dtype == vc.dtype == torch.uint8):
+        _kv_refuse(k, v, dim)
+    if not (kc.get_device() == ks.get_device() == vc.get_device() == vs.get_device() == index
+            and kc.is_contiguous() and ks.is_contiguous() and vc.is_contiguous()
+            and vs.is_contiguous()):
+        _there(index, kc, ks, vc, vs)
+    return shape[0], shape[1], shape[2]
+
+
+def _kv_refuse(k, v, dim):
+    """Says which part of a cache is wrong."""
     if not 1 <= dim <= 256:
         raise ValueError("dim must be 1 to 256")
-    shape = _kv_part(k, dim, "k")
-    if shape != _kv_part(v, dim, "v"):
+    if _kv_part(k, dim, "k") != _kv_part(v, dim, "v"):
         raise ValueError("k and v must have the same pages, heads and page size")
-    return shape[0], shape[1], shape[2]
 
 
 def _tokens(t, what):
@@ -804,19 +820,20 @@ def qt_kv_write(K, V, slots, k, v, stream=None):
         raise ValueError("K and V must have the same shape and type")
     xt = _xtype(K, "K")
     T, H, d = K.shape
-    n_pages, heads, page = _kv(k, v, d)
+    dev = K.device
+    index = K.get_device()
+    n_pages, heads, page = _kv(k, v, d, index)
     if heads != H:
         raise ValueError("K and the cache must have the same heads")
     if slots.shape != (T,) or slots.dtype != torch.int32:
         raise ValueError(f"slots must be {torch.int32} of shape {(T,)}")
-    dev = K.device
     if not _current(dev, stream):
         with _on(dev, stream):
             return qt_kv_write(K, V, slots, k, v)
     kc, ks, kb = k
     vc, vs, vb = v
-    _there(dev.index, slots, kc, ks, vc, vs)
-    if V.get_device() != dev.index:
+    _there(index, slots)
+    if V.get_device() != index:
         raise ValueError("all tensors must be on the same device")
     _check(lib().qt_kv_write(K.data_ptr(), ldk, V.data_ptr(), ldv, xt, T, slots.data_ptr(),
                              kc.data_ptr(), ks.data_ptr(), kb, vc.data_ptr(), vs.data_ptr(), vb,
@@ -826,17 +843,17 @@ def qt_kv_write(K, V, slots, k, v, stream=None):
 def qt_kv_read(slots, k, v, dim: int, dtype=torch.bfloat16, K=None, V=None, stream=None):
     """-> (K, V) [R, heads, dim] of the slots [R] int32 of the cache, in dtype
     (f32 or bf16); slots outside the cache give zeros."""
-    n_pages, heads, page = _kv(k, v, dim)
+    dev = slots.device
+    n_pages, heads, page = _kv(k, v, dim, slots.get_device())
     if slots.dim() != 1 or slots.dtype != torch.int32:
         raise ValueError("slots must be [R] of torch.int32")
     shape = (slots.shape[0], heads, dim)
-    dev = slots.device
     if not _current(dev, stream):
         with _on(dev, stream):
             return qt_kv_read(slots, k, v, dim, dtype, K, V)
     kc, ks, kb = k
     vc, vs, vb = v
-    _there(dev.index, slots, kc, ks, vc, vs)
+    _there(dev.index, slots)
     if K is None and V is None:
         K = torch.empty(shape, dtype=dtype, device=dev)
         V = torch.empty_like(K)
@@ -873,7 +890,9 @@ def qt_attn_decode(Q, k, v, page_table, lens, scale=None, window: int = 0, out=N
     ldq = _tokens(Q, "Q")
     xt = _xtype(Q, "Q")
     B, q_heads, d = shape = Q.shape
-    n_pages, heads, page = _kv(k, v, d)
+    dev = Q.device
+    index = Q.get_device()
+    n_pages, heads, page = _kv(k, v, d, index)
     if page_table.dim() != 2 or page_table.shape[0] != B or page_table.dtype != torch.int32:
         raise ValueError("page_table must be [B, table_pages] of torch.int32")
     if lens.shape != (B,) or lens.dtype != torch.int32:
@@ -881,28 +900,27 @@ def qt_attn_decode(Q, k, v, page_table, lens, scale=None, window: int = 0, out=N
     pages = page_table.shape[1]
     if scale is None:
         scale = d ** -0.5
-    dev = Q.device
     if not _current(dev, stream):
         with _on(dev, stream):
             return qt_attn_decode(Q, k, v, page_table, lens, scale, window, out, lse, want_lse,
                                   workspace)
     if out is None:
-        out = torch.empty(shape, dtype=Q.dtype, device=dev)
+        out = torch.empty_like(Q) if Q.is_contiguous() else Q.new_empty(shape)
     else:
         _is(out, shape, Q.dtype, "out")
-        _there(dev.index, out)
+        _there(index, out)
     if lse is not None:
         _is(lse, (B, q_heads), torch.float32, "lse")
-        _there(dev.index, lse)
+        _there(index, lse)
     elif want_lse:
-        lse = torch.empty((B, q_heads), dtype=torch.float32, device=dev)
+        lse = Q.new_empty((B, q_heads), dtype=torch.float32)
     need = qt_attn_decode_workspace_bytes(B, q_heads, heads, d, pages, page, window)
     if workspace is not None:
-        _there(dev.index, workspace)
+        _there(index, workspace)
     workspace, wsb = _scratch(need, dev, workspace)
     kc, ks, kb = k
     vc, vs, vb = v
-    _there(dev.index, page_table, lens, kc, ks, vc, vs)
+    _there(index, page_table, lens)
     _check(lib().qt_attn_decode(Q.data_ptr(), ldq, xt, B, q_heads, kc.data_ptr(), ks.data_ptr(),
                                 kb, vc.data_ptr(), vs.data_ptr(), vb, n_pages, page, heads, d,
                                 page_table.data_ptr(), pages, lens.data_ptr(), window, scale,
