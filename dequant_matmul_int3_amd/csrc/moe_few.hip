@@ -301,6 +301,31 @@ moe_few_up_kernel(const FewKernelArgs x) {
         u32x4_t p[NL];
         float sg, su;
     };
+    // A block's work as steps of one round each: tile after tile, its tokens in
+    // passes of RT (a pass reads the weights again).  Tile f of active expert n is
+    // counted on (dividing by FT at every step took as long as an eighth of it).
+    struct Step {
+        int it, n, f, p0, c;
+        uint32_t act, who;  // of expert n
+    };
+    auto enter = [&](Step& t) __attribute__((always_inline)) {
+        t.act = (uint32_t)__builtin_amdgcn_readfirstlane((int)rt.act[t.n]);
+        t.who = (uint32_t)__builtin_amdgcn_readfirstlane((int)rt.mask[t.act & 0xFFFFu]);
+    };
+    auto advance = [&](Step& t) __attribute__((always_inline)) {
+        if (t.it >= it1 || ++t.c < rounds) return;
+        t.c = 0;
+        t.p0 += RT;
+        if (t.p0 < __popc(t.who)) return;
+        t.p0 = 0;
+        if (++t.it == it1) {  // past the last step its loads repeat
+            t.c = rounds - 1;
+        } else if (++t.f == FT) {
+            t.f = 0;
+            ++t.n;
+            enter(t);
+        }
+    };
     // The chunk of this wave in round c of a tile (zeros past the row): the tile's
     // and chunk's place is the wave's, a lane's own place in it stays.
     int off[NL], own_at[NL];  // of a lane's pieces, in the weights and in LDS
@@ -317,9 +342,9 @@ moe_few_up_kernel(const FewKernelArgs x) {
                            (id - TG::kPieces) % TU::kParts * 16;
     }
     const int soff = (lane >> 2) * G + (lane & 3);  // row lane / 4, group lane % 4
-    auto load = [&](int it, int c, Chunk& k) __attribute__((always_inline)) {
-        const int e = __builtin_amdgcn_readfirstlane((int)(rt.act[it / FT] & 0xFFFFu));
-        const int f0 = it % FT * 16, q0 = kUpCG * (c * W + wave);
+    auto load = [&](const Step& t, Chunk& k) __attribute__((always_inline)) {
+        const int e = (int)(t.act & 0xFFFFu);
+        const int f0 = t.f * 16, q0 = kUpCG * (t.c * W + wave);
         if (q0 + kUpCG <= G && f0 + 16 <= a.F) {
             const int64_t at = ((int64_t)e * a.F + f0) * G + q0;
             const uint8_t *g = a.gate.packed + at * TG::kGB, *u = a.up.packed + at * TU::kGB;
@@ -390,27 +415,11 @@ moe_few_up_kernel(const FewKernelArgs x) {
             }
         }
     };
-    // A block's work as steps of one round each: tile after tile, its tokens in
-    // passes of RT (a pass reads the weights again).
-    struct Step {
-        int it, p0, c;
-    };
-    auto tokens_of = [&](int it) __attribute__((always_inline)) {
-        return __builtin_amdgcn_readfirstlane((int)rt.mask[rt.act[it / FT] & 0xFFFFu]);
-    };
-    auto advance = [&](Step& t) __attribute__((always_inline)) {
-        if (t.it >= it1 || ++t.c < rounds) return;
-        t.c = 0;
-        t.p0 += RT;
-        if (a.T <= RT || t.p0 >= __popc(tokens_of(t.it))) {
-            t.p0 = 0;
-            ++t.it;
-        }
-    };
-    Step now{it0, 0, 0}, ahead = now;
+    Step now{it0, it0 / FT, it0 % FT, 0, 0, 0, 0};
+    enter(now);
+    Step ahead = now;
     auto load_ahead = [&](Chunk& k) __attribute__((always_inline)) {
-        // past the last step its loads repeat
-        load(min(ahead.it, it1 - 1), ahead.it < it1 ? ahead.c : rounds - 1, k);
+        load(ahead, k);
         advance(ahead);
     };
     int have_e = -1, have_p = 0, have_c = 0;  // what the stage holds: rounds have_c ..
@@ -519,14 +528,13 @@ moe_few_up_kernel(const FewKernelArgs x) {
     };
     // one step from the chunk in k; false after the last one
     auto turn = [&](const Chunk& k) __attribute__((always_inline)) {
-        const uint32_t act = __builtin_amdgcn_readfirstlane((int)rt.act[now.it / FT]);
-        const int e = (int)(act & 0xFFFFu), who = tokens_of(now.it);
+        const int e = (int)(now.act & 0xFFFFu), who = (int)now.who;
         const int nt = min(RT, __popc(who) - now.p0);
         if (have_e != e || have_p != now.p0 || now.c < have_c || now.c >= have_c + S)
             stage(e, who, nt);
         if (now.c == 0) acc[0] = acc[1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         mul(now.c, have_c * (4 * W), k);
-        if (now.c + 1 == rounds) finish((int)(act >> 16) + now.p0, nt, now.it % FT * 16);
+        if (now.c + 1 == rounds) finish((int)(now.act >> 16) + now.p0, nt, now.f * 16);
         advance(now);
         return now.it < it1;
     };
