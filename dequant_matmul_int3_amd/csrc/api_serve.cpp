@@ -197,7 +197,7 @@ extern "C" {
 size_t qt_moe_decode_workspace_bytes(int64_t T, int32_t k, int32_t E, int64_t D, int64_t F,
                                      qt_dtype xt) {
     if (!few_sizes_ok(T, k, E, D, F) || !dtype_ok(xt)) return 0;
-    return (size_t)qt::few_plan(T, k, F, xt == QT_BF16).bytes;
+    return (size_t)qt::few_workspace(T, k, E, D, F, xt == QT_BF16);
 }
 
 qt_status qt_moe_decode(const void* X, qt_dtype xt, int64_t T, int64_t D, int64_t F,

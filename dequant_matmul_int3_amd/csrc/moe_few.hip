@@ -806,9 +806,48 @@ hipError_t run_down(const FewKernelArgs& x, hipStream_t s) {
     return hipGetLastError();
 }
 
+// bf16 tokens to f32 and back (one rounding), around the full layer's launches.
+__global__ __launch_bounds__(256) void widen_kernel(const uint16_t* x, float* y, int64_t n) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+        y[i] = __uint_as_float((uint32_t)x[i] << 16);
+}
+__global__ __launch_bounds__(256) void narrow_kernel(const float* x, __bf16* y, int64_t n) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+        y[i] = (__bf16)x[i];
+}
+
+hipError_t run_long(const FewArgs& a, void* workspace, hipStream_t s) {
+    const int64_t n = (int64_t)a.T * a.D;
+    const unsigned grid = (unsigned)std::min<int64_t>((n + 255) / 256, 2048);
+    const float* in = static_cast<const float*>(a.X);
+    float* out = static_cast<float*>(a.out);
+    if (a.bf16) {
+        float* x = reinterpret_cast<float*>(
+            static_cast<uint8_t*>(workspace) +
+            few_align((int64_t)moe_layer_workspace(a.T, a.k, a.E, a.D, a.F)));
+        out = x + few_align(n * 4) / 4;
+        widen_kernel<<<grid, 256, 0, s>>>(static_cast<const uint16_t*>(a.X), x, n);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        in = x;
+    }
+    const hipError_t e = launch_moe_layer(
+        in, a.T, a.D, a.F, a.logits, a.E, a.k, a.gate.packed, a.gate.scales, a.gate.bits,
+        a.up.packed, a.up.scales, a.up.bits, a.down.packed, a.down.scales, a.down.bits, out,
+        workspace, s);
+    if (e != hipSuccess || !a.bf16) return e;
+    narrow_kernel<<<grid, 256, 0, s>>>(out, static_cast<__bf16*>(a.out), n);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_moe_few(const FewArgs& a, void* workspace, hipStream_t s) {
+    // the full layer takes SiLU, and f32 rows aligned to 16 bytes
+    const bool wide_rows = a.bf16 || ((reinterpret_cast<uintptr_t>(a.X) | reinterpret_cast<uintptr_t>(a.out)) & 15) == 0;
+    if (wide_rows && a.act == 0 &&
+        few_long(a.T, a.k, a.E, a.D, a.F, a.bf16, a.gate.bits, a.up.bits, a.down.bits))
+        return run_long(a, workspace, s);
     const FewPlan p = few_plan(a.T, a.k, a.F, a.bf16);
     uint8_t* w = static_cast<uint8_t*>(workspace);
     FewKernelArgs x;

@@ -130,6 +130,7 @@ constexpr int kFewMaxTokens = 16;
 constexpr int kFewMaxTopK = 32;
 constexpr int kFewMaxExperts = 512;
 constexpr int64_t kFewMaxDim = int64_t(1) << 20;
+constexpr int64_t kFewLongBf16 = 2000000000, kFewLongF32 = 1000000000;  // see few_long
 
 struct FewMat {
     const uint8_t* packed;  // [E][rows x groups] packed groups
@@ -146,7 +147,8 @@ struct FewArgs {
     void* out;  // [T x D]
 };
 
-// Workspace: the routing of the call, then the activations of the pairs as bf16 pieces [pieces][pairs][groups of F x 64].
+// Workspace: the routing of the call, then the activations
+// of the pairs as bf16 pieces [pieces][pairs][groups of F x 64].
 constexpr int64_t few_align(int64_t b) { return (b + 15) / 16 * 16; }
 struct FewPlan {
     int64_t pairs, fp;        // pairs at most, F padded to whole groups
@@ -165,6 +167,34 @@ inline FewPlan few_plan(int64_t T, int64_t k, int64_t F, bool bf16) {
     p.planes = p.pair + few_align(p.pairs * 8);
     p.bytes = p.planes + p.pieces * p.pairs * p.fp * 2;
     return p;
+}
+// Long streams of weights, and many tokens, go through the launches of the full
+// layer: its blocks read 3.6 TB/s and take five tokens an expert at once, where the
+// two launches above reach 3.0 and slow down with an expert's tokens; but they
+// are five (seven with a bf16 call's conversions) and cost 20 to 30 us more for few
+// experts.  By bytes times tokens, measured both ways (us, two launches against
+// the layer's): 128 experts of 7168 x 2048, k = 8: T = 1 63 / 86, 2 103 / 105,
+// 4 199 / 181, 12 543 / 352; 16 of 8192 x 7168, k = 4: T = 1 107 / 121, 2 184 / 171;
+// 128 of 2048 x 768, k = 8: T = 4 50 / 50, 8 75 / 63, 16 136 / 80.
+inline int64_t few_stream(int64_t T, int64_t k, int64_t E, int64_t D, int64_t F, int gate_bits,
+                          int up_bits, int down_bits) {
+    auto group = [](int bits) { return bits == 3 ? 28 : 36; };  // bytes, scale included
+    return std::min(T * k, E) * (F * ((D + kGroup - 1) / kGroup) * (group(gate_bits) + group(up_bits)) +
+                                 D * ((F + kGroup - 1) / kGroup) * group(down_bits));
+}
+inline bool few_long(int64_t T, int64_t k, int64_t E, int64_t D, int64_t F, bool bf16, int gate_bits,
+                     int up_bits, int down_bits) {
+    return D % 128 == 0 && F % 128 == 0 &&
+           T * few_stream(T, k, E, D, F, gate_bits, up_bits, down_bits) >=
+               (bf16 ? kFewLongBf16 : kFewLongF32);
+}
+// The full layer's workspace, after it a bf16 call's tokens and outputs in f32.
+inline int64_t few_long_bytes(int64_t T, int64_t k, int64_t E, int64_t D, int64_t F, bool bf16) {
+    return few_align((int64_t)moe_layer_workspace(T, k, E, D, F)) + (bf16 ? 2 * few_align(T * D * 4) : 0);
+}
+inline int64_t few_workspace(int64_t T, int64_t k, int64_t E, int64_t D, int64_t F, bool bf16) {
+    const int64_t n = few_plan(T, k, F, bf16).bytes;
+    return few_long(T, k, E, D, F, bf16, 4, 4, 4) ? std::max(n, few_long_bytes(T, k, E, D, F, bf16)) : n;
 }
 hipError_t launch_moe_few(const FewArgs& a, void* workspace, hipStream_t s);
 

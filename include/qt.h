@@ -597,15 +597,17 @@ qt_status qt_attn_decode(const void* Q, int64_t ldq, qt_dtype xt, int64_t B, int
 /*
  * qt_moe_layer for a few tokens, in two launches: routing, gate, up and the
  * activation; then the down projection and the sum over a token's experts.
+ * (Long streams of weights with SiLU, D and F multiples of 128, and f32 rows
+ * aligned to 16 bytes go through qt_moe_layer's launches, which are faster there.)
  * Experts, routing, weights and formulas as qt_moe_layer (equal logits: the
  * lower expert first), with either activation of qt_ffn_gated, but
  *   1 <= T <= 16; any D and F up to 2^20; X [T x D] and out [T x D] of type
  *   xt (logits f32), at their elements' alignment; the sum over a token's
- *   experts runs in ascending order of the experts.
+ *   experts runs in a fixed order, the same at every run.
  * Logits of -inf have the weight 0 as long as the token has another one.
  * Roundings: exact codes and inputs, f32 group sums and scales; bf16 calls take
- * the activation as two bf16 pieces (2^-17), f32 calls exactly; one rounding
- * at the end.
+ * the activation as two bf16 pieces (2^-17) or exactly, f32 calls exactly; one
+ * rounding at the end.
  *   packed 16-byte aligned; workspace: qt_moe_decode_workspace_bytes(...)
  *   bytes (16-byte aligned).
  */

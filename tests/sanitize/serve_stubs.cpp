@@ -31,6 +31,9 @@ hipError_t launch_attn_decode(const AttnArgs& a, void*, hipStream_t) {
     if (covers && fits && short_ok) ++qt_stub_launches;
     return hipSuccess;
 }
+size_t moe_layer_workspace(int64_t T, int64_t k, int64_t E, int64_t D, int64_t F) {
+    return (size_t)(T * k * (4 * (D + 3 * F) + 16) + 4 * E + 96);  // of the layer's size
+}
 hipError_t launch_moe_few(const FewArgs&, void*, hipStream_t) {
     ++qt_stub_launches;
     return hipSuccess;

@@ -113,6 +113,41 @@ def test_tokens_do_not_mix(dtype):
     assert not got[2].isfinite().any() and got[5].isnan().any()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_long_streams(dtype):
+    """Enough weights and tokens for the full layer's launches: the same
+    definition, with equal and masked logits among them, from a workspace of the
+    exact size full of NaN; rows at odd addresses and GELU keep the two launches."""
+    T, E, k, D, F = 16, 64, 8, 1024, 1536
+    X, logits, k, w, v = small(T, E, k, D, F, DT[dtype])
+    logits[0] = 0.0
+    logits[1, ::2], logits[1, 1::2] = -0.0, 0.0
+    logits[2, 9:] = -math.inf
+    logits[5:8] = logits[5]
+    need = qt.qt_moe_decode_workspace_bytes(T, k, E, D, F, qt.QT_BF16 if dtype == "bf16" else qt.QT_F32)
+    assert need >= qt.qt_moe_layer_workspace_bytes(T, k, E, D, F)
+    ws = torch.full((need // 4 + 8,), math.nan, device=DEV)
+    out = qt.qt_moe_decode(X, logits, k, *w, workspace=ws[4:4 + need // 4])
+    assert ws[:4].isnan().all() and ws[4 + need // 4:].isnan().all()
+    ref, bound = reference(X, logits, k, *v, "silu", DT[dtype])
+    assert worst(out, ref, bound) <= 1
+    assert torch.equal(out, qt.qt_moe_decode(X, logits, k, *w))
+    if dtype == "f32":
+        assert torch.equal(out, qt.qt_moe_layer(X, logits, k, *w))
+    room = torch.empty(X.numel() + 1, dtype=X.dtype, device=DEV)
+    Xu = room[1:].view(X.shape)
+    Xu.copy_(X)
+    assert worst(qt.qt_moe_decode(Xu, logits, k, *w), ref, bound) <= 1
+    ref, bound = reference(X, logits, k, *v, "gelu", DT[dtype])
+    assert worst(qt.qt_moe_decode(X, logits, k, *w, act="gelu"), ref, bound) <= 1
+    Y = X.clone()
+    Y[2], Y[5, 3] = math.inf, math.nan
+    got = qt.qt_moe_decode(Y, logits, k, *w)
+    keep = [t for t in range(T) if t not in (2, 5)]
+    assert torch.equal(got[keep], out[keep])
+    assert not got[2].isfinite().any() and got[5].isnan().any()
+
+
 def test_agrees_with_the_layer_of_five_launches():
     X, logits, k, w, _ = small(T=9, E=20, k=4, D=256, F=128)
     a = qt.qt_moe_decode(X, logits, k, *w)
