@@ -1,16 +1,18 @@
-// The expert layer for a few tokens (up to 16) in two launches:
+// The expert layer for a few tokens (up to 16), in two launches unless the weights'
+// stream is long:
 //   1. h = act(Wgate_e x_t) * (Wup_e x_t) for every pair of a token and one of
 //      its k experts;
 //   2. out_t = sum_e w_te Wdown_e h_te.
-// The weights' stream is what both cannot do without; unpacking it (3.4 vector
+// The weights' stream is what both cannot do without; unpacking it (2.7 vector
 // instructions a code) bounds the first launch, the latency of a wave's few
 // chunks the second: of 128 experts of 7168 x 2048, int3, k = 8, one token takes
-// 37 + 22 us (2.8 and 2.3 TB/s), twelve (68 experts live) 296 + 174 us (3.0 and
-// 2.6 TB/s).  Codes enter the bf16 matrix cores exactly, each group's products
-// are summed in f32 and scaled by the group's f32 scale.  (Codes as they lie, as
-// FP4 operands next to inputs in FP8 pieces, save the unpacking; but the products
-// are not summed exactly there, f32 outputs came out 1.7e-5 off, and the pieces
-// of the inputs cost what the unpacking did.)
+// 36 + 22 us (2.9 and 2.3 TB/s).  Twelve tokens (68 experts live) took 280 + 174 us,
+// the full layer's launches 238 + 130 and 32 for the small ones: such streams
+// go there (few_long).  Codes enter the bf16 matrix cores exactly, each group's
+// products are summed in f32 and scaled by the group's f32 scale.  (Codes as they
+// lie, as FP4 operands next to inputs in FP8 pieces, save the unpacking; but the
+// products are not summed exactly there, f32 outputs came out 1.7e-5 off, and the
+// pieces of the inputs cost what the unpacking did.)
 //
 // Every block of the first launch routes all tokens by itself (a wave a token: k
 // rounds of a maximum over the wave), which costs less than a launch of its
