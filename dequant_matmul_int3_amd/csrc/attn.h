@@ -31,7 +31,9 @@
 // bf16 calls take int4 codes as u = v + 8: the nibble is the FP8 (E4M3)
 // encoding of u / 512, so a mask and a packed conversion make two operands,
 // and the eightfold sums are taken out again (in the keys' product as its
-// initial value, in the values' at the end).  f32 calls convert to v itself
+// initial value, in the values' at the end: eight times the sum of the very
+// pieces that were multiplied, so that values of code 0 come out as 0 and the
+// pieces' rounding counts |v| times, not v + 8).  f32 calls convert to v itself
 // (over a long flat softmax the offset costs more than f32's accuracy).
 //
 // Measured, this kernel alone: one sequence of 131072 positions, 8 heads of 128
@@ -565,16 +567,22 @@ attn_decode_kernel(const AttnKernelArgs x) {
 #pragma unroll
             for (int gr = 0; gr < G; ++gr) {
                 float y0 = p0 * sv[gr], y1 = p1 * sv[G + gr];
-                if constexpr (VC::kOffset) voff[r][gr] += y0 + y1;
 #pragma unroll
                 for (int k = 0; k < PP; ++k) {
                     uint32_t pair;
                     if (k + 1 < PP) {
+                        const float h0 = __uint_as_float(__float_as_uint(y0) & 0xFFFF0000u);
+                        const float h1 = __uint_as_float(__float_as_uint(y1) & 0xFFFF0000u);
                         pair = high_pair(y0, y1);
-                        y0 -= __uint_as_float(__float_as_uint(y0) & 0xFFFF0000u);
-                        y1 -= __uint_as_float(__float_as_uint(y1) & 0xFFFF0000u);
+                        y0 -= h0;
+                        y1 -= h1;
+                        // the offset's sum takes the pieces, not what they round
+                        if constexpr (VC::kOffset) voff[r][gr] += h0 + h1;
                     } else {
                         pair = bf16_pair(y0, y1);
+                        if constexpr (VC::kOffset)
+                            voff[r][gr] += __uint_as_float(pair << 16) +
+                                           __uint_as_float(pair & 0xFFFF0000u);
                     }
                     *reinterpret_cast<uint32_t*>(&lds[wave].probs[gr][k][4 * r + g][4 * l16]) = pair;
                 }

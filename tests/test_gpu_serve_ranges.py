@@ -1,0 +1,58 @@
+"""The cache and its attention at the ends of their values' ranges: offsets of int4
+values taken out exactly."""
+import pytest
+import torch
+
+import dequant_matmul_int3_amd as qt
+from tests import serve_util as su
+from tests.gpu_util import DEV, say
+from tests.test_gpu_serve import DT, gen
+
+pytestmark = pytest.mark.gpu
+
+
+def filled(P, H, d, kb, vb, k_codes, k_scales, v_codes, v_scales):
+    """A cache of one run of pages holding the codes [n, H, G, 64] and scales [n, H, G]
+    of positions 0 .. n - 1, with a page table of `wide` pages."""
+    n = k_codes.shape[0]
+    pages = -(-n // P)
+    k, v = qt.qt_kv_cache(pages, P, H, d, kb, vb, device=DEV)
+    slots = torch.arange(n, device=DEV)
+    su.store(k, False, slots, k_codes, k_scales)
+    su.store(v, True, slots, v_codes, v_scales)
+    return k, v
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kb,vb", [(4, 4), (8, 4), (8, 8)])
+@pytest.mark.parametrize("d,wide", [(64, 16), (128, 60), (128, 400), (256, 16)])
+@pytest.mark.parametrize("ninth", [True, False])
+def test_codes_of_zero_give_zero(ninth, d, wide, kb, vb, dtype):
+    """Values with the code 0 at every position come out as 0, whatever their group's
+    scales s, 1 <= s < 2.  Scores are equal: a probability is a power of two, a
+    value's weight its scale.  Its first bf16 piece is a multiple of 2^-7; where the
+    scale's ninth bit is set, the rest is 2^-8 at least and the second piece, of eight
+    bits, a multiple of 2^-15.  256 pieces times the offset 8 then stay below 2^24 of
+    their steps of 8 * 2^-15: exact in f32 in any order, and what is taken out again
+    is what was put in.  Otherwise both sums err by U = 2^-24 of 8 sum s, which is
+    below 16 n, for each of at most n / 8 + 200 additions."""
+    say(f"zeros {ninth} d={d} wide={wide} k{kb} v{vb} {dtype}")
+    g, P, H, n = gen(d + wide), 16, 2, 256
+    G = su.groups(d)
+    half = 2 ** (vb - 1)
+    kc = torch.randint(-8, 8, (n, H, G, 64), generator=g, device=DEV)
+    vc = torch.randint(-half, half, (n, H, G, 64), generator=g, device=DEV)
+    vc[..., ::3] = 0
+    vs = 1.0 + torch.rand((n, H, G), generator=g, device=DEV)
+    if ninth:
+        vs = (vs.view(torch.int32) | 1 << 15).view(torch.float32)
+    k, v = filled(P, H, d, kb, vb, kc, torch.ones_like(vs), vc, vs)
+    table = torch.full((1, wide), -1, dtype=torch.int32, device=DEV)
+    table[0, :n // P] = torch.arange(n // P, device=DEV)
+    lens = torch.tensor([n], device=DEV, dtype=torch.int32)
+    Q = torch.zeros(1, 3 * H, d, device=DEV, dtype=DT[dtype])
+    out = qt.qt_attn_decode(Q, k, v, table, lens)
+    at = torch.arange(d, device=DEV) % 64 % 3 == 0
+    exact = ninth or vb == 8 or dtype == "f32"  # no offset there
+    assert out[..., at].abs().max() <= (0.0 if exact else 2 * su.U * (n / 8 + 200) * 16)
+    assert out[..., ~at].any(-1).all()
