@@ -7,7 +7,7 @@
 //
 // A block owns a chunk of one sequence's positions for one key-value head and
 // up to 16 of its query heads; its four or eight waves take tiles of 32 positions in
-// turn, each with an online softmax of its own (running maximum and sum in
+// turn, each with an online softmax of its own (running base and sum in
 // f32), and join them in LDS at the end.  The cache's bytes are read once and
 // bound it; both products run on the bf16 matrix cores, whatever the number of
 // heads, so that the vector instructions per cache value stay below two.
@@ -24,9 +24,10 @@
 // a lane loads eight tokens x four values in one piece (the layout of the
 // pages).
 //
-// The running maximum need not be one: it moves when a score passes it by more
-// than 24 powers of two, which f32 sums and bf16 pieces have room for; else a tile costs
-// one comparison a score.
+// A wave's scores are taken relative to a base: eight powers of two above the
+// largest one at the time, moved when a score passes it; else a tile costs one
+// comparison a score.  No probability is above 1, so that no sum is larger than
+// the formula's own, and the largest is not below 2^-8.
 //
 // bf16 calls take int4 codes as u = v + 8: the nibble is the FP8 (E4M3)
 // encoding of u / 512, so a mask and a packed conversion make two operands,
@@ -55,7 +56,7 @@ struct AttnKernelArgs {
     uint32_t rows, items;       // B heads; rows * splits
     FastDiv page;
     bool q_vec;                 // eight query values may be loaded at once
-    float* part;                // splits > 1: [rows][splits] x (G 64 values, max, sum, 2 unused)
+    float* part;                // splits > 1: [rows][splits] x (G 64 values, base, sum, 2 unused)
 };
 
 hipError_t launch_attn_bf16(const AttnKernelArgs& k, hipStream_t s);
@@ -452,8 +453,8 @@ attn_decode_kernel(const AttnKernelArgs x) {
     }
 
     const float sc = a.scale * 1.4426950408889634f;  // powers of two from here on
-    constexpr float kRoom = 24.0f;  // how far a score may pass the running maximum
-    float m[NR], l[NR];             // head 4 r + g; l: this lane's tokens
+    constexpr float kRoom = 8.0f;  // of a new base above the largest score
+    float m[NR], l[NR];            // head 4 r + g: bases, sums of this lane's tokens
     float voff[NR][G];              // this lane's sum of p sV, where the codes are offset
     f32x4_t o[G][4];                // heads 4 g .. 4 g + 3, values 64 gr + 4 l16 + i
 #pragma unroll
@@ -527,12 +528,13 @@ attn_decode_kernel(const AttnKernelArgs x) {
         }
         bool past = false;
 #pragma unroll
-        for (int r = 0; r < NR; ++r) past |= fmaxf(s[0][r], s[1][r]) > m[r] + kRoom;
+        for (int r = 0; r < NR; ++r) past |= fmaxf(s[0][r], s[1][r]) > m[r];
         if (__any(past)) {
             float al[NR];
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
-                const float mt = fmaxf(m[r], row_max(fmaxf(s[0][r], s[1][r])));
+                const float top = row_max(fmaxf(s[0][r], s[1][r]));
+                const float mt = top > m[r] ? top + kRoom : m[r];
                 al[r] = mt == m[r] ? 1.0f : __builtin_amdgcn_exp2f(m[r] - mt);
                 m[r] = mt;
                 l[r] *= al[r];
@@ -656,7 +658,7 @@ attn_decode_kernel(const AttnKernelArgs x) {
         }
     }
 
-    // ---- the waves' parts: a common maximum, then sums in wave order
+    // ---- the waves' parts: a common base, then sums in wave order
     __shared__ float ml[WAVES][2][16];
     __shared__ float vo[WAVES][G][16];  // what the values' codes are offset by
     __syncthreads();  // every wave is done with its probabilities

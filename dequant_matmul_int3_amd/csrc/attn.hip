@@ -5,7 +5,7 @@
 namespace qt {
 namespace {
 
-// One block per (sequence, query head): the chunks' maxima, sums and value
+// One block per (sequence, query head): the chunks' bases, sums and value
 // sums, 4 values a thread, the chunks dealt to 256 / (W / 4) threads each and
 // joined in LDS, always in the same order.
 template <int G, bool F32>

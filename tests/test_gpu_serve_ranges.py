@@ -1,12 +1,15 @@
 """The cache and its attention at the ends of their values' ranges: offsets of int4
-values taken out exactly."""
+values taken out exactly, values near the largest and the smallest numbers under
+scores that rise."""
+import math
+
 import pytest
 import torch
 
 import dequant_matmul_int3_amd as qt
 from tests import serve_util as su
 from tests.gpu_util import DEV, say
-from tests.test_gpu_serve import DT, gen
+from tests.test_gpu_serve import DT, check, gen, normal
 
 pytestmark = pytest.mark.gpu
 
@@ -56,3 +59,32 @@ def test_codes_of_zero_give_zero(ninth, d, wide, kb, vb, dtype):
     exact = ninth or vb == 8 or dtype == "f32"  # no offset there
     assert out[..., at].abs().max() <= (0.0 if exact else 2 * su.U * (n / 8 + 200) * 16)
     assert out[..., ~at].any(-1).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kb,vb", [(4, 4), (8, 8)])
+@pytest.mark.parametrize("power", [120, 0, -90])
+@pytest.mark.parametrize("d,n", [(64, 250), (128, 600), (128, 3000), (256, 700)])
+def test_values_of_any_magnitude_under_rising_scores(d, n, power, kb, vb, dtype):
+    """Every position's score is above the one's before it, 22 powers of two from
+    the first to the last; values lie around 2^power.  The outputs are means of the
+    values: they exist whatever the sums on the way."""
+    say(f"rising d={d} n={n} 2^{power} k{kb} v{vb} {dtype}")
+    g, P, H = gen(n + power), 32, 2
+    G = su.groups(d)
+    kc = torch.zeros((n, H, G, 64), dtype=torch.long, device=DEV)
+    kc[:, :, 0, 0] = -2
+    ks = torch.zeros((n, H, G), device=DEV)
+    ks[..., 0] = -0.5 * torch.linspace(0, 22 * math.log(2), n, device=DEV)[:, None]
+    vc, vs = su.quantize(normal(g, n, H, d) * 2.0 ** power, vb)
+    k, v = filled(P, H, d, kb, vb, kc, ks, vc, vs)
+    table = torch.arange(-(-n // P), device=DEV, dtype=torch.int32)[None].contiguous()
+    lens = torch.tensor([n], device=DEV, dtype=torch.int32)
+    Q = torch.zeros(1, 2 * H, d, device=DEV, dtype=DT[dtype])
+    Q[..., 0] = 1.0
+    out, lse = qt.qt_attn_decode(Q, k, v, table, lens, scale=1.0, want_lse=True)
+    assert out.isfinite().all()
+    # in units of 2^power, so that the bounds' absolute part stays below them
+    small = 2.0 ** -power
+    unit = (v[0], v[1] * small, vb)
+    check(Q, k, unit, table, lens, ((out.double() * small).to(DT[dtype]), lse), scale=1.0)
