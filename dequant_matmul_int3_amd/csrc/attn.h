@@ -18,9 +18,9 @@
 // heads come in one register of every lane, 8 in two, 16 in four (NR), and the
 // softmax's instructions go by the heads there are.  A lane's two columns of a
 // tile are tokens 2 c and 2 c + 1: its probabilities, times the values' scales
-// and split into two bf16 pieces (three in f32 calls; one alone would add an
-// error as large as the output's own rounding), go to LDS as pairs and come
-// back as the second product's operand, whose other side is the values' codes:
+// and split into three bf16 pieces (exactly: with two, which are 1 to 4 % faster, one
+// bf16 output in 100 to 300 rounded the other way than the exact sum), go to LDS as
+// pairs and come back as the second product's operand, whose other side is the values' codes:
 // a lane loads eight tokens x four values in one piece (the layout of the
 // pages).
 //
@@ -32,9 +32,7 @@
 // bf16 calls take int4 codes as u = v + 8: the nibble is the FP8 (E4M3)
 // encoding of u / 512, so a mask and a packed conversion make two operands,
 // and the eightfold sums are taken out again (in the keys' product as its
-// initial value, in the values' at the end: eight times the sum of the very
-// pieces that were multiplied, so that values of code 0 come out as 0 and the
-// pieces' rounding counts |v| times, not v + 8).  f32 calls convert to v itself
+// initial value, in the values' at the end).  f32 calls convert to v itself
 // (over a long flat softmax the offset costs more than f32's accuracy).
 //
 // Measured, this kernel alone: one sequence of 131072 positions, 8 heads of 128
@@ -231,10 +229,13 @@ struct AttnPlace {
 // A row of probabilities in LDS: 32 tokens of a piece, 16 bytes apart in the banks.
 constexpr int kProbRow = 32 * 2 + 16;
 
+// Pieces of a probability times a value's scale: all of its 24 bits.
+constexpr int kProbPieces = 3;
+
 // A wave's LDS: the probabilities of its tile; at the end its value sums.
-template <int G, int NR, bool F32>
+template <int G, int NR>
 union AttnWaveLds {
-    uint8_t probs[G][F32 ? 3 : 2][4 * NR][kProbRow];
+    uint8_t probs[G][kProbPieces][4 * NR][kProbRow];
     float red[4 * NR][G * kGroup];
 };
 
@@ -246,7 +247,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(attn
 attn_decode_kernel(const AttnKernelArgs x) {
     constexpr int kHop = WAVES * kAttnTile;  // to a wave's next tile
     constexpr int NP = F32 ? 3 : 1;   // pieces of a query value
-    constexpr int PP = F32 ? 3 : 2;   // pieces of a probability
+    constexpr int PP = kProbPieces;
     constexpr int KROW = G * 8 * KB, W = G * kGroup;
     constexpr bool kWide = G > 2;  // registers are short: see there
     using KC = Code<KB, F32>;
@@ -469,7 +470,7 @@ attn_decode_kernel(const AttnKernelArgs x) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[gr][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-    __shared__ __attribute__((aligned(16))) AttnWaveLds<G, NR, F32> lds[WAVES];
+    __shared__ __attribute__((aligned(16))) AttnWaveLds<G, NR> lds[WAVES];
     // scores of the tile in tk: token 2 l16 + h, head 4 r + g
     auto scores = [&](float (&s)[2][NR]) __attribute__((always_inline)) {
 #pragma unroll
@@ -569,22 +570,16 @@ attn_decode_kernel(const AttnKernelArgs x) {
 #pragma unroll
             for (int gr = 0; gr < G; ++gr) {
                 float y0 = p0 * sv[gr], y1 = p1 * sv[G + gr];
+                if constexpr (VC::kOffset) voff[r][gr] += y0 + y1;
 #pragma unroll
                 for (int k = 0; k < PP; ++k) {
                     uint32_t pair;
                     if (k + 1 < PP) {
-                        const float h0 = __uint_as_float(__float_as_uint(y0) & 0xFFFF0000u);
-                        const float h1 = __uint_as_float(__float_as_uint(y1) & 0xFFFF0000u);
                         pair = high_pair(y0, y1);
-                        y0 -= h0;
-                        y1 -= h1;
-                        // the offset's sum takes the pieces, not what they round
-                        if constexpr (VC::kOffset) voff[r][gr] += h0 + h1;
+                        y0 -= __uint_as_float(__float_as_uint(y0) & 0xFFFF0000u);
+                        y1 -= __uint_as_float(__float_as_uint(y1) & 0xFFFF0000u);
                     } else {
                         pair = bf16_pair(y0, y1);
-                        if constexpr (VC::kOffset)
-                            voff[r][gr] += __uint_as_float(pair << 16) +
-                                           __uint_as_float(pair & 0xFFFF0000u);
                     }
                     *reinterpret_cast<uint32_t*>(&lds[wave].probs[gr][k][4 * r + g][4 * l16]) = pair;
                 }

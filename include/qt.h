@@ -577,8 +577,9 @@ qt_status qt_kv_read(const int32_t* slots, int64_t R, const uint8_t* k_codes,
  *   q_heads a multiple of heads, up to 256 per head; B <= 65535; scale finite;
  *   table_pages * page <= 2^31 - 2^16; B * q_heads < 2^24, and fewer than 2^31
  *   blocks of 2048 positions x 16 query heads of a head
- * Rounding: exact codes, scales in f32; bf16 calls take p s as two bf16 pieces
- * (2^-17), f32 calls exactly; f32 sums and softmax, one rounding at the end.
+ * Rounding: exact codes, queries and p s (in bf16 pieces: what of an f32 query or of
+ * p s lies below 2^-126 may be lost, a number of 2^-110 or more is held exactly);
+ * scales, sums and softmax in f32, one rounding at the end.
  *   workspace: qt_attn_decode_workspace_bytes(...) bytes (16-byte aligned; may
  *   be NULL when that size is 0, as for short contexts): long contexts are cut
  *   into chunks that are joined by a second launch.  Chunks depend on the sizes

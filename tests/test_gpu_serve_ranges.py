@@ -10,6 +10,7 @@ import dequant_matmul_int3_amd as qt
 from tests import serve_util as su
 from tests.gpu_util import DEV, say
 from tests.test_gpu_serve import DT, check, gen, normal
+from tests.tune_util import worst
 
 pytestmark = pytest.mark.gpu
 
@@ -29,17 +30,15 @@ def filled(P, H, d, kb, vb, k_codes, k_scales, v_codes, v_scales):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("kb,vb", [(4, 4), (8, 4), (8, 8)])
 @pytest.mark.parametrize("d,wide", [(64, 16), (128, 60), (128, 400), (256, 16)])
-@pytest.mark.parametrize("ninth", [True, False])
-def test_codes_of_zero_give_zero(ninth, d, wide, kb, vb, dtype):
+@pytest.mark.parametrize("short", [True, False])
+def test_codes_of_zero_give_zero(short, d, wide, kb, vb, dtype):
     """Values with the code 0 at every position come out as 0, whatever their group's
     scales s, 1 <= s < 2.  Scores are equal: a probability is a power of two, a
-    value's weight its scale.  Its first bf16 piece is a multiple of 2^-7; where the
-    scale's ninth bit is set, the rest is 2^-8 at least and the second piece, of eight
-    bits, a multiple of 2^-15.  256 pieces times the offset 8 then stay below 2^24 of
-    their steps of 8 * 2^-15: exact in f32 in any order, and what is taken out again
-    is what was put in.  Otherwise both sums err by U = 2^-24 of 8 sum s, which is
-    below 16 n, for each of at most n / 8 + 200 additions."""
-    say(f"zeros {ninth} d={d} wide={wide} k{kb} v{vb} {dtype}")
+    value's weight its scale.  With scales of 16 bits, 256 of them times the offset 8
+    stay below 2^24 of their steps of 8 * 2^-15: exact in f32 in any order, and what
+    is taken out again is what was put in.  Otherwise both sums err by U = 2^-24 of
+    8 sum s, which is below 16 n, for each of at most n / 8 + 200 additions."""
+    say(f"zeros {short} d={d} wide={wide} k{kb} v{vb} {dtype}")
     g, P, H, n = gen(d + wide), 16, 2, 256
     G = su.groups(d)
     half = 2 ** (vb - 1)
@@ -47,8 +46,8 @@ def test_codes_of_zero_give_zero(ninth, d, wide, kb, vb, dtype):
     vc = torch.randint(-half, half, (n, H, G, 64), generator=g, device=DEV)
     vc[..., ::3] = 0
     vs = 1.0 + torch.rand((n, H, G), generator=g, device=DEV)
-    if ninth:
-        vs = (vs.view(torch.int32) | 1 << 15).view(torch.float32)
+    if short:
+        vs = (vs.view(torch.int32) & ~0xFF).view(torch.float32)
     k, v = filled(P, H, d, kb, vb, kc, torch.ones_like(vs), vc, vs)
     table = torch.full((1, wide), -1, dtype=torch.int32, device=DEV)
     table[0, :n // P] = torch.arange(n // P, device=DEV)
@@ -56,7 +55,7 @@ def test_codes_of_zero_give_zero(ninth, d, wide, kb, vb, dtype):
     Q = torch.zeros(1, 3 * H, d, device=DEV, dtype=DT[dtype])
     out = qt.qt_attn_decode(Q, k, v, table, lens)
     at = torch.arange(d, device=DEV) % 64 % 3 == 0
-    exact = ninth or vb == 8 or dtype == "f32"  # no offset there
+    exact = short or vb == 8 or dtype == "f32"  # no offset there
     assert out[..., at].abs().max() <= (0.0 if exact else 2 * su.U * (n / 8 + 200) * 16)
     assert out[..., ~at].any(-1).all()
 
@@ -88,3 +87,28 @@ def test_values_of_any_magnitude_under_rising_scores(d, n, power, kb, vb, dtype)
     small = 2.0 ** -power
     unit = (v[0], v[1] * small, vb)
     check(Q, k, unit, table, lens, ((out.double() * small).to(DT[dtype]), lse), scale=1.0)
+
+
+@pytest.mark.parametrize("kb,vb", [(4, 4), (8, 4), (8, 8)])
+@pytest.mark.parametrize("d,wide", [(64, 16), (128, 60), (128, 400), (200, 16)])
+def test_one_position_is_rounded_once(d, wide, kb, vb):
+    """A sequence of one position: the output is s v, rounded to bf16 once.  The
+    probability is a power of two; the product's three terms and, at 4 bits, what the
+    offset 8 takes out leave 4 U of 15 s (8 bits: of |s v|) besides, U = 2^-24, the
+    quotient 2 U of |s v|."""
+    say(f"one position d={d} wide={wide} k{kb} v{vb}")
+    g, P, H, B = gen(d + wide), 16, 4, 40
+    G, half = su.groups(d), 2 ** (vb - 1)
+    kc = torch.randint(-8, 8, (B * P, H, G, 64), generator=g, device=DEV)
+    vc = torch.randint(-half, half, (B * P, H, G, 64), generator=g, device=DEV)
+    vs = torch.exp(3 * normal(g, B * P, H, G))
+    k, v = filled(P, H, d, kb, vb, kc, normal(g, B * P, H, G), vc, vs)
+    table = torch.full((B, wide), -1, dtype=torch.int32, device=DEV)
+    table[:, 0] = torch.arange(B, device=DEV)
+    lens = torch.ones(B, device=DEV, dtype=torch.int32)
+    out = qt.qt_attn_decode(normal(g, B, 2 * H, d).bfloat16(), k, v, table, lens)
+    ref = su.value(vc, vs, d)[::P].repeat_interleave(2, 1)
+    step = vs[::P].double().repeat_interleave(64, -1)[..., :d].repeat_interleave(2, 1)
+    half_ulp = torch.exp2(torch.floor(torch.log2(ref.abs().clamp_min(1e-30))) - 8)
+    bound = half_ulp + su.U * (4 * (15 * step if vb == 4 else ref.abs()) + 2 * ref.abs())
+    assert worst(out, ref, bound) <= 1
