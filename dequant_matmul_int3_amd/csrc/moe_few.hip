@@ -514,17 +514,11 @@ moe_few_up_kernel(const FewKernelArgs x) {
             const int64_t at =
                 (int64_t)(first + m) * (x.GF * 64) + f0 + (c & 8) + place_of(c & 7);
             const int64_t plane = (int64_t)x.pairs * x.GF * 64;
-            if constexpr (BF16) {
-                const float hi = __uint_as_float(__float_as_uint(h) & 0xFFFF0000u);
-                x.planes[at] = (uint16_t)(__float_as_uint(hi) >> 16);
-                x.planes[plane + at] = __builtin_bit_cast(uint16_t, (__bf16)(h - hi));
-            } else {
-                uint32_t b0, b1, b2;
-                split3(h, b0, b1, b2);
-                x.planes[at] = (uint16_t)b0;
-                x.planes[plane + at] = (uint16_t)b1;
-                x.planes[2 * plane + at] = (uint16_t)b2;
-            }
+            uint32_t b0, b1, b2;
+            split3(h, b0, b1, b2);
+            x.planes[at] = (uint16_t)b0;
+            x.planes[plane + at] = (uint16_t)b1;
+            x.planes[2 * plane + at] = (uint16_t)b2;
         }
         lds_barrier();  // the sums are read
     };
@@ -555,7 +549,7 @@ moe_few_up_kernel(const FewKernelArgs x) {
 }
 
 // Second launch: a block of 8 waves owns 16 outputs of every token and walks
-// all active experts; its waves take chunks of four groups in turn and add each
+// all active experts; its waves take chunks of eight groups in turn and add each
 // chunk's products, times the pairs' weights, to sums of their own in LDS, which
 // are added at the end in wave order.  Rows of the matrix operand are the
 // pieces of an expert's tokens.
@@ -563,16 +557,15 @@ moe_few_up_kernel(const FewKernelArgs x) {
 // Weights are loaded two chunks ahead and activations one; a chunk's expert and
 // pairs, the addresses of both, come from LDS.
 //
-// ROWS: operand rows of an expert that are staged in LDS; an expert with more
-// tokens reads them from the caches.
-template <int DB, bool BF16, int ROWS>
+// An expert's rows are staged in LDS where it has one token (as many as leave two
+// blocks a CU); one with more tokens reads them from the caches.
+template <int DB, bool BF16>
 __global__ __launch_bounds__(64 * kDownWaves) __attribute__((amdgpu_waves_per_eu(4))) void
 moe_few_down_kernel(const FewKernelArgs x) {
     constexpr int W = kDownWaves, CG = kDownCG;
-    constexpr int NP = BF16 ? 2 : 3;   // pieces of an activation
-    constexpr int PT = BF16 ? 2 : 4;   // rows of a token: its pieces (and one unused)
-    constexpr int RT = 16 / PT;        // tokens of a row tile
-    constexpr int NW = 4 / PT;         // tokens of a lane's four result rows
+    constexpr int NP = kFewPieces;  // of an activation
+    constexpr int PT = 4;           // rows of a token: its pieces and one unused
+    constexpr int RT = 16 / PT;     // tokens of a row tile: a lane's result rows are one's
     constexpr int kRowPitch = CG * 128 + 16;
     using TD = Tile<DB, CG>;
     constexpr int NL = TD::kPieces / 64;
@@ -581,7 +574,7 @@ moe_few_down_kernel(const FewKernelArgs x) {
     constexpr int kPairs = kFewMaxTokens * kFewMaxTopK;
     struct Own {
         uint8_t w[16 * TD::kPitch];
-        uint8_t h[ROWS * kRowPitch];
+        uint8_t h[NP * kRowPitch];
         float s[CG][16];
     };
     __shared__ __attribute__((aligned(16))) Own own[W];
@@ -667,16 +660,16 @@ moe_few_down_kernel(const FewKernelArgs x) {
         return x.planes + r % NP * plane +
                ((int64_t)min(first + p0 + r / NP, end - 1) * G + t.c * CG) * 64;
     };
-    auto load_h = [&](const At& t, u32x4_t (&h)[ROWS]) __attribute__((always_inline)) {
+    auto load_h = [&](const At& t, u32x4_t (&h)[NP]) __attribute__((always_inline)) {
         // a lane's 16 bytes of each row (past the row its last group's)
         const int at = min(lane, 8 * (G - t.c * CG) - 1) * 8;
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r)
+        for (int r = 0; r < NP; ++r)
             h[r] = *reinterpret_cast<const u32x4_t*>(row_of(t, 0, r) + at);
     };
     if (wave < units) {
         Weights w[3];
-        u32x4_t h[ROWS];
+        u32x4_t h[NP];
         At now{0, wave};
         while (now.c >= nchunk) {
             now.c -= nchunk;
@@ -700,13 +693,13 @@ moe_few_down_kernel(const FewKernelArgs x) {
             o.s[lane & 3][lane >> 2] = w0.s[0] * kUnit<DB>;
             o.s[(lane & 3) + 4][lane >> 2] = w0.s[1] * kUnit<DB>;
 #pragma unroll
-            for (int r = 0; r < ROWS; ++r)
+            for (int r = 0; r < NP; ++r)
                 *reinterpret_cast<u32x4_t*>(o.h + r * kRowPitch + 16 * lane) = h[r];
             load_h(next, h);
             lds_wave_sync();
             // this lane's operand row: piece of a token, a valid one past them
             const int tok = l16 / PT, pc = min(l16 % PT, NP - 1);
-            auto product = [&](const uint8_t* hp, int pitch) __attribute__((always_inline)) {
+            auto product = [&](const uint8_t* hp) __attribute__((always_inline)) {
                 f32x4_t part = {0.f, 0.f, 0.f, 0.f};
                 const int live = min(CG, G - now.c * CG);
 #pragma unroll
@@ -719,7 +712,7 @@ moe_few_down_kernel(const FewKernelArgs x) {
                     const float s = o.s[j][l16];
                     const f32x4_t y = mma(p[1], wh, mma(p[0], wl, f32x4_t{0.f, 0.f, 0.f, 0.f}));
 #pragma unroll
-                    for (int r = 0; r < (BF16 ? 4 : 3); ++r)
+                    for (int r = 0; r < NP; ++r)
                         part[r] = __builtin_fmaf(s, y[r], part[r]);
                 }
                 return part;
@@ -727,25 +720,18 @@ moe_few_down_kernel(const FewKernelArgs x) {
             // the products of the tokens from p0 on, to this wave's sums
             auto add = [&](int p0, const f32x4_t& part) __attribute__((always_inline)) {
                 lds_wave_sync();  // another lane may have added to this token before
-#pragma unroll
-                for (int z = 0; z < NW; ++z) {
-                    const int p = first + p0 + NW * h4 + z;
-                    if (p < end) {
-                        const float y = BF16 ? part[2 * z] + part[2 * z + 1]
-                                             : (part[0] + part[1]) + part[2];
-                        float& sum = sums[wave][token[p]][l16];
-                        sum = __builtin_fmaf(weight[p], y, sum);
-                    }
+                const int p = first + p0 + h4;
+                if (p < end) {
+                    float& sum = sums[wave][token[p]][l16];
+                    sum = __builtin_fmaf(weight[p], (part[0] + part[1]) + part[2], sum);
                 }
             };
-            if ((end - first) * NP <= ROWS) {
-                const int r = min(tok, end - first - 1) * NP + pc;
-                add(0, product(o.h + r * kRowPitch, kRowPitch));
+            if (end - first == 1) {
+                add(0, product(o.h + pc * kRowPitch));
             } else {
                 for (int p0 = 0; p0 < end - first; p0 += RT)
                     add(p0, product(reinterpret_cast<const uint8_t*>(
-                                        row_of(now, p0, min(tok, end - first - 1 - p0) * NP + pc)),
-                                    0));
+                                        row_of(now, p0, min(tok, end - first - 1 - p0) * NP + pc))));
             }
             now = next;
             next = then;
@@ -799,12 +785,7 @@ hipError_t up_bits(const FewKernelArgs& x, hipStream_t s) {
 template <int DB, bool BF16>
 hipError_t run_down(const FewKernelArgs& x, hipStream_t s) {
     const unsigned grid = (unsigned)((x.a.D + 15) / 16);
-    // one token's rows, or as many as leave two blocks a CU
-    constexpr int kOne = BF16 ? 2 : 3, kMore = DB == 3 ? (BF16 ? 4 : 3) : kOne;
-    if (x.a.T == 1)
-        moe_few_down_kernel<DB, BF16, kOne><<<grid, 64 * kDownWaves, 0, s>>>(x);
-    else
-        moe_few_down_kernel<DB, BF16, kMore><<<grid, 64 * kDownWaves, 0, s>>>(x);
+    moe_few_down_kernel<DB, BF16><<<grid, 64 * kDownWaves, 0, s>>>(x);
     return hipGetLastError();
 }
 
@@ -850,7 +831,7 @@ hipError_t launch_moe_few(const FewArgs& a, void* workspace, hipStream_t s) {
     if (wide_rows && a.act == 0 &&
         few_long(a.T, a.k, a.E, a.D, a.F, a.bf16, a.gate.bits, a.up.bits, a.down.bits))
         return run_long(a, workspace, s);
-    const FewPlan p = few_plan(a.T, a.k, a.F, a.bf16);
+    const FewPlan p = few_plan(a.T, a.k, a.F);
     uint8_t* w = static_cast<uint8_t*>(workspace);
     FewKernelArgs x;
     x.a = a;

@@ -147,25 +147,24 @@ struct FewArgs {
     void* out;  // [T x D]
 };
 
-// Workspace: the routing of the call, then the activations
-// of the pairs as bf16 pieces [pieces][pairs][groups of F x 64].
+// Workspace: the routing of the call, then the activations of the pairs as three bf16
+// pieces, all of their 24 bits: [pieces][pairs][groups of F x 64].
+constexpr int kFewPieces = 3;
 constexpr int64_t few_align(int64_t b) { return (b + 15) / 16 * 16; }
 struct FewPlan {
     int64_t pairs, fp;        // pairs at most, F padded to whole groups
-    int pieces;               // of an activation: two (bf16 calls) or three
     int64_t pair, planes;     // offsets of the parts in bytes; the experts are first
     int64_t bytes;
 };
-inline FewPlan few_plan(int64_t T, int64_t k, int64_t F, bool bf16) {
+inline FewPlan few_plan(int64_t T, int64_t k, int64_t F) {
     FewPlan p;
     p.pairs = T * k;
     p.fp = (F + kGroup - 1) / kGroup * kGroup;
-    p.pieces = bf16 ? 2 : 3;
     // the number of active experts (16 bytes) and each one's expert and first
     // pair; then the pairs' tokens and weights
     p.pair = 16 + few_align(p.pairs * 4);
     p.planes = p.pair + few_align(p.pairs * 8);
-    p.bytes = p.planes + p.pieces * p.pairs * p.fp * 2;
+    p.bytes = p.planes + kFewPieces * p.pairs * p.fp * 2;
     return p;
 }
 // Long streams of weights, and many tokens, go through the launches of the full
@@ -193,7 +192,7 @@ inline int64_t few_long_bytes(int64_t T, int64_t k, int64_t E, int64_t D, int64_
     return few_align((int64_t)moe_layer_workspace(T, k, E, D, F)) + (bf16 ? 2 * few_align(T * D * 4) : 0);
 }
 inline int64_t few_workspace(int64_t T, int64_t k, int64_t E, int64_t D, int64_t F, bool bf16) {
-    const int64_t n = few_plan(T, k, F, bf16).bytes;
+    const int64_t n = few_plan(T, k, F).bytes;
     return few_long(T, k, E, D, F, bf16, 4, 4, 4) ? std::max(n, few_long_bytes(T, k, E, D, F, bf16)) : n;
 }
 hipError_t launch_moe_few(const FewArgs& a, void* workspace, hipStream_t s);

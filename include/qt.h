@@ -606,9 +606,9 @@ qt_status qt_attn_decode(const void* Q, int64_t ldq, qt_dtype xt, int64_t B, int
  *   xt (logits f32), at their elements' alignment; the sum over a token's
  *   experts runs in a fixed order, the same at every run.
  * Logits of -inf have the weight 0 as long as the token has another one.
- * Roundings: exact codes and inputs, f32 group sums and scales; bf16 calls take
- * the activation as two bf16 pieces (2^-17) or exactly, f32 calls exactly; one
- * rounding at the end.
+ * Roundings: exact codes, inputs and activations (in bf16 pieces: what of them lies
+ * below 2^-126 may be lost, a number of 2^-110 or more is held exactly), f32 group
+ * sums and scales, one rounding at the end.
  *   packed 16-byte aligned; workspace: qt_moe_decode_workspace_bytes(...)
  *   bytes (16-byte aligned).
  */
