@@ -156,7 +156,9 @@ qt_status qt_attn_decode(const void* Q, int64_t ldq, qt_dtype xt, int64_t B, int
         !attn_sizes_ok(B, q_heads, heads, dim, table_pages, page, window) ||
         !ld_ok(ldq, q_heads * dim))
         return QT_ERR_SHAPE;
-    if (!kv_bits_ok(k_bits) || !kv_bits_ok(v_bits) || !std::isfinite(scale)) return QT_ERR_ARG;
+    // the kernel takes powers of two of scale * log2 e, which has to be a number
+    if (!kv_bits_ok(k_bits) || !kv_bits_ok(v_bits) || !(std::fabs(scale) <= 0x1p127f))
+        return QT_ERR_ARG;
     const size_t need =
         qt_attn_decode_workspace_bytes(B, q_heads, heads, dim, table_pages, page, window);
     if (need && (!workspace || ws_bytes < need)) return QT_ERR_WORKSPACE;

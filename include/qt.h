@@ -574,7 +574,7 @@ qt_status qt_kv_read(const int32_t* slots, int64_t R, const uint8_t* k_codes,
  *   Q [B x q_heads x dim] of type xt, sequences ldq >= q_heads*dim elements
  *   apart; page_table [B x table_pages] int32, lens [B] int32;
  *   out [B x q_heads x dim] of type xt; lse [B x q_heads] f32 or NULL
- *   q_heads a multiple of heads, up to 256 per head; B <= 65535; scale finite;
+ *   q_heads a multiple of heads, up to 256 per head; B <= 65535; |scale| <= 2^127;
  *   table_pages * page <= 2^31 - 2^16; B * q_heads < 2^24, and fewer than 2^31
  *   blocks of 2048 positions x 16 query heads of a head
  * Rounding: exact codes, queries and p s (in bf16 pieces: what of an f32 query or of
