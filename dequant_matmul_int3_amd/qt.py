@@ -840,36 +840,40 @@ def qt_kv_write(K, V, slots, k, v, stream=None):
                              n_pages, page, heads, d, _raw_stream(dev)), "qt_kv_write")
 
 
-def qt_kv_read(slots, k, v, dim: int, dtype=torch.bfloat16, K=None, V=None, stream=None):
-    """-> (K, V) [R, heads, dim] of the slots [R] int32 of the cache, in dtype
-    (f32 or bf16); slots outside the cache give zeros."""
+def qt_kv_read(slots, k, v, dim: int, dtype=None, K=None, V=None, stream=None,
+               parts: str = "kv"):
+    """-> (K, V) [R, heads, dim] of the slots [R] int32 of the cache, in dtype (f32
+    or bf16; None: the type of a K or V that is given, bf16 without one); slots outside
+    the cache give zeros.  parts "k" or "v" reads that one alone, the other is None."""
+    if parts not in ("kv", "k", "v"):
+        raise ValueError("parts must be 'kv', 'k' or 'v'")
+    if (K is not None and parts == "v") or (V is not None and parts == "k"):
+        raise ValueError("a tensor is given for a part that is not read")
     dev = slots.device
     n_pages, heads, page = _kv(k, v, dim, slots.get_device())
     if slots.dim() != 1 or slots.dtype != torch.int32:
         raise ValueError("slots must be [R] of torch.int32")
     shape = (slots.shape[0], heads, dim)
+    if dtype is None:
+        dtype = K.dtype if K is not None else V.dtype if V is not None else torch.bfloat16
     if not _current(dev, stream):
         with _on(dev, stream):
-            return qt_kv_read(slots, k, v, dim, dtype, K, V)
+            return qt_kv_read(slots, k, v, dim, dtype, K, V, None, parts)
     kc, ks, kb = k
     vc, vs, vb = v
     _there(dev.index, slots)
-    if K is None and V is None:
+    for t, what in ((K, "K"), (V, "V")):
+        if t is not None:
+            _is(t, shape, dtype, what)
+            _there(dev.index, t)
+    if K is None and parts != "v":
         K = torch.empty(shape, dtype=dtype, device=dev)
-        V = torch.empty_like(K)
-        xt = _xtype(K, "K")
-    else:
-        if K is None:
-            K = torch.empty(shape, dtype=dtype, device=dev)
-        if V is None:
-            V = torch.empty(shape, dtype=K.dtype, device=dev)
-        xt = _xtype(K, "K")
-        _is(K, shape, K.dtype, "K")
-        _is(V, shape, K.dtype, "V")
-        _there(dev.index, K, V)
+    if V is None and parts != "k":
+        V = torch.empty(shape, dtype=dtype, device=dev)
+    xt = _xtype(V if K is None else K, "K and V")
     _check(lib().qt_kv_read(slots.data_ptr(), shape[0], kc.data_ptr(), ks.data_ptr(), kb,
                             vc.data_ptr(), vs.data_ptr(), vb, n_pages, page, heads, dim,
-                            K.data_ptr(), V.data_ptr(), xt, _raw_stream(dev)), "qt_kv_read")
+                            _adr(K), _adr(V), xt, _raw_stream(dev)), "qt_kv_read")
     return K, V
 
 

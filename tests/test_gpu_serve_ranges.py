@@ -112,3 +112,33 @@ def test_one_position_is_rounded_once(d, wide, kb, vb):
     half_ulp = torch.exp2(torch.floor(torch.log2(ref.abs().clamp_min(1e-30))) - 8)
     bound = half_ulp + su.U * (4 * (15 * step if vb == 4 else ref.abs()) + 2 * ref.abs())
     assert worst(out, ref, bound) <= 1
+
+
+def test_one_part_is_read_alone():
+    """Keys or values alone, and given tensors of either type beside no other."""
+    g, R, H, d = gen(6), 70, 2, 96
+    k, v = qt.qt_kv_cache(3, 32, H, d, 8, 4, device=DEV)
+    x = normal(g, 96, H, d)
+    qt.qt_kv_write(x, x, torch.arange(96, device=DEV, dtype=torch.int32), k, v)
+    slots = torch.randint(-3, 99, (R,), generator=g, device=DEV, dtype=torch.int32)
+    both = qt.qt_kv_read(slots, k, v, d, dtype=torch.float32)
+    K, none = qt.qt_kv_read(slots, k, v, d, dtype=torch.float32, parts="k")
+    assert none is None and torch.equal(K, both[0])
+    none, V = qt.qt_kv_read(slots, k, v, d, parts="v")
+    assert none is None and torch.equal(V, both[1].bfloat16())
+    for dtype in (torch.float32, torch.bfloat16):
+        for i in (0, 1):
+            mine = torch.full((R, H, d), math.nan, device=DEV, dtype=dtype)
+            got = qt.qt_kv_read(slots, k, v, d, **{"KV"[i]: mine})
+            assert got[i] is mine
+            assert all(torch.equal(a, b.to(dtype)) for a, b in zip(got, both))
+            mine.fill_(math.nan)
+            got = qt.qt_kv_read(slots, k, v, d, parts="kv"[i], **{"KV"[i]: mine},
+                                stream=torch.cuda.current_stream())
+            assert got[i] is mine and got[1 - i] is None and torch.equal(mine, both[i].to(dtype))
+    with pytest.raises(ValueError, match="not read"):
+        qt.qt_kv_read(slots, k, v, d, K=mine, parts="v")
+    with pytest.raises(ValueError, match="parts"):
+        qt.qt_kv_read(slots, k, v, d, parts="")
+    with pytest.raises(ValueError, match="V must be"):
+        qt.qt_kv_read(slots, k, v, d, K=mine, V=mine.float())
