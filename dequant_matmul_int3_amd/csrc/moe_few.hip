@@ -829,7 +829,7 @@ hipError_t launch_moe_few(const FewArgs& a, void* workspace, hipStream_t s) {
     // the full layer takes SiLU, and f32 rows aligned to 16 bytes
     const bool wide_rows = a.bf16 || ((reinterpret_cast<uintptr_t>(a.X) | reinterpret_cast<uintptr_t>(a.out)) & 15) == 0;
     if (wide_rows && a.act == 0 &&
-        few_long(a.T, a.k, a.E, a.D, a.F, a.bf16, a.gate.bits, a.up.bits, a.down.bits))
+        few_long(a.T, a.k, a.E, a.D, a.F, a.gate.bits, a.up.bits, a.down.bits))
         return run_long(a, workspace, s);
     const FewPlan p = few_plan(a.T, a.k, a.F);
     uint8_t* w = static_cast<uint8_t*>(workspace);

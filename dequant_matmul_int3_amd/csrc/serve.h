@@ -130,7 +130,7 @@ constexpr int kFewMaxTokens = 16;
 constexpr int kFewMaxTopK = 32;
 constexpr int kFewMaxExperts = 512;
 constexpr int64_t kFewMaxDim = int64_t(1) << 20;
-constexpr int64_t kFewLongBf16 = 2000000000, kFewLongF32 = 1000000000;  // see few_long
+constexpr int64_t kFewLong = 1000000000;  // see few_long
 
 struct FewMat {
     const uint8_t* packed;  // [E][rows x groups] packed groups
@@ -170,22 +170,35 @@ inline FewPlan few_plan(int64_t T, int64_t k, int64_t F) {
 // Long streams of weights, and many tokens, go through the launches of the full
 // layer: its blocks read 3.6 TB/s and take five tokens an expert at once, where the
 // two launches above reach 3.0 and slow down with an expert's tokens; but they
-// are five (seven with a bf16 call's conversions) and cost 20 to 30 us more for few
-// experts.  By bytes times tokens, measured both ways (us, two launches against
-// the layer's): 128 experts of 7168 x 2048, k = 8: T = 1 63 / 86, 2 103 / 105,
-// 4 199 / 181, 12 543 / 352; 16 of 8192 x 7168, k = 4: T = 1 107 / 121, 2 184 / 171;
-// 128 of 2048 x 768, k = 8: T = 4 50 / 50, 8 75 / 63, 16 136 / 80.
+// are five (seven with a bf16 call's conversions) and cost 20 to 35 us more for few
+// experts.  Measured by bytes times tokens (int3, us a call: bf16 through the two
+// launches / the layer's with its conversions; f32 likewise, the two launches of large
+// ones with rows off 16 bytes, which cost them up to a tenth):
+//   10^9   experts, k             T   bf16         f32
+//   0.07   128 of 2048 x 768, 8   2    27 /  47     27 /  42
+//   0.26   the same               4    44 /  51     46 /  45
+//   0.36   64 of 2048 x 1408, 6   4    47 /  52     48 /  47
+//   0.62   128 of 7168 x 2048, 8  2    90 / 106     99 / 101
+//   0.62   8 of 4096 x 14336, 2   2    80 / 116     84 / 112
+//   1.06   128 of 2048 x 768, 8   8    72 /  63     88 /  58
+//   1.23   16 of 8192 x 7168, 4   2   169 / 172    206 / 167
+//   1.45   64 of 2048 x 1408, 6   8    80 /  65    101 /  62
+//   2.47   128 of 7168 x 2048, 8  4   172 / 174    215 / 170
+//   2.47   8 of 4096 x 14336, 2   4   159 / 159    174 / 154
+//   2.77   16 of 8192 x 7168, 4   3   225 / 216    277 / 211
+//   22.2   128 of 7168 x 2048, 8  12  419 / 343    698 / 346
+// The layer takes SiLU, widths that are multiples of 128 and f32 rows aligned to 16
+// bytes; other calls pay the difference above.
 inline int64_t few_stream(int64_t T, int64_t k, int64_t E, int64_t D, int64_t F, int gate_bits,
                           int up_bits, int down_bits) {
     auto group = [](int bits) { return bits == 3 ? 28 : 36; };  // bytes, scale included
     return std::min(T * k, E) * (F * ((D + kGroup - 1) / kGroup) * (group(gate_bits) + group(up_bits)) +
                                  D * ((F + kGroup - 1) / kGroup) * group(down_bits));
 }
-inline bool few_long(int64_t T, int64_t k, int64_t E, int64_t D, int64_t F, bool bf16, int gate_bits,
+inline bool few_long(int64_t T, int64_t k, int64_t E, int64_t D, int64_t F, int gate_bits,
                      int up_bits, int down_bits) {
     return D % 128 == 0 && F % 128 == 0 &&
-           T * few_stream(T, k, E, D, F, gate_bits, up_bits, down_bits) >=
-               (bf16 ? kFewLongBf16 : kFewLongF32);
+           T * few_stream(T, k, E, D, F, gate_bits, up_bits, down_bits) >= kFewLong;
 }
 // The full layer's workspace, after it a bf16 call's tokens and outputs in f32.
 inline int64_t few_long_bytes(int64_t T, int64_t k, int64_t E, int64_t D, int64_t F, bool bf16) {
@@ -193,7 +206,7 @@ inline int64_t few_long_bytes(int64_t T, int64_t k, int64_t E, int64_t D, int64_
 }
 inline int64_t few_workspace(int64_t T, int64_t k, int64_t E, int64_t D, int64_t F, bool bf16) {
     const int64_t n = few_plan(T, k, F).bytes;
-    return few_long(T, k, E, D, F, bf16, 4, 4, 4) ? std::max(n, few_long_bytes(T, k, E, D, F, bf16)) : n;
+    return few_long(T, k, E, D, F, 4, 4, 4) ? std::max(n, few_long_bytes(T, k, E, D, F, bf16)) : n;
 }
 hipError_t launch_moe_few(const FewArgs& a, void* workspace, hipStream_t s);
 

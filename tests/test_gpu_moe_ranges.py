@@ -47,3 +47,20 @@ def test_activations_are_held_exactly(E, bits, act, dtype):
     if dtype == "bf16":
         bound = bound + torch.exp2(torch.floor(torch.log2(ref.abs().clamp_min(1e-30))) - 8)
     assert worst(out, ref, bound) <= 1
+
+
+@pytest.mark.parametrize("T,E,k,D,F", [(16, 48, 8, 1024, 1536), (8, 64, 6, 2048, 1408)])
+def test_bf16_calls_take_the_faster_launches(T, E, k, D, F):
+    """Streams of 1 to 2 * 10^9 bytes times tokens, where the full layer's launches are
+    the faster ones of either type: the layer's outputs, rounded once."""
+    say(f"long bf16 T={T} E={E} k={k} D={D} F={F}")
+    gen = torch.Generator(device=DEV).manual_seed(T)
+    w = []
+    for rows, cols in ((F, D), (F, D), (D, F)):
+        n = rows * (cols // 64)
+        packed = torch.randint(0, 256, (E, 24 * n), generator=gen, device=DEV, dtype=torch.uint8)
+        w.append((packed, 0.01 + 0.01 * torch.rand((E, rows, cols // 64), generator=gen, device=DEV), 3))
+    X = torch.randn((T, D), generator=gen, device=DEV).bfloat16()
+    logits = torch.randn((T, E), generator=gen, device=DEV)
+    layer = qt.qt_moe_layer(X.float(), logits, k, *w).bfloat16()
+    assert torch.equal(qt.qt_moe_decode(X, logits, k, *w), layer)
