@@ -74,23 +74,12 @@ __device__ __forceinline__ void dequant_quarter(uint32_t L, uint32_t hw, uint32_
 #undef QT_CV
 }
 
-// v/16 of the two's-complement nibble in the low four bits of byte B of t.
+// v/16 of the two's-complement nibble in the low four bits of byte B of t.  The
+// conversion is the compiler's: in inline assembly it would miss the waits kept between
+// a matrix instruction and the next write of its accumulator's registers.
 template <int B>
 __device__ __forceinline__ float nib(uint32_t t) {
-    float r;
-    if constexpr (B == 0)
-        asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_0"
-            : "=v"(r) : "v"(t));
-    else if constexpr (B == 1)
-        asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_1"
-            : "=v"(r) : "v"(t));
-    else if constexpr (B == 2)
-        asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_2"
-            : "=v"(r) : "v"(t));
-    else
-        asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_3"
-            : "=v"(r) : "v"(t));
-    return r;
+    return __builtin_amdgcn_cvt_off_f32_i4((t >> (8 * B)) & 0xFFu);
 }
 
 // bf16 pair [f(a) | f(b) << 16] of two f32 values with zero low halves.
@@ -101,8 +90,10 @@ __device__ __forceinline__ uint32_t hi_pair(float a, float b) {
 // One int4 word (code n of the word in nibble n, u = v + 8) -> its 8 codes
 // as v/16 in bf16, natural order.  u ^ 8 is the two's-complement nibble of v.
 __device__ __forceinline__ u32x4_t dequant_word_i4(uint32_t w) {
-    const uint32_t t = w ^ 0x88888888u;  // even codes: low nibble of each byte
-    const uint32_t h = t >> 4;           // odd codes: low nibble of each byte
+    uint32_t t = w ^ 0x88888888u;  // even codes: low nibble of each byte
+    asm("" : "+v"(t));             // one exclusive or and one shift for all bytes, which are selected
+    uint32_t h = t >> 4;           // odd codes: low nibble of each byte
+    asm("" : "+v"(h));
     return u32x4_t{hi_pair(nib<0>(t), nib<0>(h)), hi_pair(nib<1>(t), nib<1>(h)),
                    hi_pair(nib<2>(t), nib<2>(h)), hi_pair(nib<3>(t), nib<3>(h))};
 }

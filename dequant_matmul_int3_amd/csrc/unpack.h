@@ -44,27 +44,19 @@ __device__ __forceinline__ void unpack_i3(uint32_t L, uint32_t hw, uint32_t hsel
 }
 __device__ __forceinline__ uint32_t high_sel(int q) { return (q & 1) ? 0x0C030C02u : 0x0C010C00u; }
 
-// v/16 of the two's-complement nibble in the low four bits of byte B of t.
+// v/16 of the two's-complement nibble in the low four bits of byte B of t.  The
+// conversion is the compiler's: in inline assembly it would miss the waits kept between
+// a matrix instruction and the next write of its accumulator's registers.
 template <int B>
 __device__ __forceinline__ float nibble(uint32_t t) {
-    float r;
-    if constexpr (B == 0)
-        asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_0"
-            : "=v"(r) : "v"(t));
-    else if constexpr (B == 1)
-        asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_1"
-            : "=v"(r) : "v"(t));
-    else if constexpr (B == 2)
-        asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_2"
-            : "=v"(r) : "v"(t));
-    else
-        asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_3"
-            : "=v"(r) : "v"(t));
-    return r;
+    return __builtin_amdgcn_cvt_off_f32_i4((t >> (8 * B)) & 0xFFu);
 }
 // The eight codes of an int4 word as v/16, in order.
 __device__ __forceinline__ void unpack_i4(uint32_t w, float (&v)[8]) {
-    const uint32_t t = w ^ 0x88888888u, h = t >> 4;
+    uint32_t t = w ^ 0x88888888u;
+    asm("" : "+v"(t));  // one exclusive or and one shift for all bytes, which are selected
+    uint32_t h = t >> 4;
+    asm("" : "+v"(h));
     v[0] = nibble<0>(t);
     v[1] = nibble<0>(h);
     v[2] = nibble<1>(t);
