@@ -2,9 +2,10 @@
 // read back.
 //
 // Per (token, head, group of 64): m = the value of largest magnitude (the
-// first of equals), s = -m / h with h = 8 or 128 (a power of two: exact), v =
-// clamp(nearest integer to x / s, ties to even, -h, h - 1).  m itself takes
-// the code -h exactly.
+// first of equals), s = -m / h with h = 8 or 128 (a power of two: exact but where s
+// is below the normal numbers, where it is rounded to the nearest), v =
+// clamp(nearest integer to x / s, ties to even, -h, h - 1).  Where s is exact m
+// itself takes the code -h.
 //
 // Layout of a (page, head): key rows are one token after the other, int4 as
 // the int4-g64 format (nibble j % 2 of byte j / 2), int8 byte j = v + 128.
@@ -67,7 +68,7 @@ __device__ __forceinline__ float group_scale(const float (&x)[4], int c, int hal
     who = max16(who);
     const float m = __uint_as_float(best);
     if (best >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
-    const float s = m / (float)half;  // exact: a power of two
+    const float s = m / (float)half;  // exact, or rounded once to a subnormal number
     return who & 1 ? s : -s;
 }
 

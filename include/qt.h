@@ -526,7 +526,8 @@ qt_status qt_distill_topk_bwd(const void* logits, qt_dtype lt, int64_t T, int64_
  * A group x_j of a token and head (values past dim are 0) is held as s v_j:
  *   m = the value of largest magnitude (the first of equals), h = 8 or 128,
  *   s = -m / h, v_j = clamp(nearest integer to x_j / s, ties to even, -h, h - 1),
- *   0 where s = 0: bit-exact functions of the inputs, with x_j / s unrounded.
+ *   0 where s = 0: bit-exact functions of the inputs, with s rounded to f32 (exact
+ *   but below the normal numbers) and x_j / s unrounded.
  *   A group with a NaN or an infinity has the scale NaN and reads back as NaN.
  * Key codes: a token's groups one after the other, in the int4-g64 layout above
  * or as bytes v + 128.  Value codes: blocks of 8 tokens; in a block group after

@@ -1,6 +1,6 @@
 """The cache and its attention at the ends of their values' ranges: offsets of int4
 values taken out exactly, values near the largest and the smallest numbers under
-scores that rise."""
+scores that rise, groups below the normal numbers."""
 import math
 
 import pytest
@@ -142,3 +142,32 @@ def test_one_part_is_read_alone():
         qt.qt_kv_read(slots, k, v, d, parts="")
     with pytest.raises(ValueError, match="V must be"):
         qt.qt_kv_read(slots, k, v, d, K=mine, V=mine.float())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bits", [4, 8])
+def test_groups_below_the_normal_numbers(bits, dtype):
+    """Groups from the smallest subnormal number to 2^-95: codes and scales bit for
+    bit, and what is read back."""
+    g = gen(bits)
+    T, H, d = 55 * 16, 2, 128
+    power = torch.arange(-149, -94, device=DEV).repeat_interleave(16).double()
+    x = (2.0 * torch.rand((T, H, d), generator=g, device=DEV, dtype=torch.float64) - 1.0)
+    x[:, :, 1::5] *= 2.0 ** -3
+    x = (x * 2.0 ** (power[:, None, None] + torch.randint(0, 3, (T, H, 1), generator=g, device=DEV)))
+    x = x.float().to(DT[dtype])
+    slots = torch.randperm(T, generator=g, device=DEV).int()
+    k, v = qt.qt_kv_cache(T // 16, 16, H, d, bits, bits, device=DEV)
+    qt.qt_kv_write(x, x, slots, k, v)
+    c, s = su.quantize(x.cpu(), bits)
+    # a group of zeros has the scale of its first one, whose sign s = -m / h turns
+    zero = (x == 0).view(T, H, 2, 64).all(-1).cpu()
+    s = torch.where(zero, -x.float().cpu()[:, :, ::64], s)
+    assert (s != 0).any() and (s.abs() < 2.0 ** -126).any()
+    for part, octets in ((k, False), (v, True)):
+        gc, gs = su.fetch(part, octets, slots)
+        assert torch.equal(gs.cpu().view(torch.int32), s.view(torch.int32))
+        assert torch.equal(gc.cpu(), c)
+    ref = su.value(c, s, d).float()
+    for y in qt.qt_kv_read(slots, k, v, d, dtype=torch.float32):
+        assert torch.equal(y.cpu(), ref)
