@@ -36,8 +36,8 @@
 // (over a long flat softmax the offset costs more than f32's accuracy).
 //
 // Measured, this kernel alone: one sequence of 131072 positions, 8 heads of 128
-// with 8 queries each, 4 bits: 34 us (151 MB, 4.4 TB/s); 64 sequences of up to
-// 8192, 8 and 4 bits: 88-91 us (401 MB, 4.5 TB/s), where loads and conversions
+// with 8 queries each, 4 bits: 35.7 us (151 MB, 4.2 TB/s); 64 sequences of up to
+// 8192, 8 and 4 bits: 88-92 us (401 MB, 4.4 TB/s), where loads and conversions
 // alone take 64; about 9 us of a block are its start, first loads and end.
 #pragma once
 #include "lds_barrier.h"
@@ -313,7 +313,9 @@ attn_decode_kernel(const AttnKernelArgs x) {
     };
     // Wide heads leave no registers for the lane's part of every address: it is
     // worked out anew for a tile (a value that did not fit would be reloaded
-    // in the loop, behind all loads in flight).
+    // in the loop, behind all loads in flight).  Some forms of four groups of 8-bit keys
+    // spill all the same at two blocks a CU: up to 12 registers, 40 in bf16 calls
+    // of more than eight queries.
     auto here = [&]() __attribute__((always_inline)) {
         int v = lane;
         if constexpr (kWide) asm volatile("" : "+v"(v));

@@ -3,12 +3,13 @@
 //   1. h = act(Wgate_e x_t) * (Wup_e x_t) for every pair of a token and one of
 //      its k experts;
 //   2. out_t = sum_e w_te Wdown_e h_te.
-// The weights' stream is what both cannot do without; unpacking it (2.7 vector
-// instructions a code) bounds the first launch, the latency of a wave's few
-// chunks the second: of 128 experts of 7168 x 2048, int3, k = 8, one token takes
-// 36 + 22 us (2.9 and 2.3 TB/s).  Twelve tokens (68 experts live) took 280 + 174 us,
-// the full layer's launches 238 + 130 and 32 for the small ones: such streams
-// go there (few_long).  Codes enter the bf16 matrix cores exactly, each group's
+// The weights' stream is what both cannot do without.  Of 128 experts of 7168 x 2048,
+// int3, k = 8, one token takes 36 + 24 us (2.9 and 2.1 TB/s).  In the first launch
+// the stream (103 MB, 15 to 20 us) and its unpacking (2.7 vector instructions a code,
+// 17 us) come one after the other more than at once: a block is one tile there, and
+// its first weights are loaded after the routing.  The second waits for a
+// wave's few chunks.  Twelve tokens (68 experts live) take 419 us a call through the two
+// launches, 343 through the full layer's: such streams go there (few_long).  Codes enter the bf16 matrix cores exactly, each group's
 // products are summed in f32 and scaled by the group's f32 scale.  (Codes as they
 // lie, as FP4 operands next to inputs in FP8 pieces, save the unpacking; but the
 // products are not summed exactly there, f32 outputs came out 1.7e-5 off, and the
@@ -558,7 +559,8 @@ moe_few_up_kernel(const FewKernelArgs x) {
 // pairs, the addresses of both, come from LDS.
 //
 // An expert's rows are staged in LDS where it has one token (as many as leave two
-// blocks a CU); one with more tokens reads them from the caches.
+// blocks a CU); one with more tokens reads them from the caches.  At the 128
+// registers of two blocks a CU 19 to 26 go to scratch memory (36 to 64 bytes a lane).
 template <int DB, bool BF16>
 __global__ __launch_bounds__(64 * kDownWaves) __attribute__((amdgpu_waves_per_eu(4))) void
 moe_few_down_kernel(const FewKernelArgs x) {
